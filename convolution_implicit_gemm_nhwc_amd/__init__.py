@@ -11,6 +11,11 @@ provides device memory and streams) or raw device addresses given as ints.
 
     g = WgradPlan(N, H, W, C, K, R, S, stride=1, padding="SAME", dtype="bf16")
     dw = g(x, dy)          # filter gradient, HWIO
+
+The output layer (``include/fconv_mx.h``): 4-bit weights and activations.
+
+    w4 = MxQuantPlan(N, K, "bf16")(w)                       # MXFP4, laid out once
+    y = MxPlan(M, N, K, "bf16", ops=("bias", "relu"))(x, w4, bias=b)
 """
 from __future__ import annotations
 
@@ -18,7 +23,7 @@ import ctypes
 
 from . import _abi
 
-__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS"]
+__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS", "MxTensor", "MxQuantPlan", "MxPlan"]
 
 DTYPES = {"int8": _abi.FCONV_INT8, "bf16": _abi.FCONV_BF16, "fp32": _abi.FCONV_FP32}
 OPS = {"scale": _abi.OP_SCALE, "side": _abi.OP_SIDE, "bias": _abi.OP_BIAS,
@@ -296,3 +301,6 @@ class WgradPlan:
 def autotune_cache_clear():
     """Forget every autotuned configuration of this process."""
     _abi.lib().fconv_autotune_cache_clear()
+
+
+from .mx import MxPlan, MxQuantPlan, MxTensor  # noqa: E402

@@ -120,3 +120,52 @@ def lib():
 
 def lib_path() -> str:
     return _LIB_PATH
+
+
+# --- include/fconv_mx.h (bound on first use: a library built from the
+# convolution sources alone has none of these) -----------------------------
+
+FCONV_MX_MAX_K = 1 << 22
+
+# Every symbol include/fconv_mx.h declares.
+MX_EXPORTS = ("fconv_mx_bytes", "fconv_mx_quantize", "fconv_mx_dequantize", "fconv_mx_layout",
+              "fconv_mx_plan_create", "fconv_mx_plan_workspace_size", "fconv_mx_plan_run",
+              "fconv_mx_plan_kernel_name", "fconv_mx_plan_destroy")
+
+
+class MxDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "dtype", "n_ops")] + \
+               [("ops", ctypes.c_int32 * FCONV_MAX_OPS), ("flags", ctypes.c_uint32)]
+
+
+class MxArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_mx", ctypes.c_void_p),
+                ("w_mx", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("activ_alpha", ctypes.c_float),
+                ("activ_beta", ctypes.c_float)]
+
+
+_mx_lib = None
+
+
+def mx_lib():
+    """The loaded library with the symbols of include/fconv_mx.h declared."""
+    global _mx_lib
+    if _mx_lib is None:
+        L = lib()
+        P, i32, i64, st = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
+        L.fconv_mx_bytes.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+        L.fconv_mx_quantize.argtypes = [P, P, i64, i32, i32, i32, P]
+        L.fconv_mx_dequantize.argtypes = [P, P, i32, i32, i32, P, i64]
+        L.fconv_mx_layout.argtypes = [P, P, P, i32, i32, P]
+        L.fconv_mx_plan_create.argtypes = [ctypes.POINTER(MxDesc), ctypes.POINTER(P)]
+        L.fconv_mx_plan_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        L.fconv_mx_plan_run.argtypes = [P, P, ctypes.POINTER(MxArgs)]
+        L.fconv_mx_plan_destroy.argtypes = [P]
+        for name in MX_EXPORTS:
+            getattr(L, name).restype = st
+        L.fconv_mx_plan_kernel_name.argtypes = [P]
+        L.fconv_mx_plan_kernel_name.restype = ctypes.c_char_p
+        _mx_lib = L
+    return _mx_lib

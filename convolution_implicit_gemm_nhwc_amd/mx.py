@@ -1,0 +1,160 @@
+"""MXFP4 (microscaled 4-bit floating point): binding of include/fconv_mx.h.
+
+    q = MxQuantPlan(rows, cols, "bf16")
+    t = q(x)                   # MxTensor: e2m1 codes, one e8m0 scale per 32
+    x4 = q.dequantize(t)       # the values that t stands for
+
+    w4 = MxTensor.from_codes(codes, scales, K)     # a 4-bit checkpoint
+    y = MxPlan(M, N, K, "bf16", ops=("bias", "relu"))(x, w4, bias=b)
+
+A quantised matrix is kept in the order in which the matrix cores read it
+(the header says which); it is laid out once, when it is made.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _abi
+from . import _check, DTYPES, OPS
+from ._dense import TORCH, Launch, matrix, vector
+
+__all__ = ["MxTensor", "MxQuantPlan", "MxPlan"]
+
+
+def _mx_bytes(rows, cols):
+    n = ctypes.c_size_t()
+    _check(_abi.mx_lib().fconv_mx_bytes(rows, cols, ctypes.byref(n)), "fconv_mx_bytes")
+    return n.value
+
+
+class MxTensor:
+    """A quantised [rows, cols] matrix: one uint8 GPU buffer `data` of
+    fconv_mx_bytes(rows, cols) bytes, codes and then scales."""
+
+    __slots__ = ("data", "rows", "cols")
+
+    def __init__(self, data, rows, cols):
+        self.data, self.rows, self.cols = data, rows, cols
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < _mx_bytes(rows, cols):
+            raise ValueError("data: %d bytes needed (uint8, contiguous), got %s of %s"
+                             % (_mx_bytes(rows, cols), tuple(data.shape), data.dtype))
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.data.device
+
+    @classmethod
+    def from_codes(cls, codes, scales, cols, stream=None):
+        """From row-major codes [rows, ceil(cols/32)*16] (uint8, two e2m1
+        codes to a byte, low half first) and e8m0 scales [rows,
+        ceil(cols/32)] (uint8)."""
+        rows, nb = codes.shape[0], -(-cols // 32)
+        nbytes = _mx_bytes(rows, cols)
+        pc = vector(codes, "codes", rows * nb * 16, torch.uint8)
+        ps = vector(scales, "scales", rows * nb, torch.uint8)
+        with Launch(codes.device, stream, (codes, scales)) as s:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+            _check(_abi.mx_lib().fconv_mx_layout(s, pc, ps, rows, cols, data.data_ptr()),
+                   "fconv_mx_layout")
+        return cls(data, rows, cols)
+
+
+class MxQuantPlan:
+    """Quantises [rows, cols] matrices of dtype "bf16" or "fp32", and back."""
+
+    def __init__(self, rows, cols, dtype="bf16"):
+        self.rows, self.cols, self.dtype = rows, cols, dtype
+        if dtype not in TORCH:
+            raise ValueError("dtype %r: bf16 or fp32" % (dtype,))
+        self._code, self._torch = DTYPES[dtype], TORCH[dtype]
+        self.bytes = _mx_bytes(rows, cols)
+
+    def __call__(self, x, stream=None):
+        ptr, ld = matrix(x, "x", self.rows, self.cols, self._torch)
+        with Launch(x.device, stream, (x,)) as s:
+            data = torch.empty(self.bytes, dtype=torch.uint8, device=x.device)
+            _check(_abi.mx_lib().fconv_mx_quantize(s, ptr, ld, self.rows, self.cols, self._code,
+                                                   data.data_ptr()), "fconv_mx_quantize")
+        return MxTensor(data, self.rows, self.cols)
+
+    def dequantize(self, t, stream=None):
+        """The values of an MxTensor of this plan's size, in the plan's dtype."""
+        if t.shape != (self.rows, self.cols):
+            raise ValueError("MxTensor of %s, the plan needs %s" % (t.shape, (self.rows, self.cols)))
+        with Launch(t.device, stream, (t.data,)) as s:
+            y = torch.empty(self.rows, self.cols, dtype=self._torch, device=t.device)
+            _check(_abi.mx_lib().fconv_mx_dequantize(s, t.data.data_ptr(), self.rows, self.cols,
+                                                     self._code, y.data_ptr(), self.cols),
+                   "fconv_mx_dequantize")
+        return y
+
+
+class MxPlan:
+    """y[m, n] = act(sum_k X[m, k] W[n, k] + bias[n]) with X and W in MXFP4.
+    A dense layer, or a 1x1 convolution over M = N*H*W pixels.  dtype is the
+    type of x and y; ops: [bias], [relu | leaky_relu | clipped_relu | clamp]."""
+
+    def __init__(self, M, N, K, dtype="bf16", ops=("bias",)):
+        d = _abi.MxDesc()
+        d.M, d.N, d.K = M, N, K
+        d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
+        codes = [OPS[o] if isinstance(o, str) else int(o) for o in ops]
+        if len(codes) > _abi.FCONV_MAX_OPS:
+            raise ValueError("too many ops")
+        d.n_ops = len(codes)
+        for i, c in enumerate(codes):
+            d.ops[i] = c
+        self.desc = d
+        self.M, self.N, self.K, self.dtype = M, N, K, dtype
+        self._bias = _abi.OP_BIAS in codes
+        self._h = ctypes.c_void_p()
+        L = _abi.mx_lib()
+        _check(L.fconv_mx_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_mx_plan_create")
+        self._torch = TORCH[dtype]
+        n = ctypes.c_size_t()
+        _check(L.fconv_mx_plan_workspace_size(self._h, ctypes.byref(n)), "fconv_mx_plan_workspace_size")
+        self.workspace_bytes = n.value
+        self.kernel_name = L.fconv_mx_plan_kernel_name(self._h).decode()
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            _abi.mx_lib().fconv_mx_plan_destroy(h)
+            self._h = ctypes.c_void_p()
+
+    def __call__(self, x, w, bias=None, out=None, activ_alpha=0.0, activ_beta=0.0, stream=None):
+        """x: a GPU tensor [M, K] (its rows may be apart) or an MxTensor; w: an
+        MxTensor [N, K]; bias fp32 [N] with the bias op.  Returns y [M, N] (in
+        `out`, whose rows may be apart, if given)."""
+        a = _abi.MxArgs()
+        if isinstance(x, MxTensor):
+            if x.shape != (self.M, self.K):
+                raise ValueError("x: MxTensor of %s, the plan needs %s" % (x.shape, (self.M, self.K)))
+            xt = x.data
+            a.x_mx = xt.data_ptr()
+        else:
+            xt = x
+            a.x, a.ldx = matrix(x, "x", self.M, self.K, self._torch)
+        if not isinstance(w, MxTensor) or w.shape != (self.N, self.K):
+            raise ValueError("w: an MxTensor of %s needed" % ((self.N, self.K),))
+        if self._bias != (bias is not None):
+            raise ValueError("bias: the plan has %s bias op" % ("a" if self._bias else "no"))
+        a.w_mx = w.data.data_ptr()
+        if bias is not None:
+            a.bias = vector(bias, "bias", self.N, torch.float32)
+        a.activ_alpha, a.activ_beta = activ_alpha, activ_beta
+        with Launch(xt.device, stream, (xt, w.data, bias, out)) as s:
+            if out is None:
+                out = torch.empty(self.M, self.N, dtype=self._torch, device=xt.device)
+            a.y, a.ldy = matrix(out, "out", self.M, self.N, self._torch)
+            if self.workspace_bytes:
+                ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=xt.device)
+                a.workspace, a.workspace_bytes = ws.data_ptr(), self.workspace_bytes
+            _check(_abi.mx_lib().fconv_mx_plan_run(self._h, s, ctypes.byref(a)), "fconv_mx_plan_run")
+        return out
