@@ -12,7 +12,12 @@ provides device memory and streams) or raw device addresses given as ints.
     g = WgradPlan(N, H, W, C, K, R, S, stride=1, padding="SAME", dtype="bf16")
     dw = g(x, dy)          # filter gradient, HWIO
 
-The output layer (``include/fconv_mx.h``): 4-bit weights and activations.
+The output layer (``include/fconv_xent.h``, ``include/fconv_mx.h``): its training
+loss without the logits, and 4-bit weights and activations.
+
+    c = XentPlan(T, D, V, "bf16")
+    loss, lse = c.forward(h, w, target)
+    dh, dw = c.backward(h, w, target, lse, dloss)
 
     w4 = MxQuantPlan(N, K, "bf16")(w)                       # MXFP4, laid out once
     y = MxPlan(M, N, K, "bf16", ops=("bias", "relu"))(x, w4, bias=b)
@@ -23,7 +28,8 @@ import ctypes
 
 from . import _abi
 
-__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS", "MxTensor", "MxQuantPlan", "MxPlan"]
+__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS", "MxTensor", "MxQuantPlan", "MxPlan",
+           "XentPlan"]
 
 DTYPES = {"int8": _abi.FCONV_INT8, "bf16": _abi.FCONV_BF16, "fp32": _abi.FCONV_FP32}
 OPS = {"scale": _abi.OP_SCALE, "side": _abi.OP_SIDE, "bias": _abi.OP_BIAS,
@@ -304,3 +310,4 @@ def autotune_cache_clear():
 
 
 from .mx import MxPlan, MxQuantPlan, MxTensor  # noqa: E402
+from .xent import XentPlan  # noqa: E402

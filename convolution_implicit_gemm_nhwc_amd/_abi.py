@@ -169,3 +169,48 @@ def mx_lib():
         L.fconv_mx_plan_kernel_name.restype = ctypes.c_char_p
         _mx_lib = L
     return _mx_lib
+
+
+# --- include/fconv_xent.h (bound on first use, as above) --------------------
+
+FCONV_XENT_MAX_LD = 1 << 21
+
+# Every symbol include/fconv_xent.h declares.
+XENT_EXPORTS = ("fconv_xent_plan_create", "fconv_xent_plan_forward_workspace_size",
+                "fconv_xent_plan_backward_workspace_size", "fconv_xent_plan_forward",
+                "fconv_xent_plan_backward", "fconv_xent_plan_destroy")
+
+
+class XentDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "V", "dtype")] + \
+               [("ignore_index", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
+class XentArgs(ctypes.Structure):
+    _fields_ = [("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("target", ctypes.c_void_p), ("loss", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dloss", ctypes.c_void_p), ("dh", ctypes.c_void_p),
+                ("lddh", ctypes.c_int64), ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_xent_lib = None
+
+
+def xent_lib():
+    """The loaded library with the symbols of include/fconv_xent.h declared."""
+    global _xent_lib
+    if _xent_lib is None:
+        L = lib()
+        P, st = ctypes.c_void_p, ctypes.c_int
+        size = ctypes.POINTER(ctypes.c_size_t)
+        L.fconv_xent_plan_create.argtypes = [ctypes.POINTER(XentDesc), ctypes.POINTER(P)]
+        L.fconv_xent_plan_forward_workspace_size.argtypes = [P, size]
+        L.fconv_xent_plan_backward_workspace_size.argtypes = [P, size]
+        L.fconv_xent_plan_forward.argtypes = [P, P, ctypes.POINTER(XentArgs)]
+        L.fconv_xent_plan_backward.argtypes = [P, P, ctypes.POINTER(XentArgs)]
+        L.fconv_xent_plan_destroy.argtypes = [P]
+        for name in XENT_EXPORTS:
+            getattr(L, name).restype = st
+        _xent_lib = L
+    return _xent_lib

@@ -1,0 +1,98 @@
+"""Softmax cross entropy of a linear output layer and its gradient, without
+keeping the logits: binding of include/fconv_xent.h.
+
+    c = XentPlan(T, D, V, "bf16", ignore_index=-100)
+    loss, lse = c.forward(h, w, target)              # fp32 [T] each
+    dh, dw = c.backward(h, w, target, lse, dloss)    # dloss fp32 [T]
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _abi
+from . import _check, DTYPES
+from ._dense import TORCH, Launch, matrix, vector
+
+__all__ = ["XentPlan"]
+
+
+class XentPlan:
+    """loss[t] = logsumexp_v(z[t, v]) - z[t, target[t]] with z = h w^T, h [T, D],
+    w [V, D] of dtype "bf16" or "fp32", target int64 [T].  Tokens whose target is
+    ignore_index have loss 0 and no gradient; a target outside [0, V) gives NaN."""
+
+    def __init__(self, T, D, V, dtype="bf16", ignore_index=-100):
+        d = _abi.XentDesc()
+        d.T, d.D, d.V = T, D, V
+        d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
+        d.ignore_index = ignore_index
+        self.desc = d
+        self.T, self.D, self.V, self.dtype, self.ignore_index = T, D, V, dtype, ignore_index
+        self._h = ctypes.c_void_p()
+        L = _abi.xent_lib()
+        _check(L.fconv_xent_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_xent_plan_create")
+        self._torch = TORCH[dtype]
+        n = ctypes.c_size_t()
+        _check(L.fconv_xent_plan_forward_workspace_size(self._h, ctypes.byref(n)),
+               "fconv_xent_plan_forward_workspace_size")
+        self.forward_workspace_bytes = n.value
+        _check(L.fconv_xent_plan_backward_workspace_size(self._h, ctypes.byref(n)),
+               "fconv_xent_plan_backward_workspace_size")
+        self.backward_workspace_bytes = n.value
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            _abi.xent_lib().fconv_xent_plan_destroy(h)
+            self._h = ctypes.c_void_p()
+
+    def _inputs(self, h, w, target):
+        a = _abi.XentArgs()
+        a.h, a.ldh = matrix(h, "h", self.T, self.D, self._torch)
+        a.w, a.ldw = matrix(w, "w", self.V, self.D, self._torch)
+        a.target = vector(target, "target", self.T, torch.int64)
+        return a
+
+    def forward(self, h, w, target, stream=None):
+        """(loss, lse), fp32 [T].  h and w may have rows apart."""
+        a = self._inputs(h, w, target)
+        with Launch(h.device, stream, (h, w, target)) as s:
+            out = torch.empty(2, self.T, dtype=torch.float32, device=h.device)
+            loss, lse = out[0], out[1]
+            ws = torch.empty(max(self.forward_workspace_bytes, 16), dtype=torch.uint8, device=h.device)
+            a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
+            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+            _check(_abi.xent_lib().fconv_xent_plan_forward(self._h, s, ctypes.byref(a)),
+                   "fconv_xent_plan_forward")
+        return loss, lse
+
+    def backward(self, h, w, target, lse, dloss, dh=None, dw=None, need_dh=True, need_dw=True,
+                 stream=None):
+        """(dh [T, D], dw [V, D]) from the forward pass's lse and the gradient
+        dloss [T] of the loss; in `dh` and `dw` (whose rows may be apart) if
+        given, None where not needed."""
+        if not (need_dh or need_dw):
+            raise ValueError("backward: no gradient needed")
+        if (dh is not None and not need_dh) or (dw is not None and not need_dw):
+            raise ValueError("backward: an output given for a gradient that is not needed")
+        a = self._inputs(h, w, target)
+        a.lse = vector(lse, "lse", self.T, torch.float32)
+        a.dloss = vector(dloss, "dloss", self.T, torch.float32)
+        with Launch(h.device, stream, (h, w, target, lse, dloss, dh, dw)) as s:
+            if need_dh:
+                if dh is None:
+                    dh = torch.empty(self.T, self.D, dtype=self._torch, device=h.device)
+                a.dh, a.lddh = matrix(dh, "dh", self.T, self.D, self._torch)
+            if need_dw:
+                if dw is None:
+                    dw = torch.empty(self.V, self.D, dtype=self._torch, device=h.device)
+                a.dw, a.lddw = matrix(dw, "dw", self.V, self.D, self._torch)
+            ws = torch.empty(max(self.backward_workspace_bytes, 16), dtype=torch.uint8, device=h.device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+            # Of no tokens dh has no address, and dw is all there is to write.
+            if a.dh or a.dw:
+                _check(_abi.xent_lib().fconv_xent_plan_backward(self._h, s, ctypes.byref(a)),
+                       "fconv_xent_plan_backward")
+        return dh, dw
