@@ -60,7 +60,8 @@ enum Order { kSum, kRow };
 
 struct Operand {
   const char* p;
-  int64_t ld;  // elements
+  int64_t ld;     // elements
+  int64_t width;  // kRow: readable elements of a row
 };
 
 enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart };
@@ -71,7 +72,7 @@ struct GemmArgs {
   // Number of live tokens (device), replacing nb (kSum order of b) or nk
   // (kRow order of b); NULL if there is none.
   const int32_t* n_live;
-  int32_t k_split;  // length of one range of k, blockIdx.z ranges
+  int32_t ranges;   // of k; the partial sums of each go out apart
   // kEpiLse: partial (max, sum) at [tile of a][ld_out + b]; kEpiGrad: g;
   // kEpiOut: C; kEpiPart: fp32 C of this range at range * nb_max * ld_out.
   char* out;
@@ -137,6 +138,83 @@ __device__ inline void join(float& m, float& s, float m2, float s2) {
 __device__ inline float grad_of(float z, float lse, bool hit) {
   const float p = exp_of(z - lse);
   return hit ? p - 1.0f : p;
+}
+
+// What a workgroup does with its tile of C: NI x NJ matrix tiles per wave, of
+// which this lane holds a = a_of(i) .. + 3 of b = b_of(j); ra x rb of the tile
+// exist.  Two waves (wa) share the tile's b; TB of them in all.
+template <typename E, Epilogue EPI, int NI, int NJ, int TB, typename FA, typename FB>
+__device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t a0, int64_t b0, int ra, int rb,
+                                int tile_a, int range, int wa, int q, FA a_of, FB b_of, float2* red) {
+  constexpr int ES = sizeof(E);
+  if constexpr (EPI == kEpiLse) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int b = b_of(j);
+      // The target's place in this tile, if it is here.
+      const int64_t tgt = (b < rb ? g.target[b0 + b] : -1) - a0;
+      const int at = tgt >= 0 && tgt < ra ? static_cast<int>(tgt) : -1;
+      float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (a_of(i) + e >= ra) acc[i][j][e] = -__builtin_inff();
+          m = fmaxf(m, acc[i][j][e]);
+          if (a_of(i) + e == at) g.target_logit[b0 + b] = acc[i][j][e];
+        }
+      const float base = base_of(m);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += exp_of(acc[i][j][e] - base);
+#pragma unroll
+      for (int x = 16; x < 64; x *= 2) {
+        const float m2 = __shfl_xor(m, x), s2 = __shfl_xor(s, x);
+        join(m, s, m2, s2);
+      }
+      if (q == 0) red[wa * TB + b] = make_float2(m, s);
+    }
+    __syncthreads();
+    if (threadIdx.x < static_cast<unsigned>(rb)) {
+      const float2 p0 = red[threadIdx.x], p1 = red[TB + threadIdx.x];
+      float m = p0.x, s = p0.y;
+      join(m, s, p1.x, p1.y);
+      reinterpret_cast<float2*>(g.out)[tile_a * g.ld_out + b0 + threadIdx.x] = make_float2(m, s);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int b = b_of(j);
+      if (b >= rb) continue;
+      if constexpr (EPI == kEpiGrad) {
+        const int tgt = g.live_target[b0 + b];
+        const float lse = tgt < 0 ? __builtin_nanf("") : g.lse[b0 + b];
+        const int at = static_cast<int>(tgt - g.v0 - a0);
+        char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int a = a_of(i);
+          if (a0 + a >= g.na_pad) continue;
+          f32x4 t;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = a + e < ra ? grad_of(acc[i][j][e], lse, at == a + e) : 0.0f;
+          store4<E>(row + a * ES, t, 4);
+        }
+      } else {
+        const int64_t row = EPI == kEpiOut && g.row_map ? g.row_map[b0 + b] : b0 + b;
+        const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
+        constexpr int OS = EPI == kEpiOut ? ES : 4;
+        char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) * OS;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int n = ra - a_of(i);
+          if (n <= 0) continue;
+          store4<std::conditional_t<EPI == kEpiOut, E, float>>(out + a_of(i) * OS, acc[i][j] * scale, n);
+        }
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------ general kernel
@@ -214,14 +292,16 @@ __global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
   using G = Gen<E>;
   using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
   __shared__ __attribute__((aligned(16))) char buf[2][2][G::BUF];
+  __shared__ float2 red[EPI == kEpiLse ? 2 * 64 : 1];
   const int live = g.n_live ? *g.n_live : 0;
   const int nb = g.n_live && OB == kSum ? live : g.nb;
   const int nk = g.n_live && OB == kRow ? live : g.nk;
   const int64_t a0 = static_cast<int64_t>(blockIdx.x) * 64, b0 = static_cast<int64_t>(blockIdx.y) * 64;
   if (b0 >= nb) return;
   const int ra = static_cast<int>(min<int64_t>(g.na - a0, 64)), rb = static_cast<int>(min<int64_t>(nb - b0, 64));
-  const int64_t k0 = static_cast<int64_t>(blockIdx.z) * g.k_split;
-  const int64_t k1 = min<int64_t>(nk, k0 + g.k_split);
+  const int64_t per = round_up(ceil_div(nk, g.ranges), G::SLAB);
+  const int64_t k0 = blockIdx.z * per;
+  const int64_t k1 = min<int64_t>(nk, k0 + per);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave & 1, wb = wave >> 1, r = lane & 15, q = lane >> 4;
 
@@ -257,75 +337,280 @@ __global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
     }
   }
 
-  if constexpr (EPI == kEpiLse) {
-    __shared__ float2 red[2][64];
+  epilogue<E, EPI, 2, 2, 64>(
+      g, acc, a0, b0, ra, rb, blockIdx.x, blockIdx.z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; },
+      [&](int j) { return wb * 32 + 16 * j + r; }, red);
+}
+
+// -------------------------------------------------------------- tiled kernel
+//
+// bf16, rows and their length multiples of 16 bytes.  A workgroup owns a
+// (2 H) x (2 H) tile of C in four quadrants; NW waves share each quadrant, two
+// along a, NW / 2 along b.  A slab is 64 k of both operands: four half tiles,
+// copied buffer->LDS, in one of two sets of buffers.  A slab takes four
+// phases, one quadrant each:
+//   phase   reads (LDS)    copies for the slab after next    products
+//   0       A0, B0         -                                 C00
+//   1       B1             A0, B0 (their readers are done)   C01
+//   2       A1             B1                                C11
+//   3       -              A1                                C10
+// A phase is two steps between barriers: a wave reads fragments and starts
+// copies in one, multiplies in the other.  With eight waves the four of a = 1
+// run one step behind the others, so that on every SIMD one wave multiplies
+// while the other reads, and the matrix core never waits for LDS.  A copy has
+// at least one slab's time (2048 cycles) to arrive; the wait for a whole slab
+// stands in phase 3, with the eight copies of the slab after it in flight.
+//
+// LDS order.  kSum: rows of 64 k (128 bytes), the 16-byte piece c of row r at
+// c ^ (r % 8): eight consecutive lanes of a fragment read hit eight places.
+// kRow: rows k of H elements; fragments come from the transposed read
+// (ds_read_b64_tr_b16: lane i's element e of a 16-lane group is element i % 4
+// of the 8 bytes addressed by the group's lane 4 e + i / 4), pieces swizzled
+// by swz(k) so that the rows that one read touches lie on different banks.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16* lds_v4i16_t;
+
+constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset past every extent: reads 0
+constexpr int kBufferDword3 = 0x00020000;      // raw buffer descriptor, gfx9 family
+
+__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const uint32_t n = bytes > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(bytes < 0 ? 0 : bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(n), kBufferDword3);
+}
+
+template <int H>
+__device__ inline int row_swz(int k) {
+  return H == 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : (((k & 3) << 1) ^ (((k >> 3) & 1) << 1)) & 7;
+}
+
+// One operand of a workgroup: where its half tiles come from, and this lane's
+// places in them.
+template <Order O, int H, int NW>
+struct Feed {
+  const char* base;  // of the tile's first element of the next slab to copy
+  int64_t left;      // bytes readable from base
+  int64_t step;      // bytes from slab to slab
+  int krem;          // k left from base (kSum)
+  uint32_t off[2][2];  // per half and copy of this wave
+  int chunk;           // kSum: first k of this lane's piece
+
+  // rows x k: the tile at (row0, k0), `rows` of its rows and nk of the sum exist.
+  __device__ void init(const Operand& op, int64_t row0, int64_t rows, int64_t k0, int64_t k1, int wave, int lane) {
+    if constexpr (O == kSum) {
+      base = op.p + (row0 * op.ld + k0) * 2;
+      // The last row ends with k1, rounded up to whole pieces (their rest is zeros or masked).
+      left = ((rows - 1) * op.ld + ((k1 - k0 + 7) & ~7)) * 2;
+      step = 128;
+      krem = static_cast<int>(k1 - k0);
+      chunk = ((lane & 7) ^ (lane >> 3)) * 8;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = wb * 32 + 16 * j + r;
-      const int64_t tgt = b < rb ? g.target[b0 + b] : -1;
-      float m = -__builtin_inff(), s = 0.0f;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < 2; ++c)
+          off[h][c] = static_cast<uint32_t>(((h * H + (wave * 2 + c) * 8 + (lane >> 3)) * op.ld + chunk) * 2);
+    } else {
+      base = op.p + (k0 * op.ld + row0) * 2;
+      left = ((k1 - k0 - 1) * op.ld + ((rows + 7) & ~7)) * 2;
+      step = op.ld * 128;
+      krem = 0;
+      chunk = 0;
+      constexpr int PPR = H / 8, RPC = 64 / PPR;  // pieces of a row, rows of a copy
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = wa * 32 + 16 * i + 4 * q + e;
-          if (a < ra) m = fmaxf(m, acc[i][j][e]);
-          if (a < ra && b < rb && tgt == a0 + a) g.target_logit[b0 + b] = acc[i][j][e];
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int k = (wave * 2 + c) * RPC + lane / PPR;
+          off[h][c] = static_cast<uint32_t>((k * op.ld + h * H + ((lane % PPR) ^ row_swz<H>(k)) * 8) * 2);
         }
-      const float base = base_of(m);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (wa * 32 + 16 * i + 4 * q + e < ra) s += exp_of(acc[i][j][e] - base);
-#pragma unroll
-      for (int x = 16; x < 64; x *= 2) {
-        const float m2 = __shfl_xor(m, x), s2 = __shfl_xor(s, x);
-        join(m, s, m2, s2);
-      }
-      if (q == 0) red[wa][b] = make_float2(m, s);
-    }
-    __syncthreads();
-    if (threadIdx.x < static_cast<unsigned>(rb)) {
-      const float2 p0 = red[0][threadIdx.x], p1 = red[1][threadIdx.x];
-      float m = p0.x, s = p0.y;
-      join(m, s, p1.x, p1.y);
-      reinterpret_cast<float2*>(g.out)[blockIdx.x * g.ld_out + b0 + threadIdx.x] = make_float2(m, s);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = wb * 32 + 16 * j + r;
-      if (b >= rb) continue;
-      if constexpr (EPI == kEpiGrad) {
-        const int tgt = g.live_target[b0 + b];
-        const float lse = tgt < 0 ? __builtin_nanf("") : g.lse[b0 + b];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t a = a0 + wa * 32 + 16 * i + 4 * q;
-          if (a >= g.na_pad) continue;
-          f32x4 t;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            t[e] = a + e < g.na ? grad_of(acc[i][j][e], lse, tgt == g.v0 + a + e) : 0.0f;
-          store4<E>(g.out + ((b0 + b) * g.ld_out + a) * G::ES, t, 4);
-        }
-      } else {
-        const int64_t row = EPI == kEpiOut && g.row_map ? g.row_map[b0 + b] : b0 + b;
-        const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t a = a0 + wa * 32 + 16 * i + 4 * q;
-          const int n = static_cast<int>(g.na - a);
-          if (n <= 0) continue;
-          if constexpr (EPI == kEpiOut)
-            store4<E>(g.out + (row * g.ld_out + a) * G::ES, acc[i][j] * scale, n);
-          else
-            store4<float>(g.out + (blockIdx.z * g.part_stride + row * g.ld_out + a) * 4, acc[i][j], n);
-        }
-      }
     }
   }
+  // Copies half h of the next slab into buf (this wave's 2 KiB of it).
+  __device__ void copy(int h, char* buf, int wave) const {
+    const auto rsrc = make_rsrc(base, left);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t o = off[h][c];
+      if (O == kSum && chunk >= krem) o = kOutOfRange;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(buf + (wave * 2 + c) * 1024), 16, o, 0, 0, 0);
+    }
+  }
+  __device__ void next() {
+    base += step;
+    left -= step;
+    krem -= 64;
+  }
+};
+
+// Fragments of this wave in a half tile: N matrix tiles of 16 rows from row
+// w * 16 N on, two steps of 32 k.
+template <Order O, int H, int N>
+struct Frags {
+  int at[O == kSum ? 2 : N];
+  bf16x8 f[N][2];
+
+  __device__ void init(int w, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    if constexpr (O == kSum) {
+      at[0] = (w * 16 * N + r) * 128 + ((q ^ (r & 7)) << 4);
+      at[1] = (w * 16 * N + r) * 128 + (((q + 4) ^ (r & 7)) << 4);
+    } else {
+      const int k = 8 * q + (r >> 2);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        at[i] = k * 2 * H + (((2 * (w * N + i) + ((r & 3) >> 1)) ^ row_swz<H>(k)) << 4) + (r & 1) * 8;
+    }
+  }
+  __device__ void read(const char* buf) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (O == kSum) {
+          f[i][kk] = *reinterpret_cast<const bf16x8*>(buf + at[kk] + i * 2048);
+        } else {
+          const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H));
+          const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H + 8 * H));
+          f[i][kk] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+      }
+  }
+};
+
+template <Order OA, Order OB, Epilogue EPI, int H, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
+  constexpr int MI = H / 32, MJ = 2 * H / (16 * NW);  // matrix tiles of a wave in a quadrant
+  constexpr int HB = H * 128;                         // bytes of a half tile
+  static_assert(HB == NW * 2048, "two copies per wave and half tile");
+  // Arrays of their own, so that the compiler sees which copies a read does not
+  // meet; few enough for it to follow them all (A0 and B0 go together).
+  __shared__ __attribute__((aligned(1024))) char ab0[2 * HB], b01[HB], a01[HB];
+  __shared__ __attribute__((aligned(1024))) char ab1[2 * HB], b11[HB], a11[HB];
+  __shared__ float2 red[EPI == kEpiLse ? 4 * H : 1];
+
+  const int live = g.n_live ? *g.n_live : 0;
+  const int nb = g.n_live && OB == kSum ? live : g.nb;
+  const int nk = g.n_live && OB == kRow ? live : g.nk;
+  // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
+  // tiles: eight rows of them together, so both operands stay in its L2; the
+  // ranges of a sum come one after the other.
+  const int tiles_a = (g.na + 2 * H - 1) / (2 * H), tiles_b = (nb + 2 * H - 1) / (2 * H);
+  const int tiles = tiles_a * tiles_b;
+  const int total = tiles * g.ranges, share = (total + 7) / 8;
+  const int slot = blockIdx.x / 8;
+  const int id = (blockIdx.x % 8) * share + slot;
+  if (slot >= share || id >= total) return;
+  const int range = id / tiles, tile = id % tiles;
+  const int first = tile / (8 * tiles_a) * 8, rows8 = min(8, tiles_b - first), in = tile % (8 * tiles_a);
+  const int tb = first + in % rows8, ta = in / rows8;
+  const int64_t a0 = static_cast<int64_t>(ta) * 2 * H, b0 = static_cast<int64_t>(tb) * 2 * H;
+  const int ra = static_cast<int>(min<int64_t>(g.na - a0, 2 * H)), rb = static_cast<int>(min<int64_t>(nb - b0, 2 * H));
+  // Ranges of whole slabs.
+  const int all = (nk + 63) / 64, per = (all + g.ranges - 1) / g.ranges;
+  const int64_t k0 = static_cast<int64_t>(range) * per * 64;
+  const int slabs = max(0, min(per, all - range * per));
+  const int64_t k1 = min<int64_t>(nk, k0 + static_cast<int64_t>(slabs) * 64);
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wa = wave / (NW / 2), wb = wave % (NW / 2), r = lane & 15, q = lane >> 4;
+
+  f32x4 acc[2 * MI][2 * MJ];
+#pragma unroll
+  for (int i = 0; i < 2 * MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2 * MJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (slabs > 0) {
+    Feed<OA, H, NW> fa;
+    Feed<OB, H, NW> fb;
+    fa.init(g.a, a0, OA == kRow ? g.a.width - a0 : ra, k0, k1, wave, lane);
+    fb.init(g.b, b0, OB == kRow ? g.b.width - b0 : rb, k0, k1, wave, lane);
+    Frags<OA, H, MI> xa;
+    Frags<OB, H, MJ> xb[2];
+    xa.init(wa, lane);
+    xb[0].init(wb, lane);
+    xb[1].init(wb, lane);
+
+    // Past the last slab the copies bring zeros that nobody reads.
+    auto advance = [&]() __attribute__((always_inline)) {
+      fa.next();
+      fb.next();
+    };
+    auto read_step_ends = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](int i2, int j2, Frags<OB, H, MJ>& b) __attribute__((always_inline)) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < MJ; ++j)
+            acc[i2 * MI + i][j2 * MJ + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                xa.f[i][kk], b.f[j][kk], acc[i2 * MI + i][j2 * MJ + j], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto slab = [&](char* ab, char* b1b, char* a1b) __attribute__((always_inline)) {
+      xb[0].read(ab + HB);
+      xa.read(ab);
+      read_step_ends();
+      multiply(0, 0, xb[0]);
+
+      xb[1].read(b1b);
+      fa.copy(0, ab, wave);
+      fb.copy(0, ab + HB, wave);
+      read_step_ends();
+      multiply(0, 1, xb[1]);
+
+      xa.read(a1b);
+      fb.copy(1, b1b, wave);
+      read_step_ends();
+      multiply(1, 1, xb[1]);
+
+      fa.copy(1, a1b, wave);
+      advance();
+      // All but the eight copies of this slab's successor but one: the next slab is here.
+      __builtin_amdgcn_s_waitcnt(0x0F78);
+      read_step_ends();
+      multiply(1, 0, xb[0]);
+    };
+
+    fa.copy(0, ab0, wave);
+    fb.copy(0, ab0 + HB, wave);
+    fb.copy(1, b01, wave);
+    fa.copy(1, a01, wave);
+    advance();
+    fa.copy(0, ab1, wave);
+    fb.copy(0, ab1 + HB, wave);
+    fb.copy(1, b11, wave);
+    fa.copy(1, a11, wave);
+    advance();
+    __builtin_amdgcn_s_waitcnt(0x0F78);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
+    for (int s = 0; s + 1 < slabs; s += 2) {
+      slab(ab0, b01, a01);
+      slab(ab1, b11, a11);
+    }
+    if (slabs & 1) slab(ab0, b01, a01);
+    if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab land before the LDS is given back
+  }
+
+  epilogue<__bf16, EPI, 2 * MI, 2 * MJ, 2 * H>(
+      g, acc, a0, b0, ra, rb, ta, range, wa, q,
+      [&](int i) { return i / MI * H + (wa * MI + i % MI) * 16 + 4 * q; },
+      [&](int j) { return j / MJ * H + (wb * MJ + j % MJ) * 16 + r; }, red);
 }
 
 // ------------------------------------------------------------ small kernels
@@ -519,18 +804,26 @@ __global__ __launch_bounds__(256) void xent_zero_kernel(char* out, int64_t ld, i
 }  // namespace
 }  // namespace fconv
 
+namespace fconv {
+namespace {
+// How a product is divided: the edge of its tiles (64: general kernel) and
+// the ranges of its sum.
+struct Split {
+  int32_t edge, ranges;
+};
+}  // namespace
+}  // namespace fconv
+
 struct fconv_xent_plan_s {
   fconv_xent_desc d;
   int32_t es;
-  // Forward workspace: partial (max, sum) [a_tiles][T], target logits [T].
-  int64_t a_tiles;
+  // Forward workspace: partial (max, sum) [tiles of V, at most][T], target logits [T].
   size_t fwd_target, fwd_bytes;
+  fconv::Split logits, grad, dh, dw;  // dh and dw: of one piece
   // Backward workspace.
   int64_t ld_live;               // row stride of the gathered h
   int32_t piece, pieces;         // vocabulary columns of a piece
   int64_t ld_g;
-  int32_t dh_ranges, dh_split;   // ranges of a piece's k, and their length
-  int32_t dw_ranges, dw_split;
   size_t o_g, o_h, o_index, o_target, o_lse, o_dloss, o_n, o_c, o_blocks, o_rh, o_dh, o_dw, bwd_bytes;
 };
 
@@ -539,24 +832,57 @@ namespace {
 
 constexpr int64_t kGBytes = 256 << 20;  // of g at a time: it stays in the 256 MB last-level cache
 
-// Ranges of a sum of nk terms for `tiles` output tiles: enough workgroups to
-// fill the device twice over, none shorter than 256 terms.
-int32_t ranges_of(int64_t tiles, int64_t nk) {
-  const int64_t want = ceil_div(512, tiles);
-  const int64_t most = ceil_div(nk, 256);
-  const int64_t n = want < most ? want : most;
-  return static_cast<int32_t>(n < 1 ? 1 : n);
+// The division of a product that takes the least time by a rough account (us):
+// workgroups take turns on the device, each turn as long as its slabs of 64 k
+// and what a tile costs beside them; the ranges' partial sums are written and
+// read once more.
+Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
+  struct Kind {
+    int32_t edge;
+    int64_t at_once;  // workgroups on the device
+    double slab, slab_alone, tile;
+  };
+  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.62, 0.45, 4.0}, {64, 1024, 1.1, 0.6, 3.0}};
+  Split best = {64, 1};
+  double least = 1e300;
+  for (const Kind& k : kinds) {
+    if (k.edge != 64 && !tiled) continue;
+    const int64_t tiles = ceil_div(na, k.edge) * ceil_div(nb, k.edge), slabs = ceil_div(nk, 64);
+    for (int32_t r = 1; r <= (split ? 64 : 1) && (r == 1 || slabs / r >= 2); ++r) {
+      const int64_t n = tiles * r;
+      double us = static_cast<double>(ceil_div(n, k.at_once)) *
+                  (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
+      if (r > 1) us += 3.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
+      if (us < least) {
+        least = us;
+        best = Split{k.edge, r};
+      }
+    }
+  }
+  return best;
 }
 
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
+// The kernel of a product: tiles of 64 (general), 128 or 256.
 template <typename E, Order OA, Order OB, Epilogue EPI>
-hipError_t launch_gemm(const GemmArgs& g, int ranges, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(g.na, 64)), static_cast<unsigned>(ceil_div(g.nb, 64)),
-                  static_cast<unsigned>(ranges));
+hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
+  const int64_t ta = ceil_div(g.na, edge), tb = ceil_div(g.nb, edge);
+  if constexpr (sizeof(E) == 2) {
+    const dim3 grid(static_cast<unsigned>(round_up(ta * tb * g.ranges, 8)));
+    if (edge == 256)
+      hipLaunchKernelGGL((xent_tile_kernel<OA, OB, EPI, 128, 8>), grid, dim3(512), 0, s, g);
+    else if (edge == 128)
+      hipLaunchKernelGGL((xent_tile_kernel<OA, OB, EPI, 64, 4>), grid, dim3(256), 0, s, g);
+    if (edge != 64) return hipGetLastError();
+  }
+  const dim3 grid(static_cast<unsigned>(ta), static_cast<unsigned>(tb), static_cast<unsigned>(g.ranges));
   hipLaunchKernelGGL((xent_gen_kernel<E, OA, OB, EPI>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
+
+// Rows that the tiled kernel's copies may start at.
+bool fits_tiles(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
 template <typename E>
 hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, hipStream_t s) {
@@ -567,15 +893,17 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
   g.b = Operand{static_cast<const char*>(args->h), args->ldh};
   g.na = d.V;
   g.nb = d.T;
-  g.nk = g.k_split = d.D;
+  g.nk = d.D;
+  g.ranges = 1;
   g.out = ws;
   g.ld_out = d.T;
   g.target = args->target;
   g.target_logit = reinterpret_cast<float*>(ws + p->fwd_target);
-  hipError_t e = launch_gemm<E, kSum, kSum, kEpiLse>(g, 1, s);
+  const int edge = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh) ? p->logits.edge : 64;
+  hipError_t e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 64))), dim3(256), 0, s,
-                     reinterpret_cast<const float2*>(ws), static_cast<int>(p->a_tiles),
+                     reinterpret_cast<const float2*>(ws), static_cast<int>(ceil_div(d.V, edge)),
                      static_cast<int64_t>(d.T), g.target_logit, args->target, d.ignore_index, d.T, d.V,
                      args->loss, args->lse);
   return hipGetLastError();
@@ -640,12 +968,14 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     const int32_t v0 = i * p->piece;
     const int32_t nv = d.V - v0 < p->piece ? d.V - v0 : p->piece;
     const char* w = static_cast<const char*>(args->w) + v0 * args->ldw * p->es;
+    const bool w_fits = fits_tiles(w, args->ldw);
     GemmArgs g = {};
     g.a = Operand{w, args->ldw};
     g.b = Operand{ga.h_live, p->ld_live};
     g.na = nv;
     g.nb = d.T;
-    g.nk = g.k_split = d.D;
+    g.nk = d.D;
+    g.ranges = 1;
     g.n_live = ga.n_live;
     g.out = ws + p->o_g;
     g.ld_out = p->ld_g;
@@ -653,31 +983,31 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     g.lse = ga.live_lse;
     g.v0 = v0;
     g.na_pad = static_cast<int32_t>(round_up(nv, 8));
-    if ((e = launch_gemm<E, kSum, kSum, kEpiGrad>(g, 1, s)) != hipSuccess) return e;
+    if ((e = launch_gemm<E, kSum, kSum, kEpiGrad>(g, w_fits ? p->grad.edge : 64, s)) != hipSuccess) return e;
     if (args->dh) {
       GemmArgs c = {};
-      c.a = Operand{w, args->ldw};
+      c.a = Operand{w, args->ldw, d.D};
       c.b = Operand{ws + p->o_g, p->ld_g};
       c.na = d.D;
       c.nb = d.T;
       c.nk = nv;
       c.n_live = ga.n_live;
-      c.k_split = p->dh_split;
-      const int ranges = static_cast<int>(ceil_div(nv, p->dh_split));
-      if (p->pieces * p->dh_ranges == 1) {
+      c.ranges = p->dh.ranges;
+      const int edge = w_fits ? p->dh.edge : 64;
+      if (p->pieces * p->dh.ranges == 1) {
         c.out = static_cast<char*>(args->dh);
         c.ld_out = args->lddh;
         c.row_map = ga.index;
         c.scale = ga.live_dloss;
         c.scale_step = 1;
-        e = launch_gemm<E, kRow, kSum, kEpiOut>(c, 1, s);
+        e = launch_gemm<E, kRow, kSum, kEpiOut>(c, edge, s);
       } else {
         c.ld_out = round_up(d.D, 4);
         c.part_stride = c.ld_out * d.T;
-        c.out = ws + p->o_dh + static_cast<size_t>(c.part_stride) * 4 * i * p->dh_ranges;
-        e = launch_gemm<E, kRow, kSum, kEpiPart>(c, ranges, s);
+        c.out = ws + p->o_dh + static_cast<size_t>(c.part_stride) * 4 * i * c.ranges;
+        e = launch_gemm<E, kRow, kSum, kEpiPart>(c, edge, s);
         if (e == hipSuccess && i == p->pieces - 1)
-          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), i * p->dh_ranges + ranges,
+          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), p->pieces * c.ranges,
                             c.part_stride, c.ld_out, d.T, ga.n_live, ga.index, ga.live_dloss, 1, d.D,
                             static_cast<char*>(args->dh), args->lddh, s);
       }
@@ -686,25 +1016,25 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     if (args->dw) {
       char* dw = static_cast<char*>(args->dw) + v0 * args->lddw * p->es;
       GemmArgs c = {};
-      c.a = Operand{ga.rh_live, p->ld_live};
-      c.b = Operand{ws + p->o_g, p->ld_g};
+      c.a = Operand{ga.rh_live, p->ld_live, p->ld_live};
+      c.b = Operand{ws + p->o_g, p->ld_g, round_up(nv, 8)};
       c.na = d.D;
       c.nb = nv;
       c.nk = d.T;
       c.n_live = ga.n_live;
-      c.k_split = p->dw_split;
-      if (p->dw_ranges == 1) {
+      c.ranges = p->dw.ranges;
+      if (c.ranges == 1) {
         c.out = dw;
         c.ld_out = args->lddw;
         c.scale = ga.c;
-        e = launch_gemm<E, kRow, kRow, kEpiOut>(c, 1, s);
+        e = launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s);
       } else {
         c.ld_out = round_up(d.D, 4);
         c.part_stride = c.ld_out * nv;
         c.out = ws + p->o_dw;
-        e = launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw_ranges, s);
+        e = launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
         if (e == hipSuccess)
-          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dw), p->dw_ranges, c.part_stride,
+          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dw), c.ranges, c.part_stride,
                             c.ld_out, nv, nullptr, nullptr, ga.c, 0, d.D, dw, args->lddw, s);
       }
       if (e != hipSuccess) return e;
@@ -764,8 +1094,9 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
   if (!p) return FCONV_ERR_INVALID_ARG;
   p->d = d;
   p->es = d.dtype == FCONV_BF16 ? 2 : 4;
-  p->a_tiles = ceil_div(d.V, 64);
-  p->fwd_target = static_cast<size_t>(p->a_tiles) * d.T * 8;
+  const bool tiled = d.dtype == FCONV_BF16 && d.D % 8 == 0;
+  p->logits = choose(d.V, d.T, d.D, tiled, false);
+  p->fwd_target = static_cast<size_t>(ceil_div(d.V, 64)) * d.T * 8;
   p->fwd_bytes = p->fwd_target + static_cast<size_t>(d.T) * 4;
 
   if (d.T > 0) {
@@ -782,12 +1113,9 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->piece = static_cast<int32_t>(piece);
     p->pieces = static_cast<int32_t>(ceil_div(d.V, piece));
     p->ld_g = round_up(piece, 64);
-    const int64_t td = ceil_div(d.D, 64);
-    p->dh_split = static_cast<int32_t>(
-        round_up(ceil_div(piece, ranges_of(td * ceil_div(T, 64), piece)), 64));
-    p->dh_ranges = static_cast<int32_t>(ceil_div(piece, p->dh_split));
-    p->dw_split = static_cast<int32_t>(round_up(ceil_div(T, ranges_of(td * ceil_div(piece, 64), T)), 64));
-    p->dw_ranges = static_cast<int32_t>(ceil_div(T, p->dw_split));
+    p->grad = choose(piece, T, d.D, tiled, false);
+    p->dh = choose(d.D, T, piece, tiled, true);
+    p->dw = choose(d.D, piece, T, d.dtype == FCONV_BF16, true);
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t o = at;
@@ -805,9 +1133,9 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->o_c = take(4);
     p->o_blocks = take(ceil_div(T, 1024) * 8);
     p->o_rh = take(static_cast<size_t>(T) * p->ld_live * p->es);
-    const size_t dh_parts = static_cast<size_t>(p->pieces) * p->dh_ranges;
+    const size_t dh_parts = static_cast<size_t>(p->pieces) * p->dh.ranges;
     p->o_dh = take(dh_parts > 1 ? dh_parts * T * ld4 : 0);
-    p->o_dw = take(p->dw_ranges > 1 ? static_cast<size_t>(p->dw_ranges) * piece * ld4 : 0);
+    p->o_dw = take(p->dw.ranges > 1 ? static_cast<size_t>(p->dw.ranges) * piece * ld4 : 0);
     p->bwd_bytes = at;
   }
   *out = p;

@@ -115,6 +115,7 @@ class MxPlan:
         self._bias = _abi.OP_BIAS in codes
         self._h = ctypes.c_void_p()
         L = _abi.mx_lib()
+        self._destroy = L.fconv_mx_plan_destroy  # still at hand when the interpreter ends
         _check(L.fconv_mx_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_mx_plan_create")
         self._torch = TORCH[dtype]
         n = ctypes.c_size_t()
@@ -125,7 +126,7 @@ class MxPlan:
     def __del__(self):
         h = getattr(self, "_h", None)
         if h is not None and h.value:
-            _abi.mx_lib().fconv_mx_plan_destroy(h)
+            self._destroy(h)
             self._h = ctypes.c_void_p()
 
     def __call__(self, x, w, bias=None, out=None, activ_alpha=0.0, activ_beta=0.0, stream=None):

@@ -32,6 +32,7 @@ class XentPlan:
         self.T, self.D, self.V, self.dtype, self.ignore_index = T, D, V, dtype, ignore_index
         self._h = ctypes.c_void_p()
         L = _abi.xent_lib()
+        self._destroy = L.fconv_xent_plan_destroy  # still at hand when the interpreter ends
         _check(L.fconv_xent_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_xent_plan_create")
         self._torch = TORCH[dtype]
         n = ctypes.c_size_t()
@@ -45,7 +46,7 @@ class XentPlan:
     def __del__(self):
         h = getattr(self, "_h", None)
         if h is not None and h.value:
-            _abi.xent_lib().fconv_xent_plan_destroy(h)
+            self._destroy(h)
             self._h = ctypes.c_void_p()
 
     def _inputs(self, h, w, target):
