@@ -303,47 +303,110 @@ struct MxArgs {
   float act_alpha, act_beta;
 };
 
-// The float epilogue of the convolution plans; a NaN stays a NaN.
-__device__ inline float activate(float t, int act, float alpha, float beta) {
+// The float epilogue of the convolution plans; a NaN stays a NaN.  N values;
+// the kind is asked once for all of them.
+template <int N>
+__device__ inline void activate(f32x4 (&t)[N], int act, float alpha, float beta) {
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[i][e] = f(t[i][e]);
+  };
   switch (act) {  // uniform
-    case 1: return t < 0.0f ? 0.0f : t;
-    case 2: return t > 0.0f ? t : alpha * t;
-    case 3: return t < 0.0f ? 0.0f : t > alpha ? alpha : t;
-    case 4: return t < alpha ? alpha : t > beta ? beta : t;
+    case 1: each([](float v) { return v < 0.0f ? 0.0f : v; }); break;
+    case 2: each([=](float v) { return v > 0.0f ? v : alpha * v; }); break;
+    case 3: each([=](float v) { return v < 0.0f ? 0.0f : v > alpha ? alpha : v; }); break;
+    case 4: each([=](float v) { return v < alpha ? alpha : v > beta ? beta : v; }); break;
   }
-  return t;
 }
 
-// Four consecutive n of row m.
 template <bool BF16>
-__device__ inline void store4(const MxArgs& a, int64_t m, int n, f32x4 t) {
-  if (m >= a.M || n >= a.N) return;
-  char* p = a.y + m * a.ldy_bytes + static_cast<int64_t>(n) * (BF16 ? 2 : 4);
-  const int live = a.N - n;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (a.bias && i < live) t[i] += a.bias[n + i];
-    t[i] = activate(t[i], a.act, a.act_alpha, a.act_beta);
-  }
+__device__ inline void store4(char* p, f32x4 t) {
   if constexpr (BF16) {
-    uint16_t h[4] = {f32_to_bf16(t[0]), f32_to_bf16(t[1]), f32_to_bf16(t[2]), f32_to_bf16(t[3])};
-    if (live >= 4) {
-      __builtin_memcpy(p, h, 8);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < live) __builtin_memcpy(p + 2 * i, &h[i], 2);
-    }
+    const uint16_t h[4] = {f32_to_bf16(t[0]), f32_to_bf16(t[1]), f32_to_bf16(t[2]), f32_to_bf16(t[3])};
+    __builtin_memcpy(p, h, 8);
   } else {
-    if (live >= 4) {
-      __builtin_memcpy(p, &t, 16);
+    __builtin_memcpy(p, &t, 16);
+  }
+}
+// Two matrix tiles side by side in bf16: t0 holds this lane's four n of the
+// first, t1 of the second.  Rows of 16 lanes exchange halves, so that a lane
+// ends with eight consecutive n (those of tile g % 2 from 8 (g / 2) on) and the
+// lanes of a row m write 64 bytes at once.
+__device__ inline void store_pair(char* p, f32x4 t0, f32x4 t1) {
+  uint32_t v[4];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const uint32_t x = f32_to_bf16(t0[2 * d]) | static_cast<uint32_t>(f32_to_bf16(t0[2 * d + 1])) << 16;
+    const uint32_t y = f32_to_bf16(t1[2 * d]) | static_cast<uint32_t>(f32_to_bf16(t1[2 * d + 1])) << 16;
+    const auto s = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    v[d] = s[0];
+    v[2 + d] = s[1];
+  }
+  __builtin_memcpy(p, v, 16);
+}
+template <bool BF16>
+__device__ inline void store1(char* p, float t) {
+  if constexpr (BF16) {
+    const uint16_t h = f32_to_bf16(t);
+    __builtin_memcpy(p, &h, 2);
+  } else {
+    __builtin_memcpy(p, &t, 4);
+  }
+}
+
+// Bias, activation and store of this lane's part of a tile: n[i] .. + 3 of rows
+// m[j] (g = lane / 16; tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is asked once (`whole`): element by
+// element these questions took longer than the rest of the tile's end.
+template <bool BF16, int NI, int NJ>
+__device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
+                              int g, bool whole) {
+  constexpr int ES = BF16 ? 2 : 4;
+  if (a.bias) {
+    f32x4 bias[NI] = {};
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (whole) {
+        __builtin_memcpy(&bias[i], a.bias + n[i], 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n[i] + e < a.N) bias[i][e] = a.bias[n[i] + e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[j][i] += bias[i];
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    activate(acc[j], a.act, a.act_alpha, a.act_beta);
+    if (m[j] >= a.M) continue;
+    char* row = a.y + m[j] * a.ldy_bytes;
+    if (whole) {
+      if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < NI; i += 2)
+          store_pair(row + static_cast<int64_t>(n[i] - 4 * g + (g & 1) * 16 + (g >> 1) * 8) * ES, acc[j][i],
+                     acc[j][i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) store4<BF16>(row + static_cast<int64_t>(n[i]) * ES, acc[j][i]);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < live) {
-          const float v = t[i];
-          __builtin_memcpy(p + 4 * i, &v, 4);
+      for (int i = 0; i < NI; ++i) {
+        char* p = row + static_cast<int64_t>(n[i]) * ES;
+        if (n[i] + 4 <= a.N) {
+          store4<BF16>(p, acc[j][i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n[i] + e < a.N) store1<BF16>(p + e * ES, acc[j][i][e]);
         }
+      }
     }
   }
 }
@@ -358,21 +421,35 @@ __device__ inline f32x4 mma(i32x4 w, i32x4 x, f32x4 acc, int ws, int xs) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, acc, 4, 4, SEL, ws, SEL, xs);
 }
 
-// Tiled product.  A workgroup owns (16 WA TA) n x (16 WB TB) m, a wave TA x TB
-// matrix tiles.  A stage is two k tiles (256 columns) of every row tile of the
-// workgroup, copied buffer->LDS into one of two buffers while the other is
-// consumed; the scales of two stages (four k tiles) are copied together.
-template <bool BF16, int WA, int WB, int TA, int TB>
-__global__ __launch_bounds__(WA* WB * 64) void mx_tile_kernel(MxArgs a) {
-  constexpr int NW = WA * WB;
-  constexpr int RA = WA * TA, RB = WB * TB;  // row tiles of W and of X
-  constexpr int SB = (RA + RB) * 2 * kTileBytes;
-  constexpr int CW = (RA + RB) * 2 / NW;     // copies per wave and stage
-  static_assert((RA + RB) == 4 * NW && RA % 4 == 0, "one scale copy per wave, all W or all X");
-  __shared__ __attribute__((aligned(1024))) char buf0[SB];
-  __shared__ __attribute__((aligned(1024))) char buf1[SB];
-  __shared__ __attribute__((aligned(1024))) char sc0[(RA + RB) * kScaleTile];
-  __shared__ __attribute__((aligned(1024))) char sc1[(RA + RB) * kScaleTile];
+// Tiled product.  A workgroup owns a (2 H) n x (2 H) m tile in four quadrants;
+// NW waves share each quadrant, two along n, NW / 2 along m.  A slab is two k
+// tiles (256 columns) of both operands: four half tiles, copied buffer->LDS,
+// in one of two sets of buffers.  A slab takes four phases, a quadrant each:
+//   phase   reads (LDS)                copies for the slab after next   products
+//   0       W0 but two (and scales)    scales of two slabs on           0 0
+//   1       X1, two fragments of W1    W0, X0 (their readers are done)  0 1
+//   2       the rest of W1             X1                               1 1
+//   3       next slab's X0, two of W0  W1                               1 0
+// A phase is two steps between barriers: a wave reads fragments and starts
+// copies in one, multiplies in the other.  With eight waves the four of the
+// second half of n run one step behind the others, so that on every SIMD one
+// wave multiplies while the other reads.  A step of products takes 256 cycles;
+// six fragments for each of four waves keep LDS (128 bytes a cycle) busy for
+// 192, so the reads are spread evenly.  A copy has more than a slab's time to
+// arrive; the waits stand one phase before the first reads, in phase 2 for W0
+// and X0 of the next slab and in phase 0 for this one's others.  The scales of
+// a pair of slabs (four k tiles) are copied together and read once.
+template <bool BF16, int H, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
+  constexpr int MI = H / 32, MJ = 2 * H / (16 * NW);  // matrix tiles of a wave in a quadrant
+  constexpr int RT = H / 16;                          // row tiles of a half tile
+  constexpr int HB = RT * 2 * kTileBytes;             // bytes of a half tile
+  static_assert(RT == NW, "one row tile per wave and half tile");
+  // Arrays of their own, so that the compiler sees which copies a read does not
+  // meet.
+  __shared__ __attribute__((aligned(1024))) char wx0[2 * HB], x10[HB], w10[HB];
+  __shared__ __attribute__((aligned(1024))) char wx1[2 * HB], x11[HB], w11[HB];
+  __shared__ __attribute__((aligned(1024))) char scales[2][4 * RT * kScaleTile];
 
   // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
   // tiles: eight tile rows of m together, so both panels stay in its L2.
@@ -388,102 +465,177 @@ __global__ __launch_bounds__(WA* WB * 64) void mx_tile_kernel(MxArgs a) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wa = wave % WA, wb = wave / WA;
-  const int64_t rtw = static_cast<int64_t>(tn) * RA, rtx = static_cast<int64_t>(tm) * RB;
+  const int wa = wave / (NW / 2), wb = wave % (NW / 2);
+  const int64_t rtw = static_cast<int64_t>(tn) * 2 * RT, rtx = static_cast<int64_t>(tm) * 2 * RT;
   const int64_t row_bytes = static_cast<int64_t>(a.kt) * kTileBytes;
   const int64_t srow_bytes = static_cast<int64_t>(a.ks) * kScaleTile;
   const auto wr = make_rsrc(a.w.codes + rtw * row_bytes, (a.w.row_tiles - rtw) * row_bytes);
   const auto xr = make_rsrc(a.x.codes + rtx * row_bytes, (a.x.row_tiles - rtx) * row_bytes);
-  const bool swave = 4 * wave < RA;  // this wave copies scales of W, else of X
+  // A wave copies the scales of four row tiles, of W or of X.
+  const bool swave = wave < NW / 2;
   const auto sr = swave ? make_rsrc(a.w.scales + rtw * srow_bytes, (a.w.row_tiles - rtw) * srow_bytes)
                         : make_rsrc(a.x.scales + rtx * srow_bytes, (a.x.row_tiles - rtx) * srow_bytes);
-  const uint32_t s_off = static_cast<uint32_t>((4 * wave - (swave ? 0 : RA) + (lane >> 4)) * srow_bytes +
-                                               (lane & 15) * 16);
+  const uint32_t s_off =
+      static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
+  uint32_t off[2];  // of this wave's row tile in either half, at the next slab to copy
+#pragma unroll
+  for (int h = 0; h < 2; ++h) off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + lane * 16);
+  int next_kt = 0, next_ks = 0;
 
-  auto copy_codes = [&](int st, char* buf) __attribute__((always_inline)) {
+  // Past the last k tile the copies bring zeros.
+  auto copy = [&](const __amdgpu_buffer_rsrc_t& rsrc, int h, char* buf) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < CW; ++i) {
-      const int c = wave + NW * i;
-      const int rt = c >> 1, kt = 2 * st + (c & 1);
-      uint32_t off = kOutOfRange;
-      if (kt < a.kt)
-        off = static_cast<uint32_t>(((rt < RA ? rt : rt - RA) * a.kt + kt) * kTileBytes + lane * 16);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rt < RA ? wr : xr, (lds_ptr_t)(buf + c * kTileBytes), 16,
-                                               off, 0, 0, 0);
-    }
+    for (int c = 0; c < 2; ++c)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (lds_ptr_t)(buf + (wave * 2 + c) * kTileBytes), 16,
+          next_kt + c < a.kt ? off[h] + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange, 0, 0, 0);
   };
-  auto copy_scales = [&](int ks, char* buf) __attribute__((always_inline)) {
-    const uint32_t off = ks < a.ks ? s_off + static_cast<uint32_t>(ks) * kScaleTile : kOutOfRange;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (lds_ptr_t)(buf + wave * 1024), 16, off, 0, 0, 0);
+  auto advance = [&]() __attribute__((always_inline)) {
+    next_kt += 2;
+    off[0] += 2 * kTileBytes;
+    off[1] += 2 * kTileBytes;
+  };
+  auto copy_scales = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        sr, (lds_ptr_t)(scales[next_ks & 1] + wave * 1024), 16,
+        next_ks < a.ks ? s_off + static_cast<uint32_t>(next_ks) * kScaleTile : kOutOfRange, 0, 0, 0);
+    ++next_ks;
   };
 
-  f32x4 acc[TA][TB];
+  f32x4 acc[2 * MJ][2 * MI];
 #pragma unroll
-  for (int i = 0; i < TA; ++i)
+  for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
-    for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int sa[TA], sb[TB];
+    for (int j = 0; j < 2 * MJ; ++j) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int sw[2 * MI], sx[2 * MJ];
+  // Fragments [tile][k tile] of a half of W, but for the first EARLY tiles' first
+  // k tile of W1, which are read while W0 is in use; and of the halves of X.
+  constexpr int EARLY = MI == 4 ? 2 : 0;
+  i32x4 fw[MI][2], fe[EARLY + 1], fx[2][MJ][2];
 
   auto read_scales = [&](const char* buf) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < TA; ++i)
-      sa[i] = *reinterpret_cast<const int*>(buf + (wa * TA + i) * kScaleTile + lane * 4);
+    for (int i = 0; i < 2 * MI; ++i)
+      sw[i] = *reinterpret_cast<const int*>(buf + (i / MI * RT + wa * MI + i % MI) * kScaleTile + lane * 4);
 #pragma unroll
-    for (int j = 0; j < TB; ++j)
-      sb[j] = *reinterpret_cast<const int*>(buf + (RA + wb * TB + j) * kScaleTile + lane * 4);
+    for (int j = 0; j < 2 * MJ; ++j)
+      sx[j] = *reinterpret_cast<const int*>(buf + ((2 + j / MJ) * RT + wb * MJ + j % MJ) * kScaleTile + lane * 4);
   };
-  auto half = [&](const char* buf, auto sel, int kk) __attribute__((always_inline)) {
-    i32x4 fa[TA], fb[TB];
-#pragma unroll
-    for (int i = 0; i < TA; ++i)
-      fa[i] = *reinterpret_cast<const i32x4*>(buf + ((wa * TA + i) * 2 + kk) * kTileBytes + lane * 16);
-#pragma unroll
-    for (int j = 0; j < TB; ++j)
-      fb[j] = *reinterpret_cast<const i32x4*>(buf + ((RA + wb * TB + j) * 2 + kk) * kTileBytes + lane * 16);
-#pragma unroll
-    for (int i = 0; i < TA; ++i)
-#pragma unroll
-      for (int j = 0; j < TB; ++j) acc[i][j] = mma<decltype(sel)::value>(fa[i], fb[j], acc[i][j], sa[i], sb[j]);
+  auto w_at = [&](const char* buf, int i, int kk) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x4*>(buf + ((wa * MI + i) * 2 + kk) * kTileBytes + lane * 16);
   };
-  // Every copy of the stage has landed, for every wave, and every wave has
-  // consumed the other buffer.
-  auto meet = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0);
-    asm volatile("" ::: "memory");
+  auto read_w_rest = [&](const char* buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = kk == 0 ? EARLY : 0; i < MI; ++i) fw[i][kk] = w_at(buf, i, kk);
+  };
+  auto read_x = [&](i32x4 (&x)[MJ][2], const char* buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j)
+        x[j][kk] = *reinterpret_cast<const i32x4*>(buf + ((wb * MJ + j) * 2 + kk) * kTileBytes + lane * 16);
+  };
+  auto read_step_ends = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
+    __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
-  const int nst = (a.kt + 1) / 2;  // stages
-  auto pair = [&](int st, const char* sc, char* sc_next) __attribute__((always_inline)) {
-    meet();
-    copy_codes(st + 1, buf1);  // past the last stage: zeros, never read
-    copy_scales(st / 2 + 1, sc_next);
-    read_scales(sc);
-    half(buf0, std::integral_constant<int, 0>{}, 0);
-    half(buf0, std::integral_constant<int, 1>{}, 1);
-    if (st + 1 < nst) {
-      meet();
-      copy_codes(st + 2, buf0);
-      half(buf1, std::integral_constant<int, 2>{}, 0);
-      half(buf1, std::integral_constant<int, 3>{}, 1);
-    }
+  // SEL: the byte of the scale dwords of the slab's first k tile.
+  auto multiply = [&](int i2, int j2, const i32x4 (&x)[MJ][2], auto sel) __attribute__((always_inline)) {
+    constexpr int SEL = decltype(sel)::value;
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        f32x4& c = acc[j2 * MJ + j][i2 * MI + i];
+        c = mma<SEL>(i2 == 1 && i < EARLY ? fe[i] : fw[i][0], x[j][0], c, sw[i2 * MI + i], sx[j2 * MJ + j]);
+      }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        f32x4& c = acc[j2 * MJ + j][i2 * MI + i];
+        c = mma<SEL + 1>(fw[i][1], x[j][1], c, sw[i2 * MI + i], sx[j2 * MJ + j]);
+      }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
-  copy_codes(0, buf0);
-  copy_scales(0, sc0);
-  for (int st = 0; st < nst; st += 4) {
-    pair(st, sc0, sc1);
-    if (st + 2 < nst) pair(st + 2, sc1, sc0);
+  // x0 holds this slab's X0; xb gets X1, then the next slab's X0.
+  auto slab = [&](char* wx, char* x1, char* w1, const char* wx_next, i32x4 (&x0)[MJ][2], i32x4 (&xb)[MJ][2],
+                  auto sel) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(sel)::value == 0;  // of a pair
+    if (FIRST) read_scales(scales[(next_ks - 1) & 1]);
+    read_w_rest(wx);
+    if (FIRST) copy_scales();
+    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F79 : 0x0F78);  // vmcnt(9 or 8): this slab is here
+    read_step_ends();
+    multiply(0, 0, x0, sel);
+
+    read_x(xb, x1);
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) fe[i] = w_at(w1, i, 0);
+    copy(wr, 0, wx);
+    copy(xr, 0, wx + HB);
+    read_step_ends();
+    multiply(0, 1, xb, sel);
+
+    read_w_rest(w1);
+    copy(xr, 1, x1);
+    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F7B : 0x0F7A);  // vmcnt(11 or 10): the next slab's W0 and X0 are here
+    read_step_ends();
+    multiply(1, 1, xb, sel);
+
+    read_x(xb, wx_next + HB);
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx_next, i, 0);
+    copy(wr, 1, w1);
+    advance();
+    read_step_ends();
+    multiply(1, 0, x0, sel);
+  };
+
+  copy_scales();
+  copy(wr, 0, wx0);
+  copy(xr, 0, wx0 + HB);
+  copy(xr, 1, x10);
+  copy(wr, 1, w10);
+  advance();
+  copy(wr, 0, wx1);
+  copy(xr, 0, wx1 + HB);
+  copy(xr, 1, x11);
+  copy(wr, 1, w11);
+  advance();
+  __builtin_amdgcn_s_waitcnt(0x0F78);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  read_x(fx[0], wx0 + HB);
+#pragma unroll
+  for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
+  if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
+  const int slabs = (a.kt + 1) / 2;
+  for (int s = 0; s + 1 < slabs; s += 2) {
+    slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+    slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
   }
-  __builtin_amdgcn_s_waitcnt(0);  // copies past the last stage land before exit
+  if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+  if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab land before the LDS is given back
 
   const int g = lane >> 4, r = lane & 15;
+  int n[2 * MI];
+  int64_t m[2 * MJ];
 #pragma unroll
-  for (int j = 0; j < TB; ++j) {
-    const int64_t m = (rtx + wb * TB + j) * 16 + r;
+  for (int i = 0; i < 2 * MI; ++i)
+    n[i] = static_cast<int>((rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
 #pragma unroll
-    for (int i = 0; i < TA; ++i)
-      store4<BF16>(a, m, static_cast<int>((rtw + wa * TA + i) * 16 + 4 * g), acc[i][j]);
-  }
+  for (int j = 0; j < 2 * MJ; ++j) m[j] = (rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
+  finish<BF16>(a, acc, n, m, g, (rtw + 2 * RT) * 16 <= a.N);
 }
 
 template <bool BF16>
@@ -492,9 +644,9 @@ hipError_t launch_tiles(const fconv_mx_plan_s* p, MxArgs a, hipStream_t s) {
   a.tiles_n = static_cast<int32_t>(ceil_div(a.N, p->tile));
   const int grid = static_cast<int>(ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n, 8) * 8);
   if (p->tile == 256)
-    hipLaunchKernelGGL((mx_tile_kernel<BF16, 2, 4, 8, 4>), dim3(grid), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), dim3(grid), dim3(512), 0, s, a);
   else
-    hipLaunchKernelGGL((mx_tile_kernel<BF16, 2, 2, 4, 4>), dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -120,6 +120,24 @@ __device__ inline void store4(char* p, f32x4 t, int live) {
   }
 }
 
+// The tiles of two matrix tiles side by side in bf16: t0 holds this lane's four
+// a of the first, t1 of the second.  Rows of 16 lanes exchange halves, so that
+// a lane ends with eight consecutive a and the 16 lanes of each b write 64
+// bytes at once: those of tile q % 2 from a = 8 (q / 2) on.
+__device__ inline void store_pair(char* p, f32x4 t0, f32x4 t1) {
+  uint32_t v[4];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const uint32_t x = f32_to_bf16(t0[2 * d]) | static_cast<uint32_t>(f32_to_bf16(t0[2 * d + 1])) << 16;
+    const uint32_t y = f32_to_bf16(t1[2 * d]) | static_cast<uint32_t>(f32_to_bf16(t1[2 * d + 1])) << 16;
+    const auto s = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    v[d] = s[0];
+    v[2 + d] = s[1];
+  }
+  __builtin_memcpy(p, v, 16);
+}
+__device__ inline int pair_at(int q) { return (q & 1) * 16 + (q >> 1) * 8; }
+
 // What exponents are taken relative to: the maximum, or 0 where it is
 // infinite (inf - inf would be NaN; exp(inf) = inf and exp(-inf) = 0 are right).
 __device__ inline float base_of(float m) { return __builtin_fabsf(m) < __builtin_inff() ? m : 0.0f; }
@@ -134,35 +152,45 @@ __device__ inline void join(float& m, float& s, float m2, float s2) {
   m = mm;
 }
 
-// q of one logit.
-__device__ inline float grad_of(float z, float lse, bool hit) {
-  const float p = exp_of(z - lse);
-  return hit ? p - 1.0f : p;
-}
 
 // What a workgroup does with its tile of C: NI x NJ matrix tiles per wave, of
-// which this lane holds a = a_of(i) .. + 3 of b = b_of(j); ra x rb of the tile
-// exist.  Two waves (wa) share the tile's b; TB of them in all.
-template <typename E, Epilogue EPI, int NI, int NJ, int TB, typename FA, typename FB>
+// which this lane holds a = a_of(i) .. + 3 of b = b_of(j); ra x rb of the EDGE^2
+// tile exist.  Two waves (wa) share the tile's b.  Nothing is asked element by
+// element in a whole tile: with such questions the tile's end took several
+// times as long as its instructions.
+template <typename E, Epilogue EPI, int NI, int NJ, int EDGE, typename FA, typename FB>
 __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t a0, int64_t b0, int ra, int rb,
                                 int tile_a, int range, int wa, int q, FA a_of, FB b_of, float2* red) {
   constexpr int ES = sizeof(E);
+  const bool whole = ra == EDGE;
   if constexpr (EPI == kEpiLse) {
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (a_of(i) + e >= ra)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j][e] = -__builtin_inff();
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       // The target's place in this tile, if it is here.
       const int64_t tgt = (b < rb ? g.target[b0 + b] : -1) - a0;
-      const int at = tgt >= 0 && tgt < ra ? static_cast<int>(tgt) : -1;
-      float m = -__builtin_inff(), s = 0.0f;
+      if (tgt >= 0 && tgt < ra) {
+        const int at = static_cast<int>(tgt);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (a_of(i) + e == at) g.target_logit[b0 + b] = acc[i][j][e];
+      }
+      float m = acc[0][j][0], s = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a_of(i) + e >= ra) acc[i][j][e] = -__builtin_inff();
-          m = fmaxf(m, acc[i][j][e]);
-          if (a_of(i) + e == at) g.target_logit[b0 + b] = acc[i][j][e];
-        }
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
       const float base = base_of(m);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -173,44 +201,79 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
         const float m2 = __shfl_xor(m, x), s2 = __shfl_xor(s, x);
         join(m, s, m2, s2);
       }
-      if (q == 0) red[wa * TB + b] = make_float2(m, s);
+      if (q == 0) red[wa * EDGE + b] = make_float2(m, s);
     }
     __syncthreads();
     if (threadIdx.x < static_cast<unsigned>(rb)) {
-      const float2 p0 = red[threadIdx.x], p1 = red[TB + threadIdx.x];
+      const float2 p0 = red[threadIdx.x], p1 = red[EDGE + threadIdx.x];
       float m = p0.x, s = p0.y;
       join(m, s, p1.x, p1.y);
       reinterpret_cast<float2*>(g.out)[tile_a * g.ld_out + b0 + threadIdx.x] = make_float2(m, s);
     }
-  } else {
+  } else if constexpr (EPI == kEpiGrad) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       if (b >= rb) continue;
-      if constexpr (EPI == kEpiGrad) {
-        const int tgt = g.live_target[b0 + b];
-        const float lse = tgt < 0 ? __builtin_nanf("") : g.lse[b0 + b];
-        const int at = static_cast<int>(tgt - g.v0 - a0);
-        char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
+      const int tgt = g.live_target[b0 + b];
+      const float lse = tgt < 0 ? __builtin_nanf("") : g.lse[b0 + b];
+      const int at = static_cast<int>(tgt - g.v0 - a0);
+      char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int a = a_of(i);
-          if (a0 + a >= g.na_pad) continue;
-          f32x4 t;
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] = a + e < ra ? grad_of(acc[i][j][e], lse, at == a + e) : 0.0f;
-          store4<E>(row + a * ES, t, 4);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_of(acc[i][j][e] - lse);
+      if (at >= 0 && at < ra) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (a_of(i) + e == at) acc[i][j][e] -= 1.0f;
+      }
+      if (whole) {
+        if constexpr (ES == 2) {
+#pragma unroll
+          for (int i = 0; i < NI; i += 2)
+            store_pair(row + (a_of(i) - 4 * q + pair_at(q)) * ES, acc[i][j], acc[i + 1][j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) store4<E>(row + a_of(i) * ES, acc[i][j], 4);
         }
       } else {
-        const int64_t row = EPI == kEpiOut && g.row_map ? g.row_map[b0 + b] : b0 + b;
-        const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
-        constexpr int OS = EPI == kEpiOut ? ES : 4;
-        char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) * OS;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (a0 + a_of(i) >= g.na_pad) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (a_of(i) + e >= ra) acc[i][j][e] = 0.0f;
+          store4<E>(row + a_of(i) * ES, acc[i][j], 4);
+        }
+      }
+    }
+  } else {
+    using O = std::conditional_t<EPI == kEpiOut, E, float>;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int b = b_of(j);
+      if (b >= rb) continue;
+      const int64_t row = EPI == kEpiOut && g.row_map ? g.row_map[b0 + b] : b0 + b;
+      const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
+      char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) *
+                              static_cast<int64_t>(sizeof(O));
+      if (whole) {
+        if constexpr (sizeof(O) == 2) {
+#pragma unroll
+          for (int i = 0; i < NI; i += 2)
+            store_pair(out + (a_of(i) - 4 * q + pair_at(q)) * sizeof(O), acc[i][j] * scale, acc[i + 1][j] * scale);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) store4<O>(out + a_of(i) * sizeof(O), acc[i][j] * scale, 4);
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int n = ra - a_of(i);
-          if (n <= 0) continue;
-          store4<std::conditional_t<EPI == kEpiOut, E, float>>(out + a_of(i) * OS, acc[i][j] * scale, n);
+          if (n > 0) store4<O>(out + a_of(i) * sizeof(O), acc[i][j] * scale, n);
         }
       }
     }
@@ -349,17 +412,25 @@ __global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
 // along a, NW / 2 along b.  A slab is 64 k of both operands: four half tiles,
 // copied buffer->LDS, in one of two sets of buffers.  A slab takes four
 // phases, one quadrant each:
-//   phase   reads (LDS)    copies for the slab after next    products
-//   0       A0, B0         -                                 C00
-//   1       B1             A0, B0 (their readers are done)   C01
-//   2       A1             B1                                C11
-//   3       -              A1                                C10
+//   phase   reads (LDS)                copies for the slab after next   products
+//   0       A0 but two                 -                                C00
+//   1       B1, two fragments of A1    A0, B0 (their readers are done)  C01
+//   2       the rest of A1             B1                               C11
+//   3       next slab's B0, two of A0  A1                               C10
 // A phase is two steps between barriers: a wave reads fragments and starts
 // copies in one, multiplies in the other.  With eight waves the four of a = 1
 // run one step behind the others, so that on every SIMD one wave multiplies
-// while the other reads, and the matrix core never waits for LDS.  A copy has
-// at least one slab's time (2048 cycles) to arrive; the wait for a whole slab
-// stands in phase 3, with the eight copies of the slab after it in flight.
+// while the other reads.  A step of products takes 256 cycles, and LDS gives
+// 128 bytes a cycle: six fragments for each of four waves take 192, so the
+// reads are spread evenly, 6 a phase (12, 4, 8, 0 made the steps of phases 0
+// and 2 wait for LDS: 2.98 against 2.85 million cycles of 8192 x 4096 x 32768
+// logits; the clock falls meanwhile, so less is won in time).  A copy has more
+// than a slab's time to arrive; the waits stand one phase before the first
+// reads, in phase 2 for A0 and B0 of the next slab and in phase 0 for this
+// one's others.
+//
+// Measured: 8192 x 4096 x 32768 logits 1.60 ms, 1.38 PFLOP/s; the matrix cores
+// are busy 74% of the cycles, at 1.86 GHz: power bounds the clock.
 //
 // LDS order.  kSum: rows of 64 k (128 bytes), the 16-byte piece c of row r at
 // c ^ (r % 8): eight consecutive lanes of a fragment read hit eight places.
@@ -443,12 +514,11 @@ struct Feed {
   }
 };
 
-// Fragments of this wave in a half tile: N matrix tiles of 16 rows from row
-// w * 16 N on, two steps of 32 k.
+// Where this wave finds its fragments in a half tile: N matrix tiles of 16
+// rows from row w * 16 N on, two steps of 32 k.
 template <Order O, int H, int N>
 struct Frags {
   int at[O == kSum ? 2 : N];
-  bf16x8 f[N][2];
 
   __device__ void init(int w, int lane) {
     const int r = lane & 15, q = lane >> 4;
@@ -462,19 +532,14 @@ struct Frags {
         at[i] = k * 2 * H + (((2 * (w * N + i) + ((r & 3) >> 1)) ^ row_swz<H>(k)) << 4) + (r & 1) * 8;
     }
   }
-  __device__ void read(const char* buf) {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (O == kSum) {
-          f[i][kk] = *reinterpret_cast<const bf16x8*>(buf + at[kk] + i * 2048);
-        } else {
-          const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H));
-          const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H + 8 * H));
-          f[i][kk] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-      }
+  __device__ bf16x8 one(const char* buf, int i, int kk) const {
+    if constexpr (O == kSum) {
+      return *reinterpret_cast<const bf16x8*>(buf + at[kk] + i * 2048);
+    } else {
+      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H));
+      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H + 8 * H));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
   }
 };
 
@@ -527,16 +592,31 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
     Feed<OB, H, NW> fb;
     fa.init(g.a, a0, OA == kRow ? g.a.width - a0 : ra, k0, k1, wave, lane);
     fb.init(g.b, b0, OB == kRow ? g.b.width - b0 : rb, k0, k1, wave, lane);
-    Frags<OA, H, MI> xa;
-    Frags<OB, H, MJ> xb[2];
-    xa.init(wa, lane);
-    xb[0].init(wb, lane);
-    xb[1].init(wb, lane);
+    Frags<OA, H, MI> pa;
+    Frags<OB, H, MJ> pb;
+    pa.init(wa, lane);
+    pb.init(wb, lane);
+    // Fragments [tile][step] of a half of A, but for the first EARLY tiles' first
+    // step of A1, which are read while A0 is in use; and of the halves of B.
+    constexpr int EARLY = MI == 4 ? 2 : 0;
+    bf16x8 xa[MI][2], xe[EARLY + 1], xb[2][MJ][2];
 
-    // Past the last slab the copies bring zeros that nobody reads.
+    // Past the last slab the copies bring zeros that nobody uses.
     auto advance = [&]() __attribute__((always_inline)) {
       fa.next();
       fb.next();
+    };
+    auto read_b = [&](bf16x8 (&x)[MJ][2], const char* buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) x[j][kk] = pb.one(buf, j, kk);
+    };
+    auto read_a_rest = [&](const char* buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = kk == 0 ? EARLY : 0; i < MI; ++i) xa[i][kk] = pa.one(buf, i, kk);
     };
     auto read_step_ends = [&]() __attribute__((always_inline)) {
       __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
@@ -544,7 +624,7 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto multiply = [&](int i2, int j2, Frags<OB, H, MJ>& b) __attribute__((always_inline)) {
+    auto multiply = [&](int i2, int j2, const bf16x8 (&b)[MJ][2]) __attribute__((always_inline)) {
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
@@ -553,35 +633,41 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
 #pragma unroll
           for (int j = 0; j < MJ; ++j)
             acc[i2 * MI + i][j2 * MJ + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                xa.f[i][kk], b.f[j][kk], acc[i2 * MI + i][j2 * MJ + j], 0, 0, 0);
+                i2 == 1 && kk == 0 && i < EARLY ? xe[i] : xa[i][kk], b[j][kk], acc[i2 * MI + i][j2 * MJ + j], 0, 0, 0);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto slab = [&](char* ab, char* b1b, char* a1b) __attribute__((always_inline)) {
-      xb[0].read(ab + HB);
-      xa.read(ab);
+    // b0 holds this slab's B0 and gets nothing; b1 gets B1, then the next slab's B0.
+    auto slab = [&](char* ab, char* b1b, char* a1b, const char* ab_next, bf16x8 (&b0)[MJ][2], bf16x8 (&b1)[MJ][2])
+                    __attribute__((always_inline)) {
+      read_a_rest(ab);
+      __builtin_amdgcn_s_waitcnt(0x0F78);  // vmcnt(8): this slab is here
       read_step_ends();
-      multiply(0, 0, xb[0]);
+      multiply(0, 0, b0);
 
-      xb[1].read(b1b);
+      read_b(b1, b1b);
+#pragma unroll
+      for (int i = 0; i < EARLY; ++i) xe[i] = pa.one(a1b, i, 0);
       fa.copy(0, ab, wave);
       fb.copy(0, ab + HB, wave);
       read_step_ends();
-      multiply(0, 1, xb[1]);
+      multiply(0, 1, b1);
 
-      xa.read(a1b);
+      read_a_rest(a1b);
       fb.copy(1, b1b, wave);
+      __builtin_amdgcn_s_waitcnt(0x0F7A);  // vmcnt(10): the next slab's A0 and B0 are here
       read_step_ends();
-      multiply(1, 1, xb[1]);
+      multiply(1, 1, b1);
 
+      read_b(b1, ab_next + HB);
+#pragma unroll
+      for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab_next, i, 0);
       fa.copy(1, a1b, wave);
       advance();
-      // All but the eight copies of this slab's successor but one: the next slab is here.
-      __builtin_amdgcn_s_waitcnt(0x0F78);
       read_step_ends();
-      multiply(1, 0, xb[0]);
+      multiply(1, 0, b0);
     };
 
     fa.copy(0, ab0, wave);
@@ -597,12 +683,15 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
     __builtin_amdgcn_s_waitcnt(0x0F78);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    read_b(xb[0], ab0 + HB);
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab0, i, 0);
     if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
     for (int s = 0; s + 1 < slabs; s += 2) {
-      slab(ab0, b01, a01);
-      slab(ab1, b11, a11);
+      slab(ab0, b01, a01, ab1, xb[0], xb[1]);
+      slab(ab1, b11, a11, ab0, xb[1], xb[0]);
     }
-    if (slabs & 1) slab(ab0, b01, a01);
+    if (slabs & 1) slab(ab0, b01, a01, ab1, xb[0], xb[1]);
     if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab land before the LDS is given back
   }

@@ -127,7 +127,7 @@ class MxPlan:
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             self._destroy(h)
-            self._h = ctypes.c_void_p()
+            self._h = None
 
     def __call__(self, x, w, bias=None, out=None, activ_alpha=0.0, activ_beta=0.0, stream=None):
         """x: a GPU tensor [M, K] (its rows may be apart) or an MxTensor; w: an

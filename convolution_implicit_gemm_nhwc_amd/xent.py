@@ -47,7 +47,7 @@ class XentPlan:
         h = getattr(self, "_h", None)
         if h is not None and h.value:
             self._destroy(h)
-            self._h = ctypes.c_void_p()
+            self._h = None
 
     def _inputs(self, h, w, target):
         a = _abi.XentArgs()
