@@ -32,7 +32,8 @@ struct fconv_mx_plan_s {
   bool op_bias;
   int32_t act;      // 0 none, 1 ReLU, 2 leaky, 3 clipped, 4 clamp
   int32_t kt;       // 128-column k tiles
-  int32_t tile;     // output tile edge of the tiled kernel (256 or 128)
+  int32_t kernel;   // fconv::Kernel
+  int32_t ranges;   // of k, whose partial sums a second kernel joins
   size_t ws_x;      // bytes of the quantised x in the workspace
   size_t ws_bytes;
   const char* kernel_name;
@@ -299,6 +300,13 @@ struct MxArgs {
   int64_t ldy_bytes;
   int32_t M, N, kt, ks;  // k tiles of 128, scale tiles of 512
   int32_t tiles_m, tiles_n;
+  int32_t ranges;        // of k
+  float* part;           // ranges > 1: partial sums [range][M][ldp], instead of y
+  int64_t ldp;
+  // An x that is not quantised yet (the kernels that do so themselves).
+  const char* raw;
+  int64_t ldx_bytes;
+  int32_t K;
   int32_t act;
   float act_alpha, act_beta;
 };
@@ -361,8 +369,19 @@ __device__ inline void store1(char* p, float t) {
 // element these questions took longer than the rest of the tile's end.
 template <bool BF16, int NI, int NJ>
 __device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
-                              int g, bool whole) {
+                              int g, bool whole, int range) {
   constexpr int ES = BF16 ? 2 : 4;
+  if (a.part) {  // rows of ldp, a multiple of 4
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (m[j] >= a.M) continue;
+      float* row = a.part + (static_cast<int64_t>(range) * a.M + m[j]) * a.ldp;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (n[i] < a.ldp) *reinterpret_cast<f32x4*>(row + n[i]) = acc[j][i];
+    }
+    return;
+  }
   if (a.bias) {
     f32x4 bias[NI] = {};
 #pragma unroll
@@ -456,11 +475,12 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   const int tiles = a.tiles_m * a.tiles_n;
   const int nb = gridDim.x;  // a multiple of 8
   const int id = (blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8;
-  if (id >= tiles) return;
+  if (id >= tiles * a.ranges) return;
+  const int range = id / tiles, tile = id % tiles;
   const int per = 8 * a.tiles_n;
-  const int m_first = id / per * 8;
+  const int m_first = tile / per * 8;
   const int m_rows = min(8, a.tiles_m - m_first);
-  const int in = id % per;
+  const int in = tile % per;
   const int tm = m_first + in % m_rows, tn = in / m_rows;
 
   const int lane = threadIdx.x & 63;
@@ -477,10 +497,14 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
                         : make_rsrc(a.x.scales + rtx * srow_bytes, (a.x.row_tiles - rtx) * srow_bytes);
   const uint32_t s_off =
       static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
+  // This range's k tiles, whole scale tiles of them.
+  const int ks_per = (a.ks + a.ranges - 1) / a.ranges, ks0 = range * ks_per;
+  const int kt0 = min(4 * ks0, a.kt), kt1 = min(kt0 + 4 * ks_per, a.kt);
   uint32_t off[2];  // of this wave's row tile in either half, at the next slab to copy
 #pragma unroll
-  for (int h = 0; h < 2; ++h) off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + lane * 16);
-  int next_kt = 0, next_ks = 0;
+  for (int h = 0; h < 2; ++h)
+    off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + static_cast<int64_t>(kt0) * kTileBytes + lane * 16);
+  int next_kt = kt0, next_ks = 0;  // next_ks counts from ks0
 
   // Past the last k tile the copies bring zeros.
   auto copy = [&](const __amdgpu_buffer_rsrc_t& rsrc, int h, char* buf) __attribute__((always_inline)) {
@@ -488,7 +512,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     for (int c = 0; c < 2; ++c)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (lds_ptr_t)(buf + (wave * 2 + c) * kTileBytes), 16,
-          next_kt + c < a.kt ? off[h] + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange, 0, 0, 0);
+          next_kt + c < kt1 ? off[h] + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange, 0, 0, 0);
   };
   auto advance = [&]() __attribute__((always_inline)) {
     next_kt += 2;
@@ -498,7 +522,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   auto copy_scales = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         sr, (lds_ptr_t)(scales[next_ks & 1] + wave * 1024), 16,
-        next_ks < a.ks ? s_off + static_cast<uint32_t>(next_ks) * kScaleTile : kOutOfRange, 0, 0, 0);
+        ks0 + next_ks < a.ks ? s_off + static_cast<uint32_t>(ks0 + next_ks) * kScaleTile : kOutOfRange, 0, 0, 0);
     ++next_ks;
   };
 
@@ -618,7 +642,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
 #pragma unroll
   for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
   if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
-  const int slabs = (a.kt + 1) / 2;
+  const int slabs = (kt1 - kt0 + 1) / 2;
   for (int s = 0; s + 1 < slabs; s += 2) {
     slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
     slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
@@ -635,19 +659,376 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     n[i] = static_cast<int>((rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
 #pragma unroll
   for (int j = 0; j < 2 * MJ; ++j) m[j] = (rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
-  finish<BF16>(a, acc, n, m, g, (rtw + 2 * RT) * 16 <= a.N);
+  finish<BF16>(a, acc, n, m, g, (rtw + 2 * RT) * 16 <= a.N, range);
+}
+
+// Loads of 16 bytes that the compiler may keep in flight.
+__device__ inline i32x4 load16(const char* p) { return *reinterpret_cast<const i32x4*>(p); }
+
+// Few rows of x.  The time is W's way out of memory, so W goes straight into
+// registers, in the order in which it is stored: no LDS, no barrier before the
+// end.  A workgroup owns 32 n and one range of k; its four waves take turns at
+// the range's scale tiles (512 columns: 8 KiB of W, all loads in flight, the
+// next turn's while this one is multiplied) and add their sums in LDS, in
+// order.  Many workgroups hide what a wave waits; where n alone gives too few,
+// k is cut into ranges and mx_join_kernel adds them.
+// With RAW the workgroup quantises x itself, into LDS, before it starts: for
+// the few thousand values of one or two tokens that is quicker than a launch.
+template <bool BF16, int MT, bool RAW>
+__global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
+  constexpr int NT = 2, ES = BF16 ? 2 : 4;
+  __shared__ f32x4 sums[4][NT * MT][64];
+  extern __shared__ __attribute__((aligned(16))) char raw_codes[];  // RAW: [k tile][block][M] of 16 bytes, then scales
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int groups = (a.N + 31) / 32;
+  const int range = blockIdx.x / groups;
+  const int64_t nt0 = static_cast<int64_t>(blockIdx.x % groups) * NT;
+  const int ks_per = (a.ks + a.ranges - 1) / a.ranges;
+  const int ks0 = range * ks_per, ks1 = min(ks0 + ks_per, a.ks);
+
+  // A row tile past the last one reads the last one again (it is not stored).
+  const char* wc[NT];
+  const char* wsc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t rt = nt0 + t < a.w.row_tiles ? nt0 + t : a.w.row_tiles - 1;
+    wc[t] = a.w.codes + rt * a.kt * kTileBytes + lane * 16;
+    wsc[t] = a.w.scales + rt * a.ks * kScaleTile + lane * 4;
+  }
+  const char* xc[MT];
+  const char* xsc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t rt = t < a.x.row_tiles ? t : a.x.row_tiles - 1;
+    xc[t] = a.x.codes + rt * a.kt * kTileBytes + lane * 16;
+    xsc[t] = a.x.scales + rt * a.ks * kScaleTile + lane * 4;
+  }
+
+  struct Turn {
+    i32x4 w[NT][4], x[RAW ? 1 : MT][4];
+    int ws[NT], xs[RAW ? 1 : MT];
+  };
+  // k tiles past the last one read the last one again, against zeros of x (the
+  // tail of `multiply`).
+  auto load = [&](Turn& t, int ks) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = static_cast<int64_t>(min(4 * ks + k, a.kt - 1)) * kTileBytes;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) t.w[i][k] = load16(wc[i] + at);
+      if constexpr (!RAW) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) t.x[i][k] = load16(xc[i] + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) t.ws[i] = *reinterpret_cast<const int*>(wsc[i] + static_cast<int64_t>(ks) * kScaleTile);
+    if constexpr (!RAW) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        t.xs[i] = *reinterpret_cast<const int*>(xsc[i] + static_cast<int64_t>(ks) * kScaleTile);
+    }
+  };
+  Turn now, next;
+  int ks = ks0 + wave;
+  if (ks < ks1) load(now, ks);
+
+  const int rows = a.M;  // RAW: of x, at most 16
+  char* raw_scales = raw_codes + static_cast<int64_t>(ks_per) * 4 * 64 * rows;
+  if constexpr (RAW) {
+    // Eight values a thread and step; the four lanes of a block agree on its
+    // largest magnitude.
+    const int per_row = ks_per * 64, total = per_row * rows;
+    for (int i = threadIdx.x; i < total; i += 256) {
+      const int row = i / per_row, e8 = i - row * per_row;
+      const int64_t c = static_cast<int64_t>(ks0) * 512 + e8 * 8;
+      float v[8];
+      if (c < a.K) {
+        load8<BF16>(a.raw + row * a.ldx_bytes + c * ES, static_cast<int>(a.K - c < 8 ? a.K - c : 8), v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+      const uint32_t byte = scale_byte(quad_max(m));
+      const int blk = e8 >> 2;
+      *reinterpret_cast<uint32_t*>(raw_codes + (blk * rows + row) * 16 + (e8 & 3) * 4) = encode8(v, byte);
+      if ((e8 & 3) == 0) raw_scales[blk * rows + row] = static_cast<char>(byte);
+    }
+    __syncthreads();
+  }
+
+  f32x4 acc[MT][NT] = {};
+  auto multiply = [&](Turn& t, int ks) __attribute__((always_inline)) {
+    auto step = [&](auto sel) __attribute__((always_inline)) {
+      constexpr int K = decltype(sel)::value;
+      if (4 * ks + K >= a.kt) return;  // uniform
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        i32x4 x;
+        int xs;
+        if constexpr (RAW) {
+          // Rows past M stand for row 0: they are not stored.
+          const int at = (((ks - ks0) * 4 + K) * 4 + g) * rows + (r < rows ? r : 0);
+          x = *reinterpret_cast<const i32x4*>(raw_codes + at * 16);
+          xs = static_cast<uint8_t>(raw_scales[at]) * 0x01010101;
+        } else {
+          x = t.x[j][K];
+          xs = t.xs[j];
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[j][i] = mma<K>(t.w[i][K], x, acc[j][i], t.ws[i], xs);
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  for (; ks < ks1; ks += 8) {
+    if (ks + 4 < ks1) load(next, ks + 4);
+    multiply(now, ks);
+    if (ks + 4 >= ks1) break;
+    if (ks + 8 < ks1) load(now, ks + 8);
+    multiply(next, ks + 4);
+  }
+
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sums[wave][j * NT + i][lane] = acc[j][i];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 out[1][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    out[0][i] = sums[0][wave * NT + i][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) out[0][i] += sums[w][wave * NT + i][lane];
+  }
+  const int n[NT] = {static_cast<int>(nt0 * 16 + 4 * g), static_cast<int>(nt0 * 16 + 16 + 4 * g)};
+  const int64_t m[1] = {wave * 16 + r};
+  finish<BF16>(a, out, n, m, g, nt0 * 16 + 32 <= a.N, range);
+}
+
+// Many rows, few n: x is read once anyway, so it is quantised on its way into
+// the product and never written.  A wave owns 16 rows; its lane holds one
+// block of 32 values of a row and step, which is the matrix core's own order:
+// the block's largest magnitude and its codes need no other lane.  W (NT tiles
+// of 16 n) comes through the caches; the next step's x is loaded meanwhile.
+template <bool BF16, int NT>
+__global__ __launch_bounds__(256) void mx_rows_kernel(MxArgs a) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int64_t mt = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (mt * 16 >= a.M) return;
+  const int64_t row = mt * 16 + r;
+  const char* xp = a.raw + (row < a.M ? row : a.M - 1) * a.ldx_bytes + g * 32 * ES;
+  const char* wc[NT];
+  const char* wsc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t rt = t < a.w.row_tiles ? t : a.w.row_tiles - 1;
+    wc[t] = a.w.codes + rt * a.kt * kTileBytes + lane * 16;
+    wsc[t] = a.w.scales + rt * a.ks * kScaleTile + lane * 4;
+  }
+  struct Raw {
+    i32x4 q[2 * ES];
+  };
+  auto load = [&](Raw& x, int kt) __attribute__((always_inline)) {
+    const int left = a.K - kt * 128 - g * 32;  // values of this block
+    const char* p = xp + static_cast<int64_t>(kt) * 128 * ES;
+    if (left >= 32) {
+      __builtin_memcpy(&x, p, 32 * ES);
+    } else {
+      using U = std::conditional_t<BF16, uint16_t, uint32_t>;
+      U u[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        u[i] = 0;
+        if (i < left) __builtin_memcpy(&u[i], p + i * ES, ES);
+      }
+      __builtin_memcpy(&x, u, 32 * ES);
+    }
+  };
+  f32x4 acc[1][NT] = {};
+  auto use = [&](const Raw& x, int kt) __attribute__((always_inline)) {
+    i32x4 w[NT];
+    int ws[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      w[t] = load16(wc[t] + static_cast<int64_t>(kt) * kTileBytes);
+      ws[t] = *reinterpret_cast<const int*>(wsc[t] + static_cast<int64_t>(kt >> 2) * kScaleTile) >> (8 * (kt & 3));
+    }
+    float v[32];
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = static_cast<uint32_t>(x.q[i >> 2][i & 3]);
+        v[2 * i] = __builtin_bit_cast(float, u << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, u & 0xffff0000u);
+      }
+    } else {
+      __builtin_memcpy(v, &x, 128);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, abs_bits(v[i]));
+    const uint32_t byte = scale_byte(m);
+    i32x4 c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = static_cast<int>(encode8(v + 8 * i, byte));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][t] = mma<0>(w[t], c, acc[0][t], ws[t], static_cast<int>(byte));
+  };
+  Raw now, next;
+  load(now, 0);
+  for (int kt = 0; kt < a.kt; kt += 2) {
+    if (kt + 1 < a.kt) load(next, kt + 1);
+    use(now, kt);
+    if (kt + 1 >= a.kt) break;
+    if (kt + 2 < a.kt) load(now, kt + 2);
+    use(next, kt + 1);
+  }
+  int n[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) n[t] = 16 * t + 4 * g;
+  const int64_t m[1] = {row};
+  finish<BF16>(a, acc, n, m, g, NT * 16 <= a.N, 0);
+}
+
+// y = act(sum of the ranges, in order, + bias); four n of a row per thread.
+template <bool BF16>
+__global__ __launch_bounds__(256) void mx_join_kernel(MxArgs a) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int quads = (a.N + 3) / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = i / quads;
+  const int n = static_cast<int>(i - m * quads) * 4;
+  if (m >= a.M) return;
+  f32x4 t[1] = {};
+  const float* p0 = a.part + m * a.ldp + n;
+  const int64_t step = static_cast<int64_t>(a.M) * a.ldp;
+  // Eight loads in flight (those past the last range read it again): one at a
+  // time, 13 ranges took 11 us.
+  for (int k = 0; k < a.ranges; k += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4*>(p0 + min(k + i, a.ranges - 1) * step);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < a.ranges) t[0] += v[i];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (a.bias && n + e < a.N) t[0][e] += a.bias[n + e];
+  activate(t, a.act, a.act_alpha, a.act_beta);
+  char* p = a.y + m * a.ldy_bytes + static_cast<int64_t>(n) * ES;
+  if (n + 4 <= a.N) {
+    store4<BF16>(p, t[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) store1<BF16>(p + e * ES, t[0][e]);
+  }
+}
+
+enum Kernel : int32_t { kTile256, kTile128, kFew, kFewRaw, kRows };
+const char* const kKernelNames[] = {"mx_tile_256", "mx_tile_128", "mx_few", "mx_few_raw", "mx_rows"};
+
+// LDS of the few-rows kernel that quantises: a range's codes and scales.
+int few_raw_bytes(const fconv_mx_plan_s* p) {
+  const int64_t ks_per = ceil_div(ceil_div(p->d.K, 512), p->ranges);
+  return static_cast<int>(ks_per * 4 * (64 + 4) * p->d.M);
+}
+
+// The product's kernel and ranges of k.
+void choose_kernel(fconv_mx_plan_s* p) {
+  const int64_t M = p->d.M, N = p->d.N, ks = ceil_div(p->d.K, 512);
+  p->ranges = 1;
+  if (M <= 64) {
+    p->kernel = kFew;
+    const int64_t groups = ceil_div(N, 32);
+    if (groups < 512) {
+      // Ranges until 768 workgroups, none shorter than one turn of its waves.
+      const int64_t want = ceil_div(768, groups), most = ceil_div(ks, 4);
+      const int64_t per = ceil_div(ks, want < most ? want : most);
+      p->ranges = static_cast<int32_t>(ceil_div(ks, per));
+    }
+    if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384) p->kernel = kFewRaw;
+    return;
+  }
+  if (N <= 128 && M >= 4096) {
+    p->kernel = kRows;
+    return;
+  }
+  // The least time by a rough account (us): workgroups take turns on the
+  // device, each as long as its slabs (256 columns) and what a tile costs
+  // beside them; partial sums are written and read once more.
+  struct Kind {
+    int32_t kernel;
+    int64_t edge, at_once;
+    double slab, slab_alone, tile;
+  };
+  static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 8.0}, {kTile128, 128, 512, 1.0, 0.6, 5.0}};
+  double least = 1e300;
+  for (const Kind& k : kinds) {
+    const int64_t tiles = ceil_div(M, k.edge) * ceil_div(N, k.edge);
+    for (int64_t r = 1; r <= ks && r <= 32; ++r) {
+      const int64_t per = ceil_div(ks, r);
+      if (ceil_div(ks, per) != r) continue;  // the same ranges as with fewer
+      double us = static_cast<double>(ceil_div(tiles * r, k.at_once)) *
+                  (2.0 * static_cast<double>(per) * (tiles * r > 256 ? k.slab : k.slab_alone) + k.tile);
+      if (r > 1) us += 3.0 + 8.0 * static_cast<double>(r * M) * static_cast<double>(N) / 4e6;
+      if (us < least) {
+        least = us;
+        p->kernel = k.kernel;
+        p->ranges = static_cast<int32_t>(r);
+      }
+    }
+  }
 }
 
 template <bool BF16>
-hipError_t launch_tiles(const fconv_mx_plan_s* p, MxArgs a, hipStream_t s) {
-  a.tiles_m = static_cast<int32_t>(ceil_div(a.M, p->tile));
-  a.tiles_n = static_cast<int32_t>(ceil_div(a.N, p->tile));
-  const int grid = static_cast<int>(ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n, 8) * 8);
-  if (p->tile == 256)
-    hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), dim3(grid), dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), dim3(grid), dim3(256), 0, s, a);
-  return hipGetLastError();
+hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStream_t s) {
+  const int64_t edge = kernel == kTile256 ? 256 : 128;
+  a.tiles_m = static_cast<int32_t>(ceil_div(a.M, edge));
+  a.tiles_n = static_cast<int32_t>(ceil_div(a.N, edge));
+  const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.ranges, 8) * 8));
+  const dim3 few(static_cast<unsigned>(ceil_div(a.N, 32) * a.ranges));
+  const dim3 rows(static_cast<unsigned>(ceil_div(a.M, 64)));
+  switch (kernel) {
+    case kTile256: hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), grid, dim3(512), 0, s, a); break;
+    case kTile128: hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), grid, dim3(256), 0, s, a); break;
+    case kFewRaw:
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, true>), few, dim3(256), few_raw_bytes(p), s, a);
+      break;
+    case kFew:
+      if (a.M <= 16)
+        hipLaunchKernelGGL((mx_few_kernel<BF16, 1, false>), few, dim3(256), 0, s, a);
+      else if (a.M <= 32)
+        hipLaunchKernelGGL((mx_few_kernel<BF16, 2, false>), few, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((mx_few_kernel<BF16, 4, false>), few, dim3(256), 0, s, a);
+      break;
+    case kRows:
+      if (a.N <= 64)
+        hipLaunchKernelGGL((mx_rows_kernel<BF16, 4>), rows, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((mx_rows_kernel<BF16, 8>), rows, dim3(256), 0, s, a);
+      break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && a.part) {
+    const int64_t threads = static_cast<int64_t>(a.M) * ceil_div(a.N, 4);
+    hipLaunchKernelGGL(mx_join_kernel<BF16>, dim3(static_cast<unsigned>(ceil_div(threads, 256))), dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
@@ -788,10 +1169,12 @@ fconv_status fconv_mx_plan_create(const fconv_mx_desc* desc, fconv_mx_plan* out)
   p->op_bias = bias;
   p->act = act;
   p->kt = static_cast<int32_t>(ceil_div(d.K, 128));
-  p->tile = ceil_div(d.M, 256) * ceil_div(d.N, 256) >= 256 ? 256 : 128;
-  p->ws_x = codes_bytes(d.M, d.K) + scales_bytes(d.M, d.K);
+  choose_kernel(p);
+  if (p->kernel != kFewRaw && p->kernel != kRows)
+    p->ws_x = (codes_bytes(d.M, d.K) + scales_bytes(d.M, d.K) + 255) / 256 * 256;
   p->ws_bytes = p->ws_x;
-  p->kernel_name = p->tile == 256 ? "mx_tile_256" : "mx_tile_128";
+  if (p->ranges > 1) p->ws_bytes += static_cast<size_t>(p->ranges) * d.M * ceil_div(d.N, 4) * 16;
+  p->kernel_name = kKernelNames[p->kernel];
   *out = p;
   return FCONV_OK;
 }
@@ -815,6 +1198,11 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   if ((args->x != nullptr) == (args->x_mx != nullptr)) return FCONV_ERR_INVALID_ARG;
   if (!args->w_mx || !args->y || (p->op_bias && !args->bias)) return FCONV_ERR_INVALID_ARG;
   if ((args->x && args->ldx < d.K) || args->ldy < d.N) return FCONV_ERR_INVALID_ARG;
+  // An x that comes quantised needs no place in the workspace.
+  int kernel = p->kernel;
+  const bool by_itself = args->x && (kernel == kFewRaw || kernel == kRows);
+  if (!args->x && kernel == kFewRaw) kernel = kFew;
+  if (!args->x && kernel == kRows) kernel = kTile128;
   const size_t ws = args->x ? p->ws_bytes : p->ws_bytes - p->ws_x;
   if (ws > 0 && (!args->workspace || args->workspace_bytes < p->ws_bytes)) return FCONV_ERR_WORKSPACE;
   if (!aligned(args->x, p->esize) || !aligned(args->y, p->esize) || !aligned(args->x_mx, 16) ||
@@ -822,11 +1210,12 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
       (ws > 0 && !aligned(args->workspace, 16)))
     return FCONV_ERR_MISALIGNED;
   const size_t yb = span(d.M, d.N, args->ldy, p->esize);
+  const size_t xq = codes_bytes(d.M, d.K) + scales_bytes(d.M, d.K);
   const size_t xb = args->x ? span(d.M, d.K, args->ldx, p->esize) : 0;
   const size_t wb = codes_bytes(d.N, d.K) + scales_bytes(d.N, d.K);
   const size_t wsb = ws > 0 ? p->ws_bytes : 0;
   const void* in[4] = {args->x, args->x_mx, args->w_mx, p->op_bias ? args->bias : nullptr};
-  const size_t in_bytes[4] = {xb, p->ws_x, wb, static_cast<size_t>(d.N) * 4};
+  const size_t in_bytes[4] = {xb, xq, wb, static_cast<size_t>(d.N) * 4};
   for (int i = 0; i < 4; ++i)
     if (overlaps(args->y, yb, in[i], in_bytes[i]) || overlaps(args->workspace, wsb, in[i], in_bytes[i]))
       return FCONV_ERR_INVALID_ARG;
@@ -834,14 +1223,24 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   const void* xmx = args->x_mx;
-  if (args->x) {
+  if (args->x && !by_itself) {
     if (launch_quantize(args->x, args->ldx, d.M, d.K, d.dtype, args->workspace, s) != hipSuccess)
       return FCONV_ERR_DEVICE;
     xmx = args->workspace;
   }
-  MxArgs a;
+  MxArgs a = {};
   a.w = view(args->w_mx, d.N, d.K);
-  a.x = view(xmx, d.M, d.K);
+  if (xmx) a.x = view(xmx, d.M, d.K);
+  if (by_itself) {
+    a.raw = static_cast<const char*>(args->x);
+    a.ldx_bytes = args->ldx * p->esize;
+  }
+  a.K = d.K;
+  a.ranges = p->ranges;
+  if (p->ranges > 1) {
+    a.part = reinterpret_cast<float*>(static_cast<char*>(args->workspace) + p->ws_x);
+    a.ldp = ceil_div(d.N, 4) * 4;
+  }
   a.bias = p->op_bias ? args->bias : nullptr;
   a.y = static_cast<char*>(args->y);
   a.ldy_bytes = args->ldy * p->esize;
@@ -852,7 +1251,8 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   a.act = p->act;
   a.act_alpha = args->activ_alpha;
   a.act_beta = args->activ_beta;
-  const hipError_t e = d.dtype == FCONV_BF16 ? launch_tiles<true>(p, a, s) : launch_tiles<false>(p, a, s);
+  const hipError_t e = d.dtype == FCONV_BF16 ? launch_product<true>(p, a, kernel, s)
+                                             : launch_product<false>(p, a, kernel, s);
   return e == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
 }
 

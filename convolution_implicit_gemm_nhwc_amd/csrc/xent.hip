@@ -704,26 +704,30 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
 
 // ------------------------------------------------------------ small kernels
 
-// Joins the tiles of 64 tokens: four threads per token, each every fourth
-// tile, met in LDS.
+// Joins the tiles of 16 tokens: 16 threads per token, each every 16th tile,
+// four loads in flight, met in LDS in order.
 __global__ __launch_bounds__(256) void xent_join_kernel(const float2* part, int tiles, int64_t ld,
                                                         const float* target_logit,
                                                         const int64_t* target, int64_t ignore,
                                                         int T, int V, float* loss, float* lse) {
-  __shared__ float2 red[4][64];
-  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 64 + c;
+  __shared__ float2 red[16][16];
+  const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + c;
   float m = -__builtin_inff(), s = 0.0f;
   if (t < T)
-    for (int i = k; i < tiles; i += 4) {
-      const float2 p = part[i * ld + t];
-      join(m, s, p.x, p.y);
+    for (int i = k; i < tiles; i += 64) {
+      float2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = part[(i + 16 * u < tiles ? i + 16 * u : i) * ld + t];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + 16 * u < tiles) join(m, s, p[u].x, p[u].y);
     }
   red[k][c] = make_float2(m, s);
   __syncthreads();
   if (k != 0 || t >= T) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) join(m, s, red[i][c].x, red[i][c].y);
+  for (int i = 1; i < 16; ++i) join(m, s, red[i][c].x, red[i][c].y);
   const float l = base_of(m) + logf(s);
   lse[t] = l;
   const int64_t tgt = target[t];
@@ -873,8 +877,17 @@ __global__ __launch_bounds__(256) void xent_sum_kernel(const float* part, int ra
   const int c = static_cast<int>(i - row * quads) * 4;
   if (row >= (n_live ? *n_live : rows)) return;
   f32x4 s = {};
-  for (int k = 0; k < ranges; ++k)  // rows of ld floats, a multiple of 4
-    s += *reinterpret_cast<const f32x4*>(part + k * stride + row * ld + c);
+  const float* p0 = part + row * ld + c;  // rows of ld floats, a multiple of 4
+  // Eight loads in flight; those past the last range read it again.
+  for (int k = 0; k < ranges; k += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const f32x4*>(p0 + (k + i < ranges ? k + i : ranges - 1) * stride);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < ranges) s += v[i];
+  }
   s *= scale[row * scale_step];
   store4<E>(out + ((row_map ? row_map[row] : row) * ld_out + c) * static_cast<int64_t>(sizeof(E)), s,
             cols - c);
@@ -991,7 +1004,7 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
   const int edge = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh) ? p->logits.edge : 64;
   hipError_t e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 64))), dim3(256), 0, s,
+  hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s,
                      reinterpret_cast<const float2*>(ws), static_cast<int>(ceil_div(d.V, edge)),
                      static_cast<int64_t>(d.T), g.target_logit, args->target, d.ignore_index, d.T, d.V,
                      args->loss, args->lse);
