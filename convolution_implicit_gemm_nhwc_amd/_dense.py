@@ -1,5 +1,6 @@
 """What the bindings of the dense operators share: checks of 2-D tensors, and
-where a call's stream, output and workspace come from."""
+where a call's stream, output and workspace come from.  A call of the smallest
+sizes takes longer here than on the GPU, so the common way through is short."""
 from __future__ import annotations
 
 import torch
@@ -12,11 +13,12 @@ def matrix(t, what, rows, cols, dtype):
     [rows, cols] matrix: a 2-D tensor whose rows are dense (any row stride),
     or a contiguous tensor of another shape with rows * cols elements (an
     NHWC feature map, say)."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s: dtype %s, expected %s" % (what, t.dtype, dtype))
-    if t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols:
-        ld = t.stride(0) if rows > 1 else cols
-        if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    if t.shape == (rows, cols):
+        step, one = t.stride()
+        ld = step if rows > 1 else cols
+        if (one != 1 and cols > 1) or ld < cols:
             raise ValueError("%s: rows must be dense and apart (strides %s)" % (what, tuple(t.stride())))
     elif t.numel() == rows * cols and t.is_contiguous():
         ld = cols
@@ -29,7 +31,7 @@ def matrix(t, what, rows, cols, dtype):
 
 def vector(t, what, numel, dtype):
     """Address of a dense GPU vector."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s: dtype %s, expected %s" % (what, t.dtype, dtype))
     if t.numel() != numel:
         raise ValueError("%s: %d elements, the plan needs %d" % (what, t.numel(), numel))
@@ -40,20 +42,29 @@ def vector(t, what, numel, dtype):
     return t.data_ptr()
 
 
+def same_device(first, *others):
+    """The device of all of them (None: not given)."""
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("tensors on different devices (%s and %s)" % (first.device, t.device))
+    return first.device
+
+
+def current_stream(device):
+    """The handle of torch's current stream where `device` is the current one,
+    else None."""
+    at = device.index
+    return torch._C._cuda_getCurrentRawStream(at) if at == torch._C._cuda_getDevice() else None
+
+
 class Launch:
-    """The stream of one call and the device it is on.  With no stream given
-    it is torch's current one.  With another one, torch allocates the call's
-    output and workspace for that stream, so their memory is not handed on
-    while the call still uses it, and the call's inputs are held likewise."""
+    """A call on `stream`, which may belong to another device than the current
+    one and need not be the current stream.  Torch allocates the call's output
+    and workspace for that stream, so their memory is not handed on while the
+    call still uses it, and the call's inputs are held likewise."""
 
     def __init__(self, device, stream, inputs):
-        for t in inputs:
-            if t is not None and t.device != device:
-                raise ValueError("tensors on different devices (%s and %s)" % (device, t.device))
-        self._scope = []
-        if stream is None and device.index == torch.cuda.current_device():
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif isinstance(stream, int):
@@ -64,14 +75,23 @@ class Launch:
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
-        self._scope.append(torch.cuda.stream(stream))  # switches the device too
+        self._scope = torch.cuda.stream(stream)  # switches the device too
 
     def __enter__(self):
-        for s in self._scope:
-            s.__enter__()
+        self._scope.__enter__()
         return self.handle
 
     def __exit__(self, *exc):
-        for s in self._scope:
-            s.__exit__(*exc)
-        return False
+        return self._scope.__exit__(*exc)
+
+
+def call(run, stream, *tensors):
+    """run(handle, device): enqueues a call's work, and allocates what it needs,
+    on `stream` (None: torch's current one).  tensors: what the call is given."""
+    device = same_device(*tensors)
+    if stream is None:
+        handle = current_stream(device)
+        if handle is not None:
+            return run(handle, device)
+    with Launch(device, stream, tensors) as handle:
+        return run(handle, device)

@@ -18,7 +18,7 @@ import torch
 
 from . import _abi
 from . import _check, DTYPES, OPS
-from ._dense import TORCH, Launch, matrix, vector
+from ._dense import TORCH, call, matrix, vector
 
 __all__ = ["MxTensor", "MxQuantPlan", "MxPlan"]
 
@@ -58,11 +58,20 @@ class MxTensor:
         nbytes = _mx_bytes(rows, cols)
         pc = vector(codes, "codes", rows * nb * 16, torch.uint8)
         ps = vector(scales, "scales", rows * nb, torch.uint8)
-        with Launch(codes.device, stream, (codes, scales)) as s:
-            data = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+
+        def run(s, device):
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _check(_abi.mx_lib().fconv_mx_layout(s, pc, ps, rows, cols, data.data_ptr()),
                    "fconv_mx_layout")
-        return cls(data, rows, cols)
+            return data
+        return cls(call(run, stream, codes, scales), rows, cols)
+
+    @classmethod
+    def _of(cls, data, rows, cols):
+        """Of a buffer that a plan has just made."""
+        t = cls.__new__(cls)
+        t.data, t.rows, t.cols = data, rows, cols
+        return t
 
 
 class MxQuantPlan:
@@ -74,25 +83,31 @@ class MxQuantPlan:
             raise ValueError("dtype %r: bf16 or fp32" % (dtype,))
         self._code, self._torch = DTYPES[dtype], TORCH[dtype]
         self.bytes = _mx_bytes(rows, cols)
+        self._lib = _abi.mx_lib()
 
     def __call__(self, x, stream=None):
-        ptr, ld = matrix(x, "x", self.rows, self.cols, self._torch)
-        with Launch(x.device, stream, (x,)) as s:
-            data = torch.empty(self.bytes, dtype=torch.uint8, device=x.device)
-            _check(_abi.mx_lib().fconv_mx_quantize(s, ptr, ld, self.rows, self.cols, self._code,
-                                                   data.data_ptr()), "fconv_mx_quantize")
-        return MxTensor(data, self.rows, self.cols)
+        rows, cols = self.rows, self.cols
+        ptr, ld = matrix(x, "x", rows, cols, self._torch)
+
+        def run(s, device):
+            data = torch.empty(self.bytes, dtype=torch.uint8, device=device)
+            _check(self._lib.fconv_mx_quantize(s, ptr, ld, rows, cols, self._code, data.data_ptr()),
+                   "fconv_mx_quantize")
+            return data
+        return MxTensor._of(call(run, stream, x), rows, cols)
 
     def dequantize(self, t, stream=None):
         """The values of an MxTensor of this plan's size, in the plan's dtype."""
-        if t.shape != (self.rows, self.cols):
-            raise ValueError("MxTensor of %s, the plan needs %s" % (t.shape, (self.rows, self.cols)))
-        with Launch(t.device, stream, (t.data,)) as s:
-            y = torch.empty(self.rows, self.cols, dtype=self._torch, device=t.device)
-            _check(_abi.mx_lib().fconv_mx_dequantize(s, t.data.data_ptr(), self.rows, self.cols,
-                                                     self._code, y.data_ptr(), self.cols),
+        rows, cols = self.rows, self.cols
+        if t.rows != rows or t.cols != cols:
+            raise ValueError("MxTensor of %s, the plan needs %s" % (t.shape, (rows, cols)))
+
+        def run(s, device):
+            y = torch.empty(rows, cols, dtype=self._torch, device=device)
+            _check(self._lib.fconv_mx_dequantize(s, t.data.data_ptr(), rows, cols, self._code, y.data_ptr(), cols),
                    "fconv_mx_dequantize")
-        return y
+            return y
+        return call(run, stream, t.data)
 
 
 class MxPlan:
@@ -114,7 +129,7 @@ class MxPlan:
         self.M, self.N, self.K, self.dtype = M, N, K, dtype
         self._bias = _abi.OP_BIAS in codes
         self._h = ctypes.c_void_p()
-        L = _abi.mx_lib()
+        L = self._lib = _abi.mx_lib()
         self._destroy = L.fconv_mx_plan_destroy  # still at hand when the interpreter ends
         _check(L.fconv_mx_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_mx_plan_create")
         self._torch = TORCH[dtype]
@@ -135,14 +150,13 @@ class MxPlan:
         `out`, whose rows may be apart, if given)."""
         a = _abi.MxArgs()
         if isinstance(x, MxTensor):
-            if x.shape != (self.M, self.K):
+            if x.rows != self.M or x.cols != self.K:
                 raise ValueError("x: MxTensor of %s, the plan needs %s" % (x.shape, (self.M, self.K)))
-            xt = x.data
-            a.x_mx = xt.data_ptr()
+            x = x.data
+            a.x_mx = x.data_ptr()
         else:
-            xt = x
             a.x, a.ldx = matrix(x, "x", self.M, self.K, self._torch)
-        if not isinstance(w, MxTensor) or w.shape != (self.N, self.K):
+        if not isinstance(w, MxTensor) or w.rows != self.N or w.cols != self.K:
             raise ValueError("w: an MxTensor of %s needed" % ((self.N, self.K),))
         if self._bias != (bias is not None):
             raise ValueError("bias: the plan has %s bias op" % ("a" if self._bias else "no"))
@@ -150,12 +164,17 @@ class MxPlan:
         if bias is not None:
             a.bias = vector(bias, "bias", self.N, torch.float32)
         a.activ_alpha, a.activ_beta = activ_alpha, activ_beta
-        with Launch(xt.device, stream, (xt, w.data, bias, out)) as s:
+
+        def run(s, device):
             if out is None:
-                out = torch.empty(self.M, self.N, dtype=self._torch, device=xt.device)
-            a.y, a.ldy = matrix(out, "out", self.M, self.N, self._torch)
+                y = torch.empty(self.M, self.N, dtype=self._torch, device=device)
+                a.y, a.ldy = y.data_ptr(), self.N
+            else:
+                y = out
+                a.y, a.ldy = matrix(out, "out", self.M, self.N, self._torch)
             if self.workspace_bytes:
-                ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=xt.device)
+                ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
                 a.workspace, a.workspace_bytes = ws.data_ptr(), self.workspace_bytes
-            _check(_abi.mx_lib().fconv_mx_plan_run(self._h, s, ctypes.byref(a)), "fconv_mx_plan_run")
-        return out
+            _check(self._lib.fconv_mx_plan_run(self._h, s, ctypes.byref(a)), "fconv_mx_plan_run")
+            return y
+        return call(run, stream, x, w.data, bias, out)

@@ -13,7 +13,7 @@ import torch
 
 from . import _abi
 from . import _check, DTYPES
-from ._dense import TORCH, Launch, matrix, vector
+from ._dense import TORCH, call, matrix, vector
 
 __all__ = ["XentPlan"]
 
@@ -31,7 +31,7 @@ class XentPlan:
         self.desc = d
         self.T, self.D, self.V, self.dtype, self.ignore_index = T, D, V, dtype, ignore_index
         self._h = ctypes.c_void_p()
-        L = _abi.xent_lib()
+        L = self._lib = _abi.xent_lib()
         self._destroy = L.fconv_xent_plan_destroy  # still at hand when the interpreter ends
         _check(L.fconv_xent_plan_create(ctypes.byref(d), ctypes.byref(self._h)), "fconv_xent_plan_create")
         self._torch = TORCH[dtype]
@@ -59,15 +59,16 @@ class XentPlan:
     def forward(self, h, w, target, stream=None):
         """(loss, lse), fp32 [T].  h and w may have rows apart."""
         a = self._inputs(h, w, target)
-        with Launch(h.device, stream, (h, w, target)) as s:
-            out = torch.empty(2, self.T, dtype=torch.float32, device=h.device)
-            loss, lse = out[0], out[1]
-            ws = torch.empty(max(self.forward_workspace_bytes, 16), dtype=torch.uint8, device=h.device)
+
+        def run(s, device):
+            loss = torch.empty(self.T, dtype=torch.float32, device=device)
+            lse = torch.empty(self.T, dtype=torch.float32, device=device)
+            ws = torch.empty(self.forward_workspace_bytes, dtype=torch.uint8, device=device)
             a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-            _check(_abi.xent_lib().fconv_xent_plan_forward(self._h, s, ctypes.byref(a)),
-                   "fconv_xent_plan_forward")
-        return loss, lse
+            a.workspace, a.workspace_bytes = ws.data_ptr(), self.forward_workspace_bytes
+            _check(self._lib.fconv_xent_plan_forward(self._h, s, ctypes.byref(a)), "fconv_xent_plan_forward")
+            return loss, lse
+        return call(run, stream, h, w, target)
 
     def backward(self, h, w, target, lse, dloss, dh=None, dw=None, need_dh=True, need_dw=True,
                  stream=None):
@@ -81,19 +82,23 @@ class XentPlan:
         a = self._inputs(h, w, target)
         a.lse = vector(lse, "lse", self.T, torch.float32)
         a.dloss = vector(dloss, "dloss", self.T, torch.float32)
-        with Launch(h.device, stream, (h, w, target, lse, dloss, dh, dw)) as s:
-            if need_dh:
-                if dh is None:
-                    dh = torch.empty(self.T, self.D, dtype=self._torch, device=h.device)
-                a.dh, a.lddh = matrix(dh, "dh", self.T, self.D, self._torch)
-            if need_dw:
-                if dw is None:
-                    dw = torch.empty(self.V, self.D, dtype=self._torch, device=h.device)
-                a.dw, a.lddw = matrix(dw, "dw", self.V, self.D, self._torch)
-            ws = torch.empty(max(self.backward_workspace_bytes, 16), dtype=torch.uint8, device=h.device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+
+        def run(s, device):
+            gh, gw = dh, dw
+            if gh is not None:
+                a.dh, a.lddh = matrix(gh, "dh", self.T, self.D, self._torch)
+            elif need_dh:
+                gh = torch.empty(self.T, self.D, dtype=self._torch, device=device)
+                a.dh, a.lddh = gh.data_ptr(), self.D
+            if gw is not None:
+                a.dw, a.lddw = matrix(gw, "dw", self.V, self.D, self._torch)
+            elif need_dw:
+                gw = torch.empty(self.V, self.D, dtype=self._torch, device=device)
+                a.dw, a.lddw = gw.data_ptr(), self.D
+            ws = torch.empty(self.backward_workspace_bytes, dtype=torch.uint8, device=device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), self.backward_workspace_bytes
             # Of no tokens dh has no address, and dw is all there is to write.
             if a.dh or a.dw:
-                _check(_abi.xent_lib().fconv_xent_plan_backward(self._h, s, ctypes.byref(a)),
-                       "fconv_xent_plan_backward")
-        return dh, dw
+                _check(self._lib.fconv_xent_plan_backward(self._h, s, ctypes.byref(a)), "fconv_xent_plan_backward")
+            return gh, gw
+        return call(run, stream, h, w, target, lse, dloss, dh, dw)
