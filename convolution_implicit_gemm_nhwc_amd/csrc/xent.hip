@@ -78,7 +78,7 @@ struct GemmArgs {
   char* out;
   int64_t ld_out;
   int64_t part_stride;        // elements between ranges
-  const int32_t* row_map;     // kEpiOut: row of C for b, or NULL
+  const int32_t* row_map;     // kEpiOut: row of C for b (-1 - row: zeros go there), or NULL
   // kEpiLse / kEpiGrad
   const int64_t* target;      // kEpiLse: [nb]
   float* target_logit;        // kEpiLse: [nb]
@@ -256,7 +256,15 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       if (b >= rb) continue;
-      const int64_t row = EPI == kEpiOut && g.row_map ? g.row_map[b0 + b] : b0 + b;
+      int64_t row = b0 + b;
+      if (EPI == kEpiOut && g.row_map) {
+        row = g.row_map[row];
+        if (row < 0) {
+          row = -1 - row;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      }
       const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
       char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) *
                               static_cast<int64_t>(sizeof(O));
@@ -350,20 +358,27 @@ __device__ inline f32x4 mma8(f32x8 a, f32x8 b, f32x4 c) {
   return c;
 }
 
+// LDS of a workgroup: two buffers of both operands, then the epilogue's.
+template <typename E>
+struct GenLds {
+  __attribute__((aligned(16))) char buf[2][2][Gen<E>::BUF];
+  float2 red[2 * 64];
+};
+
+// Tile (x, y) of range z.
 template <typename E, Order OA, Order OB, Epilogue EPI>
-__global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
+__device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y, int z) {
   using G = Gen<E>;
   using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
-  __shared__ __attribute__((aligned(16))) char buf[2][2][G::BUF];
-  __shared__ float2 red[EPI == kEpiLse ? 2 * 64 : 1];
+  auto& buf = lds.buf;
   const int live = g.n_live ? *g.n_live : 0;
   const int nb = g.n_live && OB == kSum ? live : g.nb;
   const int nk = g.n_live && OB == kRow ? live : g.nk;
-  const int64_t a0 = static_cast<int64_t>(blockIdx.x) * 64, b0 = static_cast<int64_t>(blockIdx.y) * 64;
+  const int64_t a0 = static_cast<int64_t>(x) * 64, b0 = static_cast<int64_t>(y) * 64;
   if (b0 >= nb) return;
   const int ra = static_cast<int>(min<int64_t>(g.na - a0, 64)), rb = static_cast<int>(min<int64_t>(nb - b0, 64));
   const int64_t per = round_up(ceil_div(nk, g.ranges), G::SLAB);
-  const int64_t k0 = blockIdx.z * per;
+  const int64_t k0 = z * per;
   const int64_t k1 = min<int64_t>(nk, k0 + per);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave & 1, wb = wave >> 1, r = lane & 15, q = lane >> 4;
@@ -401,8 +416,29 @@ __global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
   }
 
   epilogue<E, EPI, 2, 2, 64>(
-      g, acc, a0, b0, ra, rb, blockIdx.x, blockIdx.z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; },
-      [&](int j) { return wb * 32 + 16 * j + r; }, red);
+      g, acc, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; },
+      [&](int j) { return wb * 32 + 16 * j + r; }, lds.red);
+}
+
+template <typename E, Order OA, Order OB, Epilogue EPI>
+__global__ __launch_bounds__(256) void xent_gen_kernel(GemmArgs g) {
+  __shared__ GenLds<E> lds;
+  gen_tile<E, OA, OB, EPI>(g, lds, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// Both gradients in one launch: the first workgroups take dh's tiles and
+// ranges, the others dw's.
+template <typename E, Epilogue EPI_DH>
+__global__ __launch_bounds__(256) void xent_gen_grads_kernel(GemmArgs dh, GemmArgs dw) {
+  __shared__ GenLds<E> lds;
+  const int ta = (dh.na + 63) / 64, n_dh = ta * ((dh.nb + 63) / 64) * dh.ranges;
+  int i = blockIdx.x;
+  if (i < n_dh) {
+    gen_tile<E, kRow, kSum, EPI_DH>(dh, lds, i % ta, i / ta % ((dh.nb + 63) / 64), i / ta / ((dh.nb + 63) / 64));
+  } else {
+    i -= n_dh;
+    gen_tile<E, kRow, kRow, kEpiOut>(dw, lds, i % ta, i / ta, 0);
+  }
 }
 
 // -------------------------------------------------------------- tiled kernel
@@ -702,32 +738,256 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
       [&](int j) { return j / MJ * H + (wb * MJ + j % MJ) * 16 + r; }, red);
 }
 
+// ------------------------------------------------------------- few tokens
+//
+// At most 64 tokens: the logits' time is w's way out of memory, so fragments
+// of both operands go straight into registers, from any address, without LDS
+// or barriers.  A workgroup owns 32 v and all tokens; its four waves take
+// turns at steps of 128 bytes of k, the next turn's loads in flight, and add
+// their sums in LDS, in order; wave j then finishes tokens 16 j .. + 15.
+//
+// Forward: a workgroup keeps (max, sum) of its tokens over several such groups
+// of v and leaves them once.  Backward: nothing is gathered (three launches
+// less are worth more than the ignored tokens' share); ignored tokens get q = 0
+// and r h = 0, and the products' rows a sign: see row_map.
+struct FewArgs {
+  const char* w;
+  int64_t ldw;
+  const char* h;
+  int64_t ldh;
+  const int64_t* target;
+  int64_t ignore;
+  int32_t T, D, V;
+  int32_t v0, nv;  // the piece of the vocabulary: w begins with row v0
+  // Forward: partial (max, sum) [workgroup][T], and the targets' logits.
+  float2* part;
+  float* target_logit;
+  // Backward.
+  const float* lse;
+  const float* dloss;
+  char* g;
+  int64_t ld_g;
+  char* rh;  // or NULL
+  int64_t ld_rh;
+  int32_t* row_map;
+  float* live_dloss;
+  float* c;
+};
+
+template <typename E, Epilogue EPI, int MT>
+__global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
+  using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
+  constexpr int ES = sizeof(E), NA = 2, STEP = 128 / ES, KK = STEP / 32;
+  __shared__ f32x4 sums[4][MT * NA][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int groups = (f.nv + 31) / 32;
+  const int full = f.D / STEP;  // whole steps
+
+  // Rows past T read the last one again; they are not stored.
+  const char* hp[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) hp[j] = f.h + (static_cast<int64_t>(min(16 * j + r, f.T - 1)) * f.ldh + 8 * q) * ES;
+  // This wave's tokens at the end.
+  const int t = 16 * wave + r;
+  const bool mine = wave < MT && t < f.T;
+  const int64_t tgt = mine ? f.target[t] : -1;
+  const int64_t at_v = tgt - f.v0;  // the target's place in this piece
+  float run_m = -__builtin_inff(), run_s = 0.0f;
+
+  if constexpr (EPI == kEpiGrad) {
+    // r h, and what the products need of each token.  Every workgroup takes a
+    // part of the elements.
+    const int tl = lane < f.T ? lane : f.T - 1;
+    const bool live = f.target[tl] != f.ignore;
+    int m = live ? static_cast<int>(__builtin_bit_cast(uint32_t, f.dloss[tl]) & 0x7fffffffu) : 0;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) m = max(m, __shfl_xor(m, x));
+    const float c = __builtin_bit_cast(float, m);
+    if (blockIdx.x == 0 && wave == 0) {
+      if (lane < f.T) {
+        f.row_map[lane] = live ? lane : -1 - lane;
+        f.live_dloss[lane] = live ? f.dloss[lane] : 0.0f;
+      }
+      if (lane == 0) *f.c = c;
+    }
+    if (f.rh) {
+      constexpr int N = 16 / ES;
+      const int pieces = static_cast<int>(f.ld_rh / N), total = pieces * f.T;
+      for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+        const int row = i / pieces, col = (i - row * pieces) * N;
+        const float dl = f.dloss[row];
+        const float ratio = c > 0.0f ? dl / c : dl;
+        const bool on = f.target[row] != f.ignore;
+        E v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          v[k] = static_cast<E>(0.0f);
+          if (on && col + k < f.D) {
+            __builtin_memcpy(&v[k], f.h + (row * f.ldh + col + k) * ES, ES);
+            v[k] = static_cast<E>(ratio * static_cast<float>(v[k]));
+          }
+        }
+        __builtin_memcpy(f.rh + (row * f.ld_rh + col) * ES, v, 16);
+      }
+    }
+  }
+
+  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+    const char* wp[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      wp[i] = f.w + (static_cast<int64_t>(min(32 * grp + 16 * i + r, f.nv - 1)) * f.ldw + 8 * q) * ES;
+    f32x4 acc[MT][NA] = {};
+    struct Turn {
+      Frag a[NA][KK], b[MT][KK];
+    };
+    auto load = [&](Turn& x, int step) __attribute__((always_inline)) {
+      const int64_t at = static_cast<int64_t>(step) * 128;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) __builtin_memcpy(&x.a[i][k], wp[i] + at + k * 32 * ES, 8 * ES);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) __builtin_memcpy(&x.b[j][k], hp[j] + at + k * 32 * ES, 8 * ES);
+      }
+    };
+    auto multiply = [&](const Turn& x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < KK; ++k)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < NA; ++i) acc[j][i] = mma8(x.a[i][k], x.b[j][k], acc[j][i]);
+    };
+    Turn now, next;
+    int step = wave;
+    if (step < full) load(now, step);
+    for (; step < full; step += 8) {
+      if (step + 4 < full) load(next, step + 4);
+      multiply(now);
+      if (step + 4 >= full) break;
+      if (step + 8 < full) load(now, step + 8);
+      multiply(next);
+    }
+    if (full % 4 == wave && full * STEP < f.D) {  // the rest of k, element by element
+      Turn x;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        const int64_t at = static_cast<int64_t>(full) * STEP + k * 32;
+        const int n = static_cast<int>(f.D - at) - 8 * q;
+        auto part = [&](const char* p) __attribute__((always_inline)) {
+          E v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = static_cast<E>(0.0f);
+            if (e < n) __builtin_memcpy(&v[e], p + (at + e) * ES, ES);
+          }
+          Frag g;
+          __builtin_memcpy(&g, v, 8 * ES);
+          return g;
+        };
+#pragma unroll
+        for (int i = 0; i < NA; ++i) x.a[i][k] = part(wp[i]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) x.b[j][k] = part(hp[j]);
+      }
+      multiply(x);
+    }
+    __syncthreads();  // the sums of the group before are used
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NA; ++i) sums[wave][j * NA + i][lane] = acc[j][i];
+    __syncthreads();
+    if (wave >= MT) continue;
+    f32x4 z[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      z[i] = sums[0][wave * NA + i][lane];
+#pragma unroll
+      for (int x = 1; x < 4; ++x) z[i] += sums[x][wave * NA + i][lane];
+    }
+    if constexpr (EPI == kEpiLse) {
+      float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 32 * grp + 16 * i + 4 * q + e;
+          if (v >= f.nv) z[i][e] = -__builtin_inff();
+          m = fmaxf(m, z[i][e]);
+          if (mine && v < f.nv && v == at_v) f.target_logit[t] = z[i][e];
+        }
+      const float base = base_of(m);
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += exp_of(z[i][e] - base);
+      join(run_m, run_s, m, s);
+    } else if (mine) {
+      const bool live = tgt != f.ignore;
+      const float lse = tgt >= 0 && tgt < f.V ? f.lse[t] : __builtin_nanf("");
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const int v = 32 * grp + 16 * i + 4 * q;
+        if (v >= f.ld_g) continue;  // rows of whole 64s, zeros past V
+        f32x4 p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = exp_of(z[i][e] - lse);
+          if (v + e == at_v) p[e] -= 1.0f;
+          if (!live || v + e >= f.nv) p[e] = 0.0f;
+        }
+        store4<E>(f.g + (t * f.ld_g + v) * ES, p, 4);
+      }
+    }
+  }
+  if constexpr (EPI == kEpiLse) {
+    if (wave >= MT) return;
+#pragma unroll
+    for (int x = 16; x < 64; x *= 2) {
+      const float m2 = __shfl_xor(run_m, x), s2 = __shfl_xor(run_s, x);
+      join(run_m, run_s, m2, s2);
+    }
+    if (q == 0 && mine) f.part[blockIdx.x * static_cast<int64_t>(f.T) + t] = make_float2(run_m, run_s);
+  }
+}
+
 // ------------------------------------------------------------ small kernels
 
-// Joins the tiles of 16 tokens: 16 threads per token, each every 16th tile,
-// four loads in flight, met in LDS in order.
+// Joins the tiles of TOK tokens: 256 / TOK threads per token, each its share of
+// the tiles, four loads in flight, met in LDS in order.
+template <int TOK>
 __global__ __launch_bounds__(256) void xent_join_kernel(const float2* part, int tiles, int64_t ld,
                                                         const float* target_logit,
                                                         const int64_t* target, int64_t ignore,
                                                         int T, int V, float* loss, float* lse) {
-  __shared__ float2 red[16][16];
-  const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + c;
+  constexpr int PER = 256 / TOK;
+  __shared__ float2 red[PER][TOK];
+  const int c = threadIdx.x % TOK, k = threadIdx.x / TOK;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TOK + c;
   float m = -__builtin_inff(), s = 0.0f;
   if (t < T)
-    for (int i = k; i < tiles; i += 64) {
+    for (int i = k; i < tiles; i += 4 * PER) {
       float2 p[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) p[u] = part[(i + 16 * u < tiles ? i + 16 * u : i) * ld + t];
+      for (int u = 0; u < 4; ++u) p[u] = part[(i + PER * u < tiles ? i + PER * u : i) * ld + t];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (i + 16 * u < tiles) join(m, s, p[u].x, p[u].y);
+        if (i + PER * u < tiles) join(m, s, p[u].x, p[u].y);
     }
   red[k][c] = make_float2(m, s);
-  __syncthreads();
-  if (k != 0 || t >= T) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) join(m, s, red[i][c].x, red[i][c].y);
+  for (int n = PER / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (k < n) {
+      join(m, s, red[k + n][c].x, red[k + n][c].y);
+      red[k][c] = make_float2(m, s);
+    }
+  }
+  if (k != 0 || t >= T) return;
   const float l = base_of(m) + logf(s);
   lse[t] = l;
   const int64_t tgt = target[t];
@@ -889,8 +1149,12 @@ __global__ __launch_bounds__(256) void xent_sum_kernel(const float* part, int ra
       if (k + i < ranges) s += v[i];
   }
   s *= scale[row * scale_step];
-  store4<E>(out + ((row_map ? row_map[row] : row) * ld_out + c) * static_cast<int64_t>(sizeof(E)), s,
-            cols - c);
+  int64_t to = row_map ? row_map[row] : row;
+  if (to < 0) {
+    to = -1 - to;
+    s = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  store4<E>(out + (to * ld_out + c) * static_cast<int64_t>(sizeof(E)), s, cols - c);
 }
 
 // Zeros (dw of no tokens).
@@ -954,7 +1218,7 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
       const int64_t n = tiles * r;
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
-      if (r > 1) us += 3.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
+      if (r > 1) us += 6.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
       if (us < least) {
         least = us;
         best = Split{k.edge, r};
@@ -986,28 +1250,75 @@ hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
 // Rows that the tiled kernel's copies may start at.
 bool fits_tiles(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
+constexpr int32_t kFewTokens = 64;
+// Workgroups of the few-token forward kernel.
+int64_t few_groups(int32_t V) { return ceil_div(V, 32) < 1024 ? ceil_div(V, 32) : 1024; }
+
+FewArgs few_args(const fconv_xent_plan_s* p, const fconv_xent_args* args) {
+  FewArgs f = {};
+  f.w = static_cast<const char*>(args->w);
+  f.ldw = args->ldw;
+  f.h = static_cast<const char*>(args->h);
+  f.ldh = args->ldh;
+  f.target = args->target;
+  f.ignore = p->d.ignore_index;
+  f.T = p->d.T;
+  f.D = p->d.D;
+  f.V = f.nv = p->d.V;
+  return f;
+}
+
+template <typename E, Epilogue EPI>
+hipError_t launch_few(const FewArgs& f, int64_t groups, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(groups));
+  if (f.T <= 16)
+    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 1>), grid, dim3(256), 0, s, f);
+  else if (f.T <= 32)
+    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 2>), grid, dim3(256), 0, s, f);
+  else
+    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 4>), grid, dim3(256), 0, s, f);
+  return hipGetLastError();
+}
+
 template <typename E>
 hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, hipStream_t s) {
   const fconv_xent_desc& d = p->d;
   char* ws = static_cast<char*>(args->workspace);
-  GemmArgs g = {};
-  g.a = Operand{static_cast<const char*>(args->w), args->ldw};
-  g.b = Operand{static_cast<const char*>(args->h), args->ldh};
-  g.na = d.V;
-  g.nb = d.T;
-  g.nk = d.D;
-  g.ranges = 1;
-  g.out = ws;
-  g.ld_out = d.T;
-  g.target = args->target;
-  g.target_logit = reinterpret_cast<float*>(ws + p->fwd_target);
-  const int edge = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh) ? p->logits.edge : 64;
-  hipError_t e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
+  float2* part = reinterpret_cast<float2*>(ws);
+  float* target_logit = reinterpret_cast<float*>(ws + p->fwd_target);
+  int tiles;
+  hipError_t e;
+  if (d.T <= kFewTokens) {
+    FewArgs f = few_args(p, args);
+    f.part = part;
+    f.target_logit = target_logit;
+    tiles = static_cast<int>(few_groups(d.V));
+    e = launch_few<E, kEpiLse>(f, tiles, s);
+  } else {
+    GemmArgs g = {};
+    g.a = Operand{static_cast<const char*>(args->w), args->ldw};
+    g.b = Operand{static_cast<const char*>(args->h), args->ldh};
+    g.na = d.V;
+    g.nb = d.T;
+    g.nk = d.D;
+    g.ranges = 1;
+    g.out = ws;
+    g.ld_out = d.T;
+    g.target = args->target;
+    g.target_logit = target_logit;
+    const int edge = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh) ? p->logits.edge : 64;
+    tiles = static_cast<int>(ceil_div(d.V, edge));
+    e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
+  }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(xent_join_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s,
-                     reinterpret_cast<const float2*>(ws), static_cast<int>(ceil_div(d.V, edge)),
-                     static_cast<int64_t>(d.T), g.target_logit, args->target, d.ignore_index, d.T, d.V,
-                     args->loss, args->lse);
+  if (d.T <= 256)
+    hipLaunchKernelGGL(xent_join_kernel<4>, dim3(static_cast<unsigned>(ceil_div(d.T, 4))), dim3(256), 0, s, part,
+                       tiles, static_cast<int64_t>(d.T), target_logit, args->target, d.ignore_index, d.T, d.V,
+                       args->loss, args->lse);
+  else
+    hipLaunchKernelGGL(xent_join_kernel<16>, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s, part,
+                       tiles, static_cast<int64_t>(d.T), target_logit, args->target, d.ignore_index, d.T, d.V,
+                       args->loss, args->lse);
   return hipGetLastError();
 }
 
@@ -1033,114 +1344,152 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
                        static_cast<char*>(args->dw), args->lddw, static_cast<int64_t>(d.V), d.D);
     return hipGetLastError();
   }
+  float* live_dloss = reinterpret_cast<float*>(ws + p->o_dloss);
+  float* c_max = reinterpret_cast<float*>(ws + p->o_c);
+  int32_t* index = reinterpret_cast<int32_t*>(ws + p->o_index);
+  int32_t* n_live = reinterpret_cast<int32_t*>(ws + p->o_n);
+  const bool few = d.T <= kFewTokens;
   GatherArgs ga = {};
-  ga.h = static_cast<const char*>(args->h);
-  ga.ldh = args->ldh;
-  ga.target = args->target;
-  ga.lse = args->lse;
-  ga.dloss = args->dloss;
-  ga.ignore = d.ignore_index;
-  ga.T = d.T;
-  ga.D = d.D;
-  ga.V = d.V;
-  ga.h_live = ws + p->o_h;
-  ga.ld_live = p->ld_live;
-  ga.index = reinterpret_cast<int32_t*>(ws + p->o_index);
-  ga.live_target = reinterpret_cast<int32_t*>(ws + p->o_target);
-  ga.live_lse = reinterpret_cast<float*>(ws + p->o_lse);
-  ga.live_dloss = reinterpret_cast<float*>(ws + p->o_dloss);
-  ga.n_live = reinterpret_cast<int32_t*>(ws + p->o_n);
-  ga.dh = static_cast<char*>(args->dh);
-  ga.lddh = args->lddh;
-  ga.c = reinterpret_cast<float*>(ws + p->o_c);
-  ga.rh_live = args->dw ? ws + p->o_rh : nullptr;
-  // Every workgroup looks at all tokens, which is quicker than another launch
-  // up to some thousands of them.
-  if (d.T > 2048) {
-    int2* blocks = reinterpret_cast<int2*>(ws + p->o_blocks);
-    hipLaunchKernelGGL(xent_count_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 1024))), dim3(256), 0, s,
-                       args->target, args->dloss, d.ignore_index, d.T, blocks);
+  if (few) {
+    n_live = nullptr;
+  } else {
+    ga.h = static_cast<const char*>(args->h);
+    ga.ldh = args->ldh;
+    ga.target = args->target;
+    ga.lse = args->lse;
+    ga.dloss = args->dloss;
+    ga.ignore = d.ignore_index;
+    ga.T = d.T;
+    ga.D = d.D;
+    ga.V = d.V;
+    ga.h_live = ws + p->o_h;
+    ga.ld_live = p->ld_live;
+    ga.index = index;
+    ga.live_target = reinterpret_cast<int32_t*>(ws + p->o_target);
+    ga.live_lse = reinterpret_cast<float*>(ws + p->o_lse);
+    ga.live_dloss = live_dloss;
+    ga.n_live = n_live;
+    ga.dh = static_cast<char*>(args->dh);
+    ga.lddh = args->lddh;
+    ga.c = c_max;
+    ga.rh_live = args->dw ? ws + p->o_rh : nullptr;
+    // Every workgroup looks at all tokens, which is quicker than another launch
+    // up to some thousands of them.
+    if (d.T > 2048) {
+      int2* blocks = reinterpret_cast<int2*>(ws + p->o_blocks);
+      hipLaunchKernelGGL(xent_count_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 1024))), dim3(256), 0, s,
+                         args->target, args->dloss, d.ignore_index, d.T, blocks);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      ga.blocks = blocks;
+    }
+    hipLaunchKernelGGL(xent_gather_kernel<E>, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s, ga);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    ga.blocks = blocks;
   }
-  hipLaunchKernelGGL(xent_gather_kernel<E>, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s, ga);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
 
   for (int i = 0; i < p->pieces; ++i) {
     const int32_t v0 = i * p->piece;
     const int32_t nv = d.V - v0 < p->piece ? d.V - v0 : p->piece;
     const char* w = static_cast<const char*>(args->w) + v0 * args->ldw * p->es;
     const bool w_fits = fits_tiles(w, args->ldw);
-    GemmArgs g = {};
-    g.a = Operand{w, args->ldw};
-    g.b = Operand{ga.h_live, p->ld_live};
-    g.na = nv;
-    g.nb = d.T;
-    g.nk = d.D;
-    g.ranges = 1;
-    g.n_live = ga.n_live;
-    g.out = ws + p->o_g;
-    g.ld_out = p->ld_g;
-    g.live_target = ga.live_target;
-    g.lse = ga.live_lse;
-    g.v0 = v0;
-    g.na_pad = static_cast<int32_t>(round_up(nv, 8));
-    if ((e = launch_gemm<E, kSum, kSum, kEpiGrad>(g, w_fits ? p->grad.edge : 64, s)) != hipSuccess) return e;
-    if (args->dh) {
-      GemmArgs c = {};
-      c.a = Operand{w, args->ldw, d.D};
-      c.b = Operand{ws + p->o_g, p->ld_g};
-      c.na = d.D;
-      c.nb = d.T;
-      c.nk = nv;
-      c.n_live = ga.n_live;
-      c.ranges = p->dh.ranges;
-      const int edge = w_fits ? p->dh.edge : 64;
-      if (p->pieces * p->dh.ranges == 1) {
-        c.out = static_cast<char*>(args->dh);
-        c.ld_out = args->lddh;
-        c.row_map = ga.index;
-        c.scale = ga.live_dloss;
-        c.scale_step = 1;
-        e = launch_gemm<E, kRow, kSum, kEpiOut>(c, edge, s);
-      } else {
-        c.ld_out = round_up(d.D, 4);
-        c.part_stride = c.ld_out * d.T;
-        c.out = ws + p->o_dh + static_cast<size_t>(c.part_stride) * 4 * i * c.ranges;
-        e = launch_gemm<E, kRow, kSum, kEpiPart>(c, edge, s);
-        if (e == hipSuccess && i == p->pieces - 1)
-          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), p->pieces * c.ranges,
-                            c.part_stride, c.ld_out, d.T, ga.n_live, ga.index, ga.live_dloss, 1, d.D,
-                            static_cast<char*>(args->dh), args->lddh, s);
-      }
-      if (e != hipSuccess) return e;
+    if (few) {
+      FewArgs f = few_args(p, args);
+      f.w = w;
+      f.v0 = v0;
+      f.nv = nv;
+      f.lse = args->lse;
+      f.dloss = args->dloss;
+      f.g = ws + p->o_g;
+      f.ld_g = p->ld_g;
+      f.rh = args->dw ? ws + p->o_rh : nullptr;
+      f.ld_rh = p->ld_live;
+      f.row_map = index;
+      f.live_dloss = live_dloss;
+      f.c = c_max;
+      e = launch_few<E, kEpiGrad>(f, p->ld_g / 32, s);
+    } else {
+      GemmArgs g = {};
+      g.a = Operand{w, args->ldw};
+      g.b = Operand{ga.h_live, p->ld_live};
+      g.na = nv;
+      g.nb = d.T;
+      g.nk = d.D;
+      g.ranges = 1;
+      g.n_live = n_live;
+      g.out = ws + p->o_g;
+      g.ld_out = p->ld_g;
+      g.live_target = ga.live_target;
+      g.lse = ga.live_lse;
+      g.v0 = v0;
+      g.na_pad = static_cast<int32_t>(round_up(nv, 8));
+      e = launch_gemm<E, kSum, kSum, kEpiGrad>(g, w_fits ? p->grad.edge : 64, s);
     }
-    if (args->dw) {
-      char* dw = static_cast<char*>(args->dw) + v0 * args->lddw * p->es;
-      GemmArgs c = {};
-      c.a = Operand{ga.rh_live, p->ld_live, p->ld_live};
-      c.b = Operand{ws + p->o_g, p->ld_g, round_up(nv, 8)};
-      c.na = d.D;
-      c.nb = nv;
-      c.nk = d.T;
-      c.n_live = ga.n_live;
-      c.ranges = p->dw.ranges;
-      if (c.ranges == 1) {
-        c.out = dw;
-        c.ld_out = args->lddw;
-        c.scale = ga.c;
-        e = launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s);
-      } else {
-        c.ld_out = round_up(d.D, 4);
-        c.part_stride = c.ld_out * nv;
-        c.out = ws + p->o_dw;
-        e = launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
-        if (e == hipSuccess)
-          e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dw), c.ranges, c.part_stride,
-                            c.ld_out, nv, nullptr, nullptr, ga.c, 0, d.D, dw, args->lddw, s);
-      }
-      if (e != hipSuccess) return e;
+    if (e != hipSuccess) return e;
+
+    // dh of this piece: written at once, or as partial sums that the last piece joins.
+    const bool dh_whole = p->pieces * p->dh.ranges == 1;
+    const int dh_edge = w_fits ? p->dh.edge : 64;
+    GemmArgs h = {};
+    h.a = Operand{w, args->ldw, d.D};
+    h.b = Operand{ws + p->o_g, p->ld_g};
+    h.na = d.D;
+    h.nb = d.T;
+    h.nk = nv;
+    h.n_live = n_live;
+    h.ranges = p->dh.ranges;
+    if (dh_whole) {
+      h.out = static_cast<char*>(args->dh);
+      h.ld_out = args->lddh;
+      h.row_map = index;
+      h.scale = live_dloss;
+      h.scale_step = 1;
+    } else {
+      h.ld_out = round_up(d.D, 4);
+      h.part_stride = h.ld_out * d.T;
+      h.out = ws + p->o_dh + static_cast<size_t>(h.part_stride) * 4 * i * h.ranges;
     }
+    const bool dw_whole = p->dw.ranges == 1;
+    char* dw = static_cast<char*>(args->dw) + (args->dw ? v0 * args->lddw * p->es : 0);
+    GemmArgs c = {};
+    c.a = Operand{ws + p->o_rh, p->ld_live, p->ld_live};
+    c.b = Operand{ws + p->o_g, p->ld_g, round_up(nv, 8)};
+    c.na = d.D;
+    c.nb = nv;
+    c.nk = d.T;
+    c.n_live = n_live;
+    c.ranges = p->dw.ranges;
+    if (dw_whole) {
+      c.out = dw;
+      c.ld_out = args->lddw;
+      c.scale = c_max;
+    } else {
+      c.ld_out = round_up(d.D, 4);
+      c.part_stride = c.ld_out * nv;
+      c.out = ws + p->o_dw;
+    }
+    if (args->dh && args->dw && dh_edge == 64 && p->dw.edge == 64 && dw_whole) {
+      const int64_t ta = ceil_div(d.D, 64);
+      const dim3 grid(static_cast<unsigned>(ta * (ceil_div(d.T, 64) * h.ranges + ceil_div(nv, 64))));
+      if (dh_whole)
+        hipLaunchKernelGGL((xent_gen_grads_kernel<E, kEpiOut>), grid, dim3(256), 0, s, h, c);
+      else
+        hipLaunchKernelGGL((xent_gen_grads_kernel<E, kEpiPart>), grid, dim3(256), 0, s, h, c);
+      e = hipGetLastError();
+    } else {
+      if (args->dh)
+        e = dh_whole ? launch_gemm<E, kRow, kSum, kEpiOut>(h, dh_edge, s)
+                     : launch_gemm<E, kRow, kSum, kEpiPart>(h, dh_edge, s);
+      if (e == hipSuccess && args->dw)
+        e = dw_whole ? launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s)
+                     : launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
+    }
+    if (e == hipSuccess && args->dh && !dh_whole && i == p->pieces - 1)
+      e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), p->pieces * h.ranges, h.part_stride,
+                        h.ld_out, d.T, n_live, index, live_dloss, 1, d.D, static_cast<char*>(args->dh),
+                        args->lddh, s);
+    if (e == hipSuccess && args->dw && !dw_whole)
+      e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dw), c.ranges, c.part_stride, c.ld_out, nv,
+                        nullptr, nullptr, c_max, 0, d.D, dw, args->lddw, s);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
@@ -1198,7 +1547,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
   p->es = d.dtype == FCONV_BF16 ? 2 : 4;
   const bool tiled = d.dtype == FCONV_BF16 && d.D % 8 == 0;
   p->logits = choose(d.V, d.T, d.D, tiled, false);
-  p->fwd_target = static_cast<size_t>(ceil_div(d.V, 64)) * d.T * 8;
+  p->fwd_target = static_cast<size_t>(d.T <= kFewTokens ? few_groups(d.V) : ceil_div(d.V, 64)) * d.T * 8;
   p->fwd_bytes = p->fwd_target + static_cast<size_t>(d.T) * 4;
 
   if (d.T > 0) {

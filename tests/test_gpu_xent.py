@@ -94,6 +94,8 @@ def _check(h, w, t, dl, dtype, plan=None, **kw):
 SIZES = [(1, 1, 1), (1, 64, 500), (2, 8, 70), (3, 33, 17), (16, 100, 300), (17, 1000, 1003), (32, 512, 1000),
          (64, 64, 64), (65, 130, 257), (130, 511, 129), (33, 8, 5000), (200, 96, 700), (300, 520, 1100),
          (700, 64, 600), (1500, 72, 520)]
+# At most 64 tokens, and the first number above; k of less than a step, whole steps, a ragged rest; many groups of v.
+SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576, 2000), (66, 576, 2000), (5, 40, 70001)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
