@@ -158,9 +158,36 @@ __device__ inline void join(float& m, float& s, float m2, float s2) {
 // tile exist.  Two waves (wa) share the tile's b.  Nothing is asked element by
 // element in a whole tile: with such questions the tile's end took several
 // times as long as its instructions.
+template <Epilogue EPI, int NJ>
+struct PerB {  // what it has to know of each b
+  int at[NJ];    // kEpiLse, kEpiGrad: the target's place in the tile, or none; kEpiOut: the row
+  float f[NJ];   // kEpiGrad: lse; kEpiOut: factor
+};
+template <Epilogue EPI, int NJ, typename FB>
+__device__ inline PerB<EPI, NJ> load_per_b(const GemmArgs& g, int64_t a0, int64_t b0, int ra, int rb, FB b_of) {
+  PerB<EPI, NJ> p;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int64_t b = b0 + min(b_of(j), rb - 1);
+    if constexpr (EPI == kEpiLse) {
+      const int64_t t = g.target[b] - a0;
+      p.at[j] = t >= 0 && t < ra ? static_cast<int>(t) : -1;
+    } else if constexpr (EPI == kEpiGrad) {
+      const int t = g.live_target[b];
+      p.at[j] = static_cast<int>(t - g.v0 - a0);
+      p.f[j] = t < 0 ? __builtin_nanf("") : g.lse[b];
+    } else if constexpr (EPI == kEpiOut) {
+      p.at[j] = g.row_map ? g.row_map[b] : static_cast<int>(b);
+      p.f[j] = g.scale[b * g.scale_step];
+    }
+  }
+  return p;
+}
+
 template <typename E, Epilogue EPI, int NI, int NJ, int EDGE, typename FA, typename FB>
-__device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t a0, int64_t b0, int ra, int rb,
-                                int tile_a, int range, int wa, int q, FA a_of, FB b_of, float2* red) {
+__device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const PerB<EPI, NJ>& per, int64_t a0,
+                                int64_t b0, int ra, int rb, int tile_a, int range, int wa, int q, FA a_of,
+                                FB b_of, float2* red) {
   constexpr int ES = sizeof(E);
   const bool whole = ra == EDGE;
   if constexpr (EPI == kEpiLse) {
@@ -176,10 +203,8 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
-      // The target's place in this tile, if it is here.
-      const int64_t tgt = (b < rb ? g.target[b0 + b] : -1) - a0;
-      if (tgt >= 0 && tgt < ra) {
-        const int at = static_cast<int>(tgt);
+      const int at = b < rb ? per.at[j] : -1;
+      if (at >= 0) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -215,9 +240,8 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       if (b >= rb) continue;
-      const int tgt = g.live_target[b0 + b];
-      const float lse = tgt < 0 ? __builtin_nanf("") : g.lse[b0 + b];
-      const int at = static_cast<int>(tgt - g.v0 - a0);
+      const int at = per.at[j];
+      const float lse = per.f[j];
       char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -257,15 +281,16 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
       const int b = b_of(j);
       if (b >= rb) continue;
       int64_t row = b0 + b;
-      if (EPI == kEpiOut && g.row_map) {
-        row = g.row_map[row];
+      float scale = 1.0f;
+      if constexpr (EPI == kEpiOut) {
+        row = per.at[j];
+        scale = per.f[j];
         if (row < 0) {
           row = -1 - row;
 #pragma unroll
           for (int i = 0; i < NI; ++i) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
       }
-      const float scale = EPI == kEpiOut ? g.scale[(b0 + b) * g.scale_step] : 1.0f;
       char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) *
                               static_cast<int64_t>(sizeof(O));
       if (whole) {
@@ -288,13 +313,44 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], int64_t
   }
 }
 
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16* lds_v4i16_t;
+
+constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset past every extent: reads 0
+constexpr int kBufferDword3 = 0x00020000;      // raw buffer descriptor, gfx9 family
+
+__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const uint32_t n = bytes > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(bytes < 0 ? 0 : bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(n), kBufferDword3);
+}
+
+// Place of 16-byte pieces in a row k of H bf16 in LDS (xor of their number), so
+// that the rows that one transposed read touches lie on different banks.
+template <int H>
+__device__ inline int row_swz(int k) {
+  return H == 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : (((k & 3) << 1) ^ (((k >> 3) & 1) << 1)) & 7;
+}
+
+// Eight consecutive k of row a of an operand in kRow order: lane i's element e
+// of a 16-lane group is element i % 4 of the 8 bytes addressed by the group's
+// lane 4 e + i / 4; `p` is this lane's address, `next` bytes on are four rows.
+__device__ inline bf16x8 read_transposed(const char* p, int next) {
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)p);
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(p + next));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // ------------------------------------------------------------ general kernel
 //
 // Any type, alignment and stride: 64 x 64 tiles, four waves of 32 x 32, slabs
 // of 128 bytes of k staged through registers into one of two LDS buffers
 // (rows of 128 + 16 bytes, so that fragment reads spread over the banks).  A
 // fragment is eight consecutive k of a row; for fp32 the eight 16x16x4
-// products take one of them each, in both operands alike.
+// products take one of them each, in both operands alike.  An operand in kRow
+// order is transposed on its way out of LDS for bf16 (the tiled kernel's order
+// and reads), on its way in for fp32.
 template <typename E>
 struct Gen {
   static constexpr int ES = sizeof(E);
@@ -340,12 +396,31 @@ __device__ inline void gen_write(char* buf, const E v[32 / sizeof(E)]) {
   const int tid = threadIdx.x;
   if constexpr (O == kSum) {
     __builtin_memcpy(buf + (tid >> 2) * Gen<E>::PITCH + (tid & 3) * 32, v, 32);
+  } else if constexpr (sizeof(E) == 2) {
+    const int k = tid >> 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_memcpy(buf + k * 128 + (((2 * (tid & 3) + i) ^ row_swz<64>(k)) << 4), v + 8 * i, 16);
   } else {
     constexpr int TPK = 64 / N;
     const int k = tid / TPK, c = (tid % TPK) * N;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       *reinterpret_cast<E*>(buf + (c + i) * Gen<E>::PITCH + k * sizeof(E)) = v[i];
+  }
+}
+
+// Fragment of rows row0 + lane % 16, k from kk + 8 (lane / 16) on.
+template <typename E, Order O>
+__device__ inline auto gen_read(const char* buf, int row0, int kk) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  if constexpr (O == kRow && sizeof(E) == 2) {
+    const int k = kk + 8 * q + (r >> 2);
+    return read_transposed(buf + k * 128 + (((row0 / 8 + ((r & 3) >> 1)) ^ row_swz<64>(k)) << 4) + (r & 1) * 8, 512);
+  } else {
+    std::conditional_t<sizeof(E) == 2, bf16x8, f32x8> f;
+    __builtin_memcpy(&f, buf + (row0 + r) * Gen<E>::PITCH + (kk + 8 * q) * sizeof(E), 8 * sizeof(E));
+    return f;
   }
 }
 
@@ -405,8 +480,8 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
       Frag fa[2], fb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        __builtin_memcpy(&fa[i], ba + (wa * 32 + 16 * i + r) * G::PITCH + (kk + 8 * q) * G::ES, 8 * G::ES);
-        __builtin_memcpy(&fb[i], bb + (wb * 32 + 16 * i + r) * G::PITCH + (kk + 8 * q) * G::ES, 8 * G::ES);
+        fa[i] = gen_read<E, OA>(ba, wa * 32 + 16 * i, kk);
+        fb[i] = gen_read<E, OB>(bb, wb * 32 + 16 * i, kk);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -415,9 +490,10 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
     }
   }
 
+  auto b_of = [&](int j) { return wb * 32 + 16 * j + r; };
+  const auto per_b = load_per_b<EPI, 2>(g, a0, b0, ra, rb, b_of);
   epilogue<E, EPI, 2, 2, 64>(
-      g, acc, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; },
-      [&](int j) { return wb * 32 + 16 * j + r; }, lds.red);
+      g, acc, per_b, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; }, b_of, lds.red);
 }
 
 template <typename E, Order OA, Order OB, Epilogue EPI>
@@ -474,24 +550,6 @@ __global__ __launch_bounds__(256) void xent_gen_grads_kernel(GemmArgs dh, GemmAr
 // (ds_read_b64_tr_b16: lane i's element e of a 16-lane group is element i % 4
 // of the 8 bytes addressed by the group's lane 4 e + i / 4), pieces swizzled
 // by swz(k) so that the rows that one read touches lie on different banks.
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4i16* lds_v4i16_t;
-
-constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset past every extent: reads 0
-constexpr int kBufferDword3 = 0x00020000;      // raw buffer descriptor, gfx9 family
-
-__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const uint32_t n = bytes > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(bytes < 0 ? 0 : bytes);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
-                                           static_cast<int>(n), kBufferDword3);
-}
-
-template <int H>
-__device__ inline int row_swz(int k) {
-  return H == 128 ? ((k & 3) << 1) | (((k >> 3) & 1) << 3) : (((k & 3) << 1) ^ (((k >> 3) & 1) << 1)) & 7;
-}
-
 // One operand of a workgroup: where its half tiles come from, and this lane's
 // places in them.
 template <Order O, int H, int NW>
@@ -503,14 +561,9 @@ struct Feed {
   uint32_t off[2][2];  // per half and copy of this wave
   int chunk;           // kSum: first k of this lane's piece
 
-  // rows x k: the tile at (row0, k0), `rows` of its rows and nk of the sum exist.
-  __device__ void init(const Operand& op, int64_t row0, int64_t rows, int64_t k0, int64_t k1, int wave, int lane) {
+  __device__ void init(const Operand& op, int wave, int lane) {
     if constexpr (O == kSum) {
-      base = op.p + (row0 * op.ld + k0) * 2;
-      // The last row ends with k1, rounded up to whole pieces (their rest is zeros or masked).
-      left = ((rows - 1) * op.ld + ((k1 - k0 + 7) & ~7)) * 2;
       step = 128;
-      krem = static_cast<int>(k1 - k0);
       chunk = ((lane & 7) ^ (lane >> 3)) * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -518,8 +571,6 @@ struct Feed {
         for (int c = 0; c < 2; ++c)
           off[h][c] = static_cast<uint32_t>(((h * H + (wave * 2 + c) * 8 + (lane >> 3)) * op.ld + chunk) * 2);
     } else {
-      base = op.p + (k0 * op.ld + row0) * 2;
-      left = ((k1 - k0 - 1) * op.ld + ((rows + 7) & ~7)) * 2;
       step = op.ld * 128;
       krem = 0;
       chunk = 0;
@@ -531,6 +582,18 @@ struct Feed {
           const int k = (wave * 2 + c) * RPC + lane / PPR;
           off[h][c] = static_cast<uint32_t>((k * op.ld + h * H + ((lane % PPR) ^ row_swz<H>(k)) * 8) * 2);
         }
+    }
+  }
+  // The tile at (row0, k0): `rows` of its rows and k0 .. k1 of the sum exist.
+  __device__ void start(const Operand& op, int64_t row0, int64_t rows, int64_t k0, int64_t k1) {
+    if constexpr (O == kSum) {
+      base = op.p + (row0 * op.ld + k0) * 2;
+      // The last row ends with k1, rounded up to whole pieces (their rest is zeros or masked).
+      left = ((rows - 1) * op.ld + ((k1 - k0 + 7) & ~7)) * 2;
+      krem = static_cast<int>(k1 - k0);
+    } else {
+      base = op.p + (k0 * op.ld + row0) * 2;
+      left = ((k1 - k0 - 1) * op.ld + ((rows + 7) & ~7)) * 2;
     }
   }
   // Copies half h of the next slab into buf (this wave's 2 KiB of it).
@@ -572,9 +635,7 @@ struct Frags {
     if constexpr (O == kSum) {
       return *reinterpret_cast<const bf16x8*>(buf + at[kk] + i * 2048);
     } else {
-      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H));
-      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t)(buf + at[i] + kk * 64 * H + 8 * H));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      return read_transposed(buf + at[i] + kk * 64 * H, 8 * H);
     }
   }
 };
@@ -599,35 +660,60 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
   const int tiles_a = (g.na + 2 * H - 1) / (2 * H), tiles_b = (nb + 2 * H - 1) / (2 * H);
   const int tiles = tiles_a * tiles_b;
   const int total = tiles * g.ranges, share = (total + 7) / 8;
-  const int slot = blockIdx.x / 8;
-  const int id = (blockIdx.x % 8) * share + slot;
-  if (slot >= share || id >= total) return;
-  const int range = id / tiles, tile = id % tiles;
-  const int first = tile / (8 * tiles_a) * 8, rows8 = min(8, tiles_b - first), in = tile % (8 * tiles_a);
-  const int tb = first + in % rows8, ta = in / rows8;
-  const int64_t a0 = static_cast<int64_t>(ta) * 2 * H, b0 = static_cast<int64_t>(tb) * 2 * H;
-  const int ra = static_cast<int>(min<int64_t>(g.na - a0, 2 * H)), rb = static_cast<int>(min<int64_t>(nb - b0, 2 * H));
-  // Ranges of whole slabs.
-  const int all = (nk + 63) / 64, per = (all + g.ranges - 1) / g.ranges;
-  const int64_t k0 = static_cast<int64_t>(range) * per * 64;
-  const int slabs = max(0, min(per, all - range * per));
-  const int64_t k1 = min<int64_t>(nk, k0 + static_cast<int64_t>(slabs) * 64);
+  const int first_id = (blockIdx.x % 8) * share, end = min(share, total - first_id);
+  int slot = blockIdx.x / 8;
+  if (slot >= end) return;
+  const int all = (nk + 63) / 64, per = (all + g.ranges - 1) / g.ranges;  // slabs: of all ranges, of one
+  struct Place {
+    int range, ta, ra, rb, slabs;
+    int64_t a0, b0, k0, k1;
+  };
+  auto locate = [&](int id) __attribute__((always_inline)) {
+    Place p;
+    const int tile = id % tiles;
+    const int first = tile / (8 * tiles_a) * 8, rows8 = min(8, tiles_b - first), in = tile % (8 * tiles_a);
+    p.range = id / tiles;
+    p.ta = in / rows8;
+    p.a0 = static_cast<int64_t>(p.ta) * 2 * H;
+    p.b0 = static_cast<int64_t>(first + in % rows8) * 2 * H;
+    p.ra = static_cast<int>(min<int64_t>(g.na - p.a0, 2 * H));
+    p.rb = static_cast<int>(min<int64_t>(nb - p.b0, 2 * H));
+    p.k0 = static_cast<int64_t>(p.range) * per * 64;
+    p.slabs = max(0, min(per, all - p.range * per));
+    p.k1 = min<int64_t>(nk, p.k0 + static_cast<int64_t>(p.slabs) * 64);
+    return p;
+  };
+  Place at = locate(first_id + slot);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wa = wave / (NW / 2), wb = wave % (NW / 2), r = lane & 15, q = lane >> 4;
+  const int wa = wave / (NW / 2), wb = wave % (NW / 2);
 
   f32x4 acc[2 * MI][2 * MJ];
-#pragma unroll
-  for (int i = 0; i < 2 * MI; ++i)
-#pragma unroll
-    for (int j = 0; j < 2 * MJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (slabs > 0) {
-    Feed<OA, H, NW> fa;
-    Feed<OB, H, NW> fb;
-    fa.init(g.a, a0, OA == kRow ? g.a.width - a0 : ra, k0, k1, wave, lane);
-    fb.init(g.b, b0, OB == kRow ? g.b.width - b0 : rb, k0, k1, wave, lane);
+  Feed<OA, H, NW> fa;
+  Feed<OB, H, NW> fb;
+  fa.init(g.a, wave, lane);
+  fb.init(g.b, wave, lane);
+    // Past the last slab the copies bring zeros that nobody uses.
+    auto advance = [&]() __attribute__((always_inline)) {
+      fa.next();
+      fb.next();
+    };
+  // The first two slabs of a tile.
+  auto begin = [&](const Place& p) __attribute__((always_inline)) {
+    fa.start(g.a, p.a0, OA == kRow ? g.a.width - p.a0 : p.ra, p.k0, p.k1);
+    fb.start(g.b, p.b0, OB == kRow ? g.b.width - p.b0 : p.rb, p.k0, p.k1);
+    fa.copy(0, ab0, wave);
+    fb.copy(0, ab0 + HB, wave);
+    fb.copy(1, b01, wave);
+    fa.copy(1, a01, wave);
+    advance();
+    fa.copy(0, ab1, wave);
+    fb.copy(0, ab1 + HB, wave);
+    fb.copy(1, b11, wave);
+    fa.copy(1, a11, wave);
+    advance();
+  };
     Frags<OA, H, MI> pa;
     Frags<OB, H, MJ> pb;
     pa.init(wa, lane);
@@ -636,12 +722,6 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
     // step of A1, which are read while A0 is in use; and of the halves of B.
     constexpr int EARLY = MI == 4 ? 2 : 0;
     bf16x8 xa[MI][2], xe[EARLY + 1], xb[2][MJ][2];
-
-    // Past the last slab the copies bring zeros that nobody uses.
-    auto advance = [&]() __attribute__((always_inline)) {
-      fa.next();
-      fb.next();
-    };
     auto read_b = [&](bf16x8 (&x)[MJ][2], const char* buf) __attribute__((always_inline)) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
@@ -706,36 +786,47 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
       multiply(1, 0, b0);
     };
 
-    fa.copy(0, ab0, wave);
-    fb.copy(0, ab0 + HB, wave);
-    fb.copy(1, b01, wave);
-    fa.copy(1, a01, wave);
-    advance();
-    fa.copy(0, ab1, wave);
-    fb.copy(0, ab1 + HB, wave);
-    fb.copy(1, b11, wave);
-    fa.copy(1, a11, wave);
-    advance();
-    __builtin_amdgcn_s_waitcnt(0x0F78);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    read_b(xb[0], ab0 + HB);
+  if (at.slabs > 0) begin(at);
+  for (;;) {
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab0, i, 0);
-    if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
-    for (int s = 0; s + 1 < slabs; s += 2) {
-      slab(ab0, b01, a01, ab1, xb[0], xb[1]);
-      slab(ab1, b11, a11, ab0, xb[1], xb[0]);
+    for (int i = 0; i < 2 * MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * MJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (at.slabs > 0) {
+      __builtin_amdgcn_s_waitcnt(0x0F78);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      read_b(xb[0], ab0 + HB);
+#pragma unroll
+      for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab0, i, 0);
+      if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
+      for (int s = 0; s + 1 < at.slabs; s += 2) {
+        slab(ab0, b01, a01, ab1, xb[0], xb[1]);
+        slab(ab1, b11, a11, ab0, xb[1], xb[0]);
+      }
+      if (at.slabs & 1) slab(ab0, b01, a01, ab1, xb[0], xb[1]);
+      if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab have landed
     }
-    if (slabs & 1) slab(ab0, b01, a01, ab1, xb[0], xb[1]);
-    if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab land before the LDS is given back
+    // The next tile's copies are under way while this one is finished; what the
+    // finish has to load comes before them, since loads return in order.
+    int l = lane;
+    asm volatile("" : "+v"(l));  // computed here, not kept in registers through the products
+    const int r = l & 15, q = l >> 4;
+    auto a_of = [&](int i) { return i / MI * H + (wa * MI + i % MI) * 16 + 4 * q; };
+    auto b_of = [&](int j) { return j / MJ * H + (wb * MJ + j % MJ) * 16 + r; };
+    const auto per_b = load_per_b<EPI, 2 * MJ>(g, at.a0, at.b0, at.ra, at.rb, b_of);
+    const Place done = at;
+    slot += gridDim.x / 8;
+    const bool more = slot < end;
+    if (more) {
+      at = locate(first_id + slot);
+      if (at.slabs > 0) begin(at);
+    }
+    epilogue<__bf16, EPI, 2 * MI, 2 * MJ, 2 * H>(g, acc, per_b, done.a0, done.b0, done.ra, done.rb, done.ta,
+                                                 done.range, wa, q, a_of, b_of, red);
+    if (!more) break;
   }
-
-  epilogue<__bf16, EPI, 2 * MI, 2 * MJ, 2 * H>(
-      g, acc, a0, b0, ra, rb, ta, range, wa, q,
-      [&](int i) { return i / MI * H + (wa * MI + i % MI) * 16 + 4 * q; },
-      [&](int j) { return j / MJ * H + (wb * MJ + j % MJ) * 16 + r; }, red);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -1235,7 +1326,10 @@ template <typename E, Order OA, Order OB, Epilogue EPI>
 hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
   const int64_t ta = ceil_div(g.na, edge), tb = ceil_div(g.nb, edge);
   if constexpr (sizeof(E) == 2) {
-    const dim3 grid(static_cast<unsigned>(round_up(ta * tb * g.ranges, 8)));
+    // As many workgroups as the device holds at once (one or two a CU, by their
+    // LDS), in eighths; each takes every so manieth tile of its XCD's share.
+    const int64_t most = edge == 256 ? 256 : 512, n = round_up(ta * tb * g.ranges, 8);
+    const dim3 grid(static_cast<unsigned>(n < most ? n : most));
     if (edge == 256)
       hipLaunchKernelGGL((xent_tile_kernel<OA, OB, EPI, 128, 8>), grid, dim3(512), 0, s, g);
     else if (edge == 128)
