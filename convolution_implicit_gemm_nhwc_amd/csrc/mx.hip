@@ -364,12 +364,29 @@ __device__ inline void store1(char* p, float t) {
   }
 }
 
+// The bias of this lane's n[i] .. + 3.
+template <int NI>
+__device__ inline void load_bias(const MxArgs& a, const int (&n)[NI], bool whole, f32x4 (&bias)[NI]) {
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    bias[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!a.bias) continue;
+    if (whole) {
+      __builtin_memcpy(&bias[i], a.bias + n[i], 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n[i] + e < a.N) bias[i][e] = a.bias[n[i] + e];
+    }
+  }
+}
+
 // Bias, activation and store of this lane's part of a tile: n[i] .. + 3 of rows
 // m[j] (g = lane / 16; tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is asked once (`whole`): element by
 // element these questions took longer than the rest of the tile's end.
 template <bool BF16, int NI, int NJ>
 __device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
-                              int g, bool whole, int range) {
+                              const f32x4 (&bias)[NI], int g, bool whole, int range) {
   constexpr int ES = BF16 ? 2 : 4;
   if (a.part) {  // rows of ldp, a multiple of 4
 #pragma unroll
@@ -383,17 +400,6 @@ __device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (
     return;
   }
   if (a.bias) {
-    f32x4 bias[NI] = {};
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (whole) {
-        __builtin_memcpy(&bias[i], a.bias + n[i], 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n[i] + e < a.N) bias[i][e] = a.bias[n[i] + e];
-      }
-    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -440,6 +446,12 @@ __device__ inline f32x4 mma(i32x4 w, i32x4 x, f32x4 acc, int ws, int xs) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, acc, 4, 4, SEL, ws, SEL, xs);
 }
 
+// A wave's copy of 1 KiB into LDS, 16 bytes a lane from base + off (this lane's;
+// zeros past `bytes`).
+__device__ inline void copy_1k(const char* base, int64_t bytes, char* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_ptr_t)lds, 16, off, 0, 0, 0);
+}
+
 // Tiled product.  A workgroup owns a (2 H) n x (2 H) m tile in four quadrants;
 // NW waves share each quadrant, two along n, NW / 2 along m.  A slab is two k
 // tiles (256 columns) of both operands: four half tiles, copied buffer->LDS,
@@ -472,65 +484,87 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
 
   // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
   // tiles: eight tile rows of m together, so both panels stay in its L2.
+  // The workgroup stays for every so manieth tile of its XCD's share.
   const int tiles = a.tiles_m * a.tiles_n;
-  const int nb = gridDim.x;  // a multiple of 8
-  const int id = (blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8;
-  if (id >= tiles * a.ranges) return;
-  const int range = id / tiles, tile = id % tiles;
-  const int per = 8 * a.tiles_n;
-  const int m_first = tile / per * 8;
-  const int m_rows = min(8, a.tiles_m - m_first);
-  const int in = tile % per;
-  const int tm = m_first + in % m_rows, tn = in / m_rows;
+  const int total = tiles * a.ranges, share = (total + 7) / 8;
+  const int first_id = (blockIdx.x % 8) * share, end = min(share, total - first_id);
+  int slot = blockIdx.x / 8;
+  if (slot >= end) return;
+  const int64_t row_bytes = static_cast<int64_t>(a.kt) * kTileBytes;
+  const int64_t srow_bytes = static_cast<int64_t>(a.ks) * kScaleTile;
+  const int ks_per = (a.ks + a.ranges - 1) / a.ranges;
+  struct Place {
+    int range, ks0, kt0, kt1;  // this range's k tiles, whole scale tiles of them
+    int64_t rtw, rtx;
+  };
+  auto locate = [&](int id) __attribute__((always_inline)) {
+    Place p;
+    const int tile = id % tiles;
+    const int per = 8 * a.tiles_n;
+    const int m_first = tile / per * 8, m_rows = min(8, a.tiles_m - m_first), in = tile % per;
+    p.range = id / tiles;
+    p.rtw = static_cast<int64_t>(in / m_rows) * 2 * RT;
+    p.rtx = static_cast<int64_t>(m_first + in % m_rows) * 2 * RT;
+    p.ks0 = p.range * ks_per;
+    p.kt0 = min(4 * p.ks0, a.kt);
+    p.kt1 = min(p.kt0 + 4 * ks_per, a.kt);
+    return p;
+  };
+  Place at = locate(first_id + slot);
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave / (NW / 2), wb = wave % (NW / 2);
-  const int64_t rtw = static_cast<int64_t>(tn) * 2 * RT, rtx = static_cast<int64_t>(tm) * 2 * RT;
-  const int64_t row_bytes = static_cast<int64_t>(a.kt) * kTileBytes;
-  const int64_t srow_bytes = static_cast<int64_t>(a.ks) * kScaleTile;
-  const auto wr = make_rsrc(a.w.codes + rtw * row_bytes, (a.w.row_tiles - rtw) * row_bytes);
-  const auto xr = make_rsrc(a.x.codes + rtx * row_bytes, (a.x.row_tiles - rtx) * row_bytes);
   // A wave copies the scales of four row tiles, of W or of X.
   const bool swave = wave < NW / 2;
-  const auto sr = swave ? make_rsrc(a.w.scales + rtw * srow_bytes, (a.w.row_tiles - rtw) * srow_bytes)
-                        : make_rsrc(a.x.scales + rtx * srow_bytes, (a.x.row_tiles - rtx) * srow_bytes);
   const uint32_t s_off =
       static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
-  // This range's k tiles, whole scale tiles of them.
-  const int ks_per = (a.ks + a.ranges - 1) / a.ranges, ks0 = range * ks_per;
-  const int kt0 = min(4 * ks0, a.kt), kt1 = min(kt0 + 4 * ks_per, a.kt);
-  uint32_t off[2];  // of this wave's row tile in either half, at the next slab to copy
+  uint32_t first_off[2];  // of this wave's row tile in either half
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + static_cast<int64_t>(kt0) * kTileBytes + lane * 16);
-  int next_kt = kt0, next_ks = 0;  // next_ks counts from ks0
+  for (int h = 0; h < 2; ++h) first_off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + lane * 16);
+  // The next slab to copy: its offset, k tiles, and scale tile counted from the range's first.
+  uint32_t off;
+  int next_kt, next_ks;
 
   // Past the last k tile the copies bring zeros.
-  auto copy = [&](const __amdgpu_buffer_rsrc_t& rsrc, int h, char* buf) __attribute__((always_inline)) {
+  auto copy = [&](bool x, int h, char* buf) __attribute__((always_inline)) {
+    const MxView& v = x ? a.x : a.w;
+    const int64_t rt = x ? at.rtx : at.rtw;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (lds_ptr_t)(buf + (wave * 2 + c) * kTileBytes), 16,
-          next_kt + c < kt1 ? off[h] + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange, 0, 0, 0);
+      copy_1k(v.codes + rt * row_bytes, (v.row_tiles - rt) * row_bytes, buf + (wave * 2 + c) * kTileBytes,
+              next_kt + c < at.kt1 ? first_off[h] + off + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange);
   };
   auto advance = [&]() __attribute__((always_inline)) {
     next_kt += 2;
-    off[0] += 2 * kTileBytes;
-    off[1] += 2 * kTileBytes;
+    off += 2 * kTileBytes;
   };
   auto copy_scales = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        sr, (lds_ptr_t)(scales[next_ks & 1] + wave * 1024), 16,
-        ks0 + next_ks < a.ks ? s_off + static_cast<uint32_t>(ks0 + next_ks) * kScaleTile : kOutOfRange, 0, 0, 0);
+    const MxView& v = swave ? a.w : a.x;
+    const int64_t rt = swave ? at.rtw : at.rtx;
+    copy_1k(v.scales + rt * srow_bytes, (v.row_tiles - rt) * srow_bytes, scales[next_ks & 1] + wave * 1024,
+            at.ks0 + next_ks < a.ks ? s_off + static_cast<uint32_t>(at.ks0 + next_ks) * kScaleTile : kOutOfRange);
     ++next_ks;
   };
 
+  // The first two slabs of a tile, and the scales of both.
+  auto begin = [&]() __attribute__((always_inline)) {
+    next_kt = at.kt0;
+    next_ks = 0;
+    off = static_cast<uint32_t>(at.kt0) * kTileBytes;
+    copy_scales();
+    copy(false, 0, wx0);
+    copy(true, 0, wx0 + HB);
+    copy(true, 1, x10);
+    copy(false, 1, w10);
+    advance();
+    copy(false, 0, wx1);
+    copy(true, 0, wx1 + HB);
+    copy(true, 1, x11);
+    copy(false, 1, w11);
+    advance();
+  };
   f32x4 acc[2 * MJ][2 * MI];
-#pragma unroll
-  for (int i = 0; i < 2 * MI; ++i)
-#pragma unroll
-    for (int j = 0; j < 2 * MJ; ++j) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   int sw[2 * MI], sx[2 * MJ];
   // Fragments [tile][k tile] of a half of W, but for the first EARLY tiles' first
   // k tile of W1, which are read while W0 is in use; and of the halves of X.
@@ -604,13 +638,13 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     read_x(xb, x1);
 #pragma unroll
     for (int i = 0; i < EARLY; ++i) fe[i] = w_at(w1, i, 0);
-    copy(wr, 0, wx);
-    copy(xr, 0, wx + HB);
+    copy(false, 0, wx);
+    copy(true, 0, wx + HB);
     read_step_ends();
     multiply(0, 1, xb, sel);
 
     read_w_rest(w1);
-    copy(xr, 1, x1);
+    copy(true, 1, x1);
     __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F7B : 0x0F7A);  // vmcnt(11 or 10): the next slab's W0 and X0 are here
     read_step_ends();
     multiply(1, 1, xb, sel);
@@ -618,48 +652,59 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     read_x(xb, wx_next + HB);
 #pragma unroll
     for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx_next, i, 0);
-    copy(wr, 1, w1);
+    copy(false, 1, w1);
     advance();
     read_step_ends();
     multiply(1, 0, x0, sel);
   };
 
-  copy_scales();
-  copy(wr, 0, wx0);
-  copy(xr, 0, wx0 + HB);
-  copy(xr, 1, x10);
-  copy(wr, 1, w10);
-  advance();
-  copy(wr, 0, wx1);
-  copy(xr, 0, wx1 + HB);
-  copy(xr, 1, x11);
-  copy(wr, 1, w11);
-  advance();
-  __builtin_amdgcn_s_waitcnt(0x0F78);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  read_x(fx[0], wx0 + HB);
+  begin();
+  for (;;) {
 #pragma unroll
-  for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
-  if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
-  const int slabs = (kt1 - kt0 + 1) / 2;
-  for (int s = 0; s + 1 < slabs; s += 2) {
-    slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
-    slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
-  }
-  if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
-  if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab land before the LDS is given back
+    for (int j = 0; j < 2 * MJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 2 * MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __builtin_amdgcn_s_waitcnt(0x0F78);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_x(fx[0], wx0 + HB);
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
+    if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
+    const int slabs = (at.kt1 - at.kt0 + 1) / 2;
+    for (int s = 0; s + 1 < slabs; s += 2) {
+      slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+      slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
+    }
+    if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+    if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab have landed
 
-  const int g = lane >> 4, r = lane & 15;
-  int n[2 * MI];
-  int64_t m[2 * MJ];
+    // The next tile's copies are under way while this one is finished; the bias
+    // comes before them, since loads return in order.
+    int l = lane;
+    asm volatile("" : "+v"(l));  // places computed here, not kept in registers through the products
+    const int g = l >> 4, r = l & 15;
+    const Place done = at;
+    int n[2 * MI];
+    int64_t m[2 * MJ];
+    f32x4 bias[2 * MI];
 #pragma unroll
-  for (int i = 0; i < 2 * MI; ++i)
-    n[i] = static_cast<int>((rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
+    for (int i = 0; i < 2 * MI; ++i)
+      n[i] = static_cast<int>((done.rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
 #pragma unroll
-  for (int j = 0; j < 2 * MJ; ++j) m[j] = (rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
-  finish<BF16>(a, acc, n, m, g, (rtw + 2 * RT) * 16 <= a.N, range);
+    for (int j = 0; j < 2 * MJ; ++j) m[j] = (done.rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
+    const bool whole = (done.rtw + 2 * RT) * 16 <= a.N;
+    load_bias(a, n, whole, bias);
+    slot += gridDim.x / 8;
+    const bool more = slot < end;
+    if (more) {
+      at = locate(first_id + slot);
+      begin();
+    }
+    finish<BF16>(a, acc, n, m, bias, g, whole, done.range);
+    if (!more) break;
+  }
 }
 
 // Loads of 16 bytes that the compiler may keep in flight.
@@ -812,7 +857,9 @@ __global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
   }
   const int n[NT] = {static_cast<int>(nt0 * 16 + 4 * g), static_cast<int>(nt0 * 16 + 16 + 4 * g)};
   const int64_t m[1] = {wave * 16 + r};
-  finish<BF16>(a, out, n, m, g, nt0 * 16 + 32 <= a.N, range);
+  f32x4 bias[NT];
+  load_bias(a, n, nt0 * 16 + 32 <= a.N, bias);
+  finish<BF16>(a, out, n, m, bias, g, nt0 * 16 + 32 <= a.N, range);
 }
 
 // Many rows, few n: x is read once anyway, so it is quantised on its way into
@@ -898,7 +945,9 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxArgs a) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) n[t] = 16 * t + 4 * g;
   const int64_t m[1] = {row};
-  finish<BF16>(a, acc, n, m, g, NT * 16 <= a.N, 0);
+  f32x4 bias[NT];
+  load_bias(a, n, NT * 16 <= a.N, bias);
+  finish<BF16>(a, acc, n, m, bias, g, NT * 16 <= a.N, 0);
 }
 
 // y = act(sum of the ranges, in order, + bias); four n of a row per thread.
@@ -998,7 +1047,10 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
   const int64_t edge = kernel == kTile256 ? 256 : 128;
   a.tiles_m = static_cast<int32_t>(ceil_div(a.M, edge));
   a.tiles_n = static_cast<int32_t>(ceil_div(a.N, edge));
-  const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.ranges, 8) * 8));
+  // As many workgroups as the device holds at once (one or two a CU, by their LDS), in eighths.
+  const int64_t most = kernel == kTile256 ? 256 : 512;
+  const int64_t all = ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.ranges, 8) * 8;
+  const dim3 grid(static_cast<unsigned>(all < most ? all : most));
   const dim3 few(static_cast<unsigned>(ceil_div(a.N, 32) * a.ranges));
   const dim3 rows(static_cast<unsigned>(ceil_div(a.M, 64)));
   switch (kernel) {
