@@ -57,6 +57,7 @@ constexpr int64_t kMaxGroups = (1 << 23) - 8;
 constexpr int32_t kMaxK = 1 << 22;             // 256 rows of codes stay below 2^31 bytes
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t min_of(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // Codes and scales of one quantised matrix.
 struct MxView {
@@ -712,17 +713,16 @@ __device__ inline i32x4 load16(const char* p) { return *reinterpret_cast<const i
 
 // Few rows of x.  The time is W's way out of memory, so W goes straight into
 // registers, in the order in which it is stored: no LDS, no barrier before the
-// end.  A workgroup owns 32 n and one range of k; its four waves take turns at
+// end.  A workgroup owns 32 n and one range of k; its NW waves take turns at
 // the range's scale tiles (512 columns: 8 KiB of W, all loads in flight, the
 // next turn's while this one is multiplied) and add their sums in LDS, in
-// order.  Many workgroups hide what a wave waits; where n alone gives too few,
-// k is cut into ranges and mx_join_kernel adds them.
+// order.  Four waves, or eight where K is longer than a turn of those.
 // With RAW the workgroup quantises x itself, into LDS, before it starts: for
 // the few thousand values of one or two tokens that is quicker than a launch.
-template <bool BF16, int MT, bool RAW>
-__global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
+template <bool BF16, int MT, int NW, bool RAW>
+__global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   constexpr int NT = 2, ES = BF16 ? 2 : 4;
-  __shared__ f32x4 sums[4][NT * MT][64];
+  __shared__ f32x4 sums[NW][NT * MT][64];
   extern __shared__ __attribute__((aligned(16))) char raw_codes[];  // RAW: [k tile][block][M] of 16 bytes, then scales
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -786,7 +786,7 @@ __global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
     // Eight values a thread and step; the four lanes of a block agree on its
     // largest magnitude.
     const int per_row = ks_per * 64, total = per_row * rows;
-    for (int i = threadIdx.x; i < total; i += 256) {
+    for (int i = threadIdx.x; i < total; i += NW * 64) {
       const int row = i / per_row, e8 = i - row * per_row;
       const int64_t c = static_cast<int64_t>(ks0) * 512 + e8 * 8;
       float v[8];
@@ -834,12 +834,12 @@ __global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
     step(std::integral_constant<int, 2>{});
     step(std::integral_constant<int, 3>{});
   };
-  for (; ks < ks1; ks += 8) {
-    if (ks + 4 < ks1) load(next, ks + 4);
+  for (; ks < ks1; ks += 2 * NW) {
+    if (ks + NW < ks1) load(next, ks + NW);
     multiply(now, ks);
-    if (ks + 4 >= ks1) break;
-    if (ks + 8 < ks1) load(now, ks + 8);
-    multiply(next, ks + 4);
+    if (ks + NW >= ks1) break;
+    if (ks + 2 * NW < ks1) load(now, ks + 2 * NW);
+    multiply(next, ks + NW);
   }
 
 #pragma unroll
@@ -853,7 +853,7 @@ __global__ __launch_bounds__(256) void mx_few_kernel(MxArgs a) {
   for (int i = 0; i < NT; ++i) {
     out[0][i] = sums[0][wave * NT + i][lane];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) out[0][i] += sums[w][wave * NT + i][lane];
+    for (int w = 1; w < NW; ++w) out[0][i] += sums[w][wave * NT + i][lane];
   }
   const int n[NT] = {static_cast<int>(nt0 * 16 + 4 * g), static_cast<int>(nt0 * 16 + 16 + 4 * g)};
   const int64_t m[1] = {wave * 16 + r};
@@ -1001,17 +1001,18 @@ void choose_kernel(fconv_mx_plan_s* p) {
   p->ranges = 1;
   if (M <= 64) {
     p->kernel = kFew;
-    const int64_t groups = ceil_div(N, 32);
-    if (groups < 512) {
-      // Ranges until 768 workgroups, none shorter than one turn of its waves.
-      const int64_t want = ceil_div(768, groups), most = ceil_div(ks, 4);
-      const int64_t per = ceil_div(ks, want < most ? want : most);
-      p->ranges = static_cast<int32_t>(ceil_div(ks, per));
-    }
+    // Ranges only where a wave would take more than eight turns (K > 32768):
+    // 32 rows of 25088 -> 1024 take 11.8 us in one, 10.1 us in eight and the
+    // join, which does not cover its launch.
+    p->ranges = static_cast<int32_t>(min_of(ceil_div(ks, 64), ceil_div(1024, ceil_div(N, 32))));
+    p->ranges = static_cast<int32_t>(ceil_div(ks, ceil_div(ks, p->ranges)));
     if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384) p->kernel = kFewRaw;
     return;
   }
-  if (N <= 128 && M >= 4096) {
+  // W comes anew for every 16 rows there, so a long K costs more than writing
+  // the quantised x (us, against both kernels): 8192 x 64, K 1024 8.7 (15.7),
+  // 50000 x 100, K 2000 67 (64), 20480 x 128, K 4388 fp32 140 (97).
+  if (N <= 128 && M >= 4096 && p->d.K <= 1024) {
     p->kernel = kRows;
     return;
   }
@@ -1023,7 +1024,7 @@ void choose_kernel(fconv_mx_plan_s* p) {
     int64_t edge, at_once;
     double slab, slab_alone, tile;
   };
-  static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 8.0}, {kTile128, 128, 512, 1.0, 0.6, 5.0}};
+  static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 10.0}, {kTile128, 128, 512, 1.05, 0.7, 5.0}};
   double least = 1e300;
   for (const Kind& k : kinds) {
     const int64_t tiles = ceil_div(M, k.edge) * ceil_div(N, k.edge);
@@ -1032,7 +1033,7 @@ void choose_kernel(fconv_mx_plan_s* p) {
       if (ceil_div(ks, per) != r) continue;  // the same ranges as with fewer
       double us = static_cast<double>(ceil_div(tiles * r, k.at_once)) *
                   (2.0 * static_cast<double>(per) * (tiles * r > 256 ? k.slab : k.slab_alone) + k.tile);
-      if (r > 1) us += 3.0 + 8.0 * static_cast<double>(r * M) * static_cast<double>(N) / 4e6;
+      if (r > 1) us += 4.0 + 8.0 * static_cast<double>(r * M) * static_cast<double>(N) / 6e6;
       if (us < least) {
         least = us;
         p->kernel = k.kernel;
@@ -1057,15 +1058,24 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
     case kTile256: hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), grid, dim3(512), 0, s, a); break;
     case kTile128: hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), grid, dim3(256), 0, s, a); break;
     case kFewRaw:
-      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, true>), few, dim3(256), few_raw_bytes(p), s, a);
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, true>), few, dim3(256), few_raw_bytes(p), s, a);
       break;
     case kFew:
-      if (a.M <= 16)
-        hipLaunchKernelGGL((mx_few_kernel<BF16, 1, false>), few, dim3(256), 0, s, a);
-      else if (a.M <= 32)
-        hipLaunchKernelGGL((mx_few_kernel<BF16, 2, false>), few, dim3(256), 0, s, a);
-      else
-        hipLaunchKernelGGL((mx_few_kernel<BF16, 4, false>), few, dim3(256), 0, s, a);
+      if (ceil_div(a.ks, a.ranges) <= 4) {
+        if (a.M <= 16)
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, false>), few, dim3(256), 0, s, a);
+        else if (a.M <= 32)
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 4, false>), few, dim3(256), 0, s, a);
+        else
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 4, false>), few, dim3(256), 0, s, a);
+      } else {
+        if (a.M <= 16)
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 8, false>), few, dim3(512), 0, s, a);
+        else if (a.M <= 32)
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 8, false>), few, dim3(512), 0, s, a);
+        else
+          hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 8, false>), few, dim3(512), 0, s, a);
+      }
       break;
     case kRows:
       if (a.N <= 64)

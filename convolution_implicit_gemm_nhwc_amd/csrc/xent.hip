@@ -1299,7 +1299,7 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
     int64_t at_once;  // workgroups on the device
     double slab, slab_alone, tile;
   };
-  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.62, 0.45, 4.0}, {64, 1024, 1.1, 0.6, 3.0}};
+  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.1, 0.6, 3.0}};
   Split best = {64, 1};
   double least = 1e300;
   for (const Kind& k : kinds) {

@@ -133,7 +133,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 32), (1, 1000, 512), (2, 33, 129), (5, 1000, 1000
 # many rows of few outputs, and sums cut into ranges in the tiled kernels.
 PRODUCTS += [(1, 32, 16385), (3, 40, 5000), (4, 16400, 520), (16, 16399, 1030), (15, 33, 16000), (31, 70, 9000),
              (33, 50, 9001), (40, 4000, 1500), (49, 33, 2049), (64, 64, 25088), (65, 100, 9000), (300, 200, 20000),
-             (4096, 1, 33), (5000, 64, 256), (4099, 67, 700), (6000, 128, 1000), (4100, 17, 129)]
+             (4096, 1, 33), (5000, 64, 256), (4099, 67, 700), (6000, 128, 1000), (4100, 17, 129), (20, 40, 40000), (2, 33, 70001),
+             (4500, 100, 1500)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
