@@ -170,7 +170,7 @@ __device__ inline PerB<EPI, NJ> load_per_b(const GemmArgs& g, int64_t a0, int64_
   for (int j = 0; j < NJ; ++j) {
     const int64_t b = b0 + min(b_of(j), rb - 1);
     if constexpr (EPI == kEpiLse) {
-      const int64_t t = g.target[b] - a0;
+      const int64_t t = g.target[b] - g.v0 - a0;
       p.at[j] = t >= 0 && t < ra ? static_cast<int>(t) : -1;
     } else if constexpr (EPI == kEpiGrad) {
       const int t = g.live_target[b];
@@ -460,21 +460,20 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
 
   f32x4 acc[2][2] = {};
   const int slabs = k1 > k0 ? static_cast<int>(ceil_div(k1 - k0, G::SLAB)) : 0;
-  E va[32 / G::ES], vb[32 / G::ES];
-  if (slabs > 0) {
-    gen_load<E, OA>(g.a, a0, ra, k0, k1, va);
-    gen_load<E, OB>(g.b, b0, rb, k0, k1, vb);
-  }
-  for (int s = 0; s < slabs; ++s) {
-    char* ba = buf[s & 1][0];
-    char* bb = buf[s & 1][1];
-    gen_write<E, OA>(ba, va);
-    gen_write<E, OB>(bb, vb);
+  // Two slabs are on their way in registers while one is multiplied: with one,
+  // a workgroup alone on its CU waited for most of a slab's time.
+  E va[2][32 / G::ES], vb[2][32 / G::ES];
+  auto load = [&](int s) __attribute__((always_inline)) {
+    if (s >= slabs) return;
+    gen_load<E, OA>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, va[s & 1]);
+    gen_load<E, OB>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, vb[s & 1]);
+  };
+  auto step = [&](int s, char* ba, char* bb, const E(&xa)[32 / G::ES], const E(&xb)[32 / G::ES])
+                  __attribute__((always_inline)) {
+    gen_write<E, OA>(ba, xa);
+    gen_write<E, OB>(bb, xb);
     __syncthreads();
-    if (s + 1 < slabs) {
-      gen_load<E, OA>(g.a, a0, ra, k0 + (s + 1) * static_cast<int64_t>(G::SLAB), k1, va);
-      gen_load<E, OB>(g.b, b0, rb, k0 + (s + 1) * static_cast<int64_t>(G::SLAB), k1, vb);
-    }
+    load(s + 2);
 #pragma unroll
     for (int kk = 0; kk < G::SLAB; kk += 32) {
       Frag fa[2], fb[2];
@@ -488,6 +487,12 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mma8(fa[i], fb[j], acc[i][j]);
     }
+  };
+  load(0);
+  load(1);
+  for (int s = 0; s < slabs; s += 2) {
+    step(s, buf[0][0], buf[0][1], va[0], vb[0]);
+    if (s + 1 < slabs) step(s + 1, buf[1][0], buf[1][1], va[1], vb[1]);
   }
 
   auto b_of = [&](int j) { return wb * 32 + 16 * j + r; };
@@ -1215,6 +1220,36 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
   }
 }
 
+// Rows of bf16 from anywhere into rows of ld (a multiple of 8) from 16-byte
+// boundaries, zeros past cols.  Four pieces of 16 bytes per thread in flight.
+__global__ __launch_bounds__(256) void xent_pack_kernel(const char* src, int64_t ld_src, int64_t rows, int cols,
+                                                        char* dst, int64_t ld) {
+  const int per_row = static_cast<int>(ld / 8);
+  const int64_t total = rows * per_row, first = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x;
+  uint16_t v[4][8];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t i = first + 256 * u, row = i / per_row;
+    const int c = static_cast<int>(i - row * per_row) * 8;
+    if (i >= total) break;
+    const char* p = src + (row * ld_src + c) * 2;
+    if (c + 8 <= cols) {
+      __builtin_memcpy(v[u], p, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[u][e] = 0;
+        if (c + e < cols) __builtin_memcpy(&v[u][e], p + 2 * e, 2);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t i = first + 256 * u;
+    if (i < total) __builtin_memcpy(dst + i * 16, v[u], 16);
+  }
+}
+
 // C[row, a] = sum of the ranges' partial sums, in order; four a per thread.
 template <typename E>
 __global__ __launch_bounds__(256) void xent_sum_kernel(const float* part, int ranges, int64_t stride,
@@ -1267,6 +1302,7 @@ namespace {
 // the ranges of its sum.
 struct Split {
   int32_t edge, ranges;
+  double us;  // by choose()'s account
 };
 }  // namespace
 }  // namespace fconv
@@ -1276,6 +1312,12 @@ struct fconv_xent_plan_s {
   int32_t es;
   // Forward workspace: partial (max, sum) [tiles of V, at most][T], target logits [T].
   size_t fwd_target, fwd_bytes;
+  // bf16 rows that are no multiple of 16 bytes are packed for the tiled kernel
+  // where that is quicker than the general one: h, and w piece by piece.
+  bool pack_fwd, pack_bwd;
+  int32_t fwd_piece;  // rows of w packed at a time
+  int64_t ld_pack;
+  size_t fwd_h, fwd_w, o_w;
   fconv::Split logits, grad, dh, dw;  // dh and dw: of one piece
   // Backward workspace.
   int64_t ld_live;               // row stride of the gathered h
@@ -1299,9 +1341,8 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
     int64_t at_once;  // workgroups on the device
     double slab, slab_alone, tile;
   };
-  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.1, 0.6, 3.0}};
-  Split best = {64, 1};
-  double least = 1e300;
+  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.15, 0.95, 3.0}};
+  Split best = {64, 1, 1e300};
   for (const Kind& k : kinds) {
     if (k.edge != 64 && !tiled) continue;
     const int64_t tiles = ceil_div(na, k.edge) * ceil_div(nb, k.edge), slabs = ceil_div(nk, 64);
@@ -1310,14 +1351,14 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
       if (r > 1) us += 6.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
-      if (us < least) {
-        least = us;
-        best = Split{k.edge, r};
-      }
+      if (us < best.us) best = Split{k.edge, r, us};
     }
   }
   return best;
 }
+
+// Time (us) of packing a matrix: a launch, one read and one write.
+double pack_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 4e6; }
 
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
@@ -1347,6 +1388,13 @@ bool fits_tiles(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>
 constexpr int32_t kFewTokens = 64;
 // Workgroups of the few-token forward kernel.
 int64_t few_groups(int32_t V) { return ceil_div(V, 32) < 1024 ? ceil_div(V, 32) : 1024; }
+
+hipError_t launch_pack(const void* src, int64_t ld_src, int64_t rows, int32_t cols, char* dst, int64_t ld,
+                       hipStream_t s) {
+  hipLaunchKernelGGL(xent_pack_kernel, dim3(static_cast<unsigned>(ceil_div(rows * (ld / 8), 1024))), dim3(256), 0, s,
+                     static_cast<const char*>(src), ld_src, rows, cols, dst, ld);
+  return hipGetLastError();
+}
 
 FewArgs few_args(const fconv_xent_plan_s* p, const fconv_xent_args* args) {
   FewArgs f = {};
@@ -1392,17 +1440,36 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
     GemmArgs g = {};
     g.a = Operand{static_cast<const char*>(args->w), args->ldw};
     g.b = Operand{static_cast<const char*>(args->h), args->ldh};
-    g.na = d.V;
     g.nb = d.T;
     g.nk = d.D;
     g.ranges = 1;
-    g.out = ws;
     g.ld_out = d.T;
     g.target = args->target;
     g.target_logit = target_logit;
-    const int edge = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh) ? p->logits.edge : 64;
+    int edge = p->logits.edge;
+    if (p->pack_fwd) {
+      if ((e = launch_pack(args->h, args->ldh, d.T, d.D, ws + p->fwd_h, p->ld_pack, s)) != hipSuccess) return e;
+      g.b = Operand{ws + p->fwd_h, p->ld_pack};
+    } else if (!fits_tiles(args->w, args->ldw) || !fits_tiles(args->h, args->ldh)) {
+      edge = 64;
+    }
     tiles = static_cast<int>(ceil_div(d.V, edge));
-    e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
+    for (int32_t v0 = 0; v0 < d.V; v0 += p->fwd_piece) {
+      g.na = d.V - v0 < p->fwd_piece ? d.V - v0 : p->fwd_piece;
+      g.v0 = v0;
+      g.out = ws + static_cast<size_t>(v0 / edge) * d.T * 8;
+      if (p->pack_fwd) {
+        if ((e = launch_pack(g.a.p + v0 * args->ldw * 2, args->ldw, g.na, d.D, ws + p->fwd_w, p->ld_pack, s)) !=
+            hipSuccess)
+          return e;
+        GemmArgs piece = g;
+        piece.a = Operand{ws + p->fwd_w, p->ld_pack};
+        e = launch_gemm<E, kSum, kSum, kEpiLse>(piece, edge, s);
+      } else {
+        e = launch_gemm<E, kSum, kSum, kEpiLse>(g, edge, s);
+      }
+      if (e != hipSuccess) return e;
+    }
   }
   if (e != hipSuccess) return e;
   if (d.T <= 256)
@@ -1484,7 +1551,13 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     const int32_t v0 = i * p->piece;
     const int32_t nv = d.V - v0 < p->piece ? d.V - v0 : p->piece;
     const char* w = static_cast<const char*>(args->w) + v0 * args->ldw * p->es;
-    const bool w_fits = fits_tiles(w, args->ldw);
+    int64_t ldw = args->ldw;
+    if (p->pack_bwd) {
+      if ((e = launch_pack(w, ldw, nv, d.D, ws + p->o_w, p->ld_pack, s)) != hipSuccess) return e;
+      w = ws + p->o_w;
+      ldw = p->ld_pack;
+    }
+    const bool w_fits = fits_tiles(w, ldw);
     if (few) {
       FewArgs f = few_args(p, args);
       f.w = w;
@@ -1502,7 +1575,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       e = launch_few<E, kEpiGrad>(f, p->ld_g / 32, s);
     } else {
       GemmArgs g = {};
-      g.a = Operand{w, args->ldw};
+      g.a = Operand{w, ldw};
       g.b = Operand{ga.h_live, p->ld_live};
       g.na = nv;
       g.nb = d.T;
@@ -1523,7 +1596,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     const bool dh_whole = p->pieces * p->dh.ranges == 1;
     const int dh_edge = w_fits ? p->dh.edge : 64;
     GemmArgs h = {};
-    h.a = Operand{w, args->ldw, d.D};
+    h.a = Operand{w, ldw, p->pack_bwd ? ldw : d.D};
     h.b = Operand{ws + p->o_g, p->ld_g};
     h.na = d.D;
     h.nb = d.T;
@@ -1639,10 +1712,27 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
   if (!p) return FCONV_ERR_INVALID_ARG;
   p->d = d;
   p->es = d.dtype == FCONV_BF16 ? 2 : 4;
-  const bool tiled = d.dtype == FCONV_BF16 && d.D % 8 == 0;
+  const bool bf16 = d.dtype == FCONV_BF16, tiled = bf16 && d.D % 8 == 0;
+  p->ld_pack = round_up(d.D, 8);
   p->logits = choose(d.V, d.T, d.D, tiled, false);
+  p->fwd_piece = d.V;
+  if (bf16 && !tiled && d.T > kFewTokens) {
+    const Split packed = choose(d.V, d.T, d.D, true, false);
+    p->pack_fwd = packed.us + pack_us(d.V, d.D) + pack_us(d.T, d.D) < p->logits.us;
+    if (p->pack_fwd) {
+      p->logits = packed;
+      const int64_t piece = round_up(kGBytes / 2 / p->ld_pack, 256);
+      if (piece < d.V) p->fwd_piece = static_cast<int32_t>(piece);
+    }
+  }
   p->fwd_target = static_cast<size_t>(d.T <= kFewTokens ? few_groups(d.V) : ceil_div(d.V, 64)) * d.T * 8;
-  p->fwd_bytes = p->fwd_target + static_cast<size_t>(d.T) * 4;
+  p->fwd_h = (p->fwd_target + static_cast<size_t>(d.T) * 4 + 255) / 256 * 256;
+  p->fwd_w = p->fwd_h;
+  p->fwd_bytes = p->fwd_h;
+  if (p->pack_fwd) {
+    p->fwd_w += (static_cast<size_t>(d.T) * p->ld_pack * 2 + 255) / 256 * 256;
+    p->fwd_bytes = p->fwd_w + static_cast<size_t>(p->fwd_piece) * p->ld_pack * 2;
+  }
 
   if (d.T > 0) {
     const int64_t T = d.T;
@@ -1660,6 +1750,14 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->ld_g = round_up(piece, 64);
     p->grad = choose(piece, T, d.D, tiled, false);
     p->dh = choose(d.D, T, piece, tiled, true);
+    if (bf16 && !tiled && T > kFewTokens) {
+      const Split grad = choose(piece, T, d.D, true, false), dh = choose(d.D, T, piece, true, true);
+      p->pack_bwd = grad.us + dh.us + pack_us(piece, d.D) < p->grad.us + p->dh.us;
+      if (p->pack_bwd) {
+        p->grad = grad;
+        p->dh = dh;
+      }
+    }
     p->dw = choose(d.D, piece, T, d.dtype == FCONV_BF16, true);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -1678,6 +1776,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->o_c = take(4);
     p->o_blocks = take(ceil_div(T, 1024) * 8);
     p->o_rh = take(static_cast<size_t>(T) * p->ld_live * p->es);
+    p->o_w = take(p->pack_bwd ? static_cast<size_t>(piece) * p->ld_pack * 2 : 0);
     const size_t dh_parts = static_cast<size_t>(p->pieces) * p->dh.ranges;
     p->o_dh = take(dh_parts > 1 ? dh_parts * T * ld4 : 0);
     p->o_dw = take(p->dw.ranges > 1 ? static_cast<size_t>(p->dw.ranges) * piece * ld4 : 0);

@@ -96,6 +96,8 @@ SIZES = [(1, 1, 1), (1, 64, 500), (2, 8, 70), (3, 33, 17), (16, 100, 300), (17, 
          (700, 64, 600), (1500, 72, 520)]
 # At most 64 tokens, and the first number above; k of less than a step, whole steps, a ragged rest; many groups of v.
 SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576, 2000), (66, 576, 2000), (5, 40, 70001)]
+# Rows that are no multiple of 16 bytes, packed for the tiled kernel.
+SIZES += [(513, 1001, 3000), (700, 260, 5000), (1100, 513, 2500)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
