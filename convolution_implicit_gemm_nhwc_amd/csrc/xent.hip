@@ -463,17 +463,16 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
   // Two slabs are on their way in registers while one is multiplied: with one,
   // a workgroup alone on its CU waited for most of a slab's time.
   E va[2][32 / G::ES], vb[2][32 / G::ES];
-  auto load = [&](int s) __attribute__((always_inline)) {
+  auto load = [&](int s, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     if (s >= slabs) return;
-    gen_load<E, OA>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, va[s & 1]);
-    gen_load<E, OB>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, vb[s & 1]);
+    gen_load<E, OA>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, xa);
+    gen_load<E, OB>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, xb);
   };
-  auto step = [&](int s, char* ba, char* bb, const E(&xa)[32 / G::ES], const E(&xb)[32 / G::ES])
-                  __attribute__((always_inline)) {
+  auto step = [&](int s, char* ba, char* bb, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     gen_write<E, OA>(ba, xa);
     gen_write<E, OB>(bb, xb);
     __syncthreads();
-    load(s + 2);
+    load(s + 2, xa, xb);
 #pragma unroll
     for (int kk = 0; kk < G::SLAB; kk += 32) {
       Frag fa[2], fb[2];
@@ -488,8 +487,8 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
         for (int j = 0; j < 2; ++j) acc[i][j] = mma8(fa[i], fb[j], acc[i][j]);
     }
   };
-  load(0);
-  load(1);
+  load(0, va[0], vb[0]);
+  load(1, va[1], vb[1]);
   for (int s = 0; s < slabs; s += 2) {
     step(s, buf[0][0], buf[0][1], va[0], vb[0]);
     if (s + 1 < slabs) step(s + 1, buf[1][0], buf[1][1], va[1], vb[1]);
@@ -838,7 +837,8 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
 //
 // At most 64 tokens: the logits' time is w's way out of memory, so fragments
 // of both operands go straight into registers, from any address, without LDS
-// or barriers.  A workgroup owns 32 v and all tokens; its four waves take
+// or barriers.  A workgroup owns 32 v and up to 64 tokens (32 with ODD, whose
+// fragments take more registers); its four waves take
 // turns at steps of 128 bytes of k, the next turn's loads in flight, and add
 // their sums in LDS, in order; wave j then finishes tokens 16 j .. + 15.
 //
@@ -846,6 +846,64 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
 // of v and leaves them once.  Backward: nothing is gathered (three launches
 // less are worth more than the ignored tokens' share); ignored tokens get q = 0
 // and r h = 0, and the products' rows a sign: see row_map.
+// BYTES of elements from p on, in registers.  Loads of 16 bytes whose address is
+// no multiple of 4 took more than twice as long (61 tokens of 2895 x 7168: 52 us,
+// of 2894 and 2896: 25), so with ODD (some row of bf16 begins between dwords)
+// the dwords around the elements are loaded and shifted when they are used.
+// Every dword that is read holds one of the elements.
+template <int BYTES, bool ODD>
+struct Raw;
+
+template <int BYTES>
+struct Raw<BYTES, false> {
+  typedef uint32_t Words __attribute__((ext_vector_type(BYTES / 4)));
+  Words d;
+  static __device__ uint32_t shift_of(const char*) { return 0; }
+  __device__ void load(const char* p) { __builtin_memcpy(&d, p, BYTES); }
+  template <typename F>
+  __device__ F get(uint32_t) const {
+    return __builtin_bit_cast(F, d);
+  }
+  __device__ void set(const void* v, uint32_t) { __builtin_memcpy(&d, v, BYTES); }
+};
+
+template <int BYTES>
+struct Raw<BYTES, true> {
+  static constexpr int N = BYTES / 4;
+  uint32_t d[N + 1];
+  static __device__ uint32_t shift_of(const char* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8;
+  }
+  __device__ void load(const char* p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const char* q = reinterpret_cast<const char*>(at & ~static_cast<uintptr_t>(3));
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) __builtin_memcpy(&d[4 * i], __builtin_assume_aligned(q + 16 * i, 4), 16);
+    d[N] = reinterpret_cast<const uint32_t*>(q)[at & 2 ? N : 0];
+  }
+  // The elements, given shift_of their address.
+  template <typename F>
+  __device__ F get(uint32_t shift) const {
+    uint32_t v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], shift);
+    F f;
+    __builtin_memcpy(&f, v, BYTES);
+    return f;
+  }
+  // As if `v` had been loaded.
+  __device__ void set(const void* v, uint32_t shift) {
+    uint32_t u[N], below = 0;
+    __builtin_memcpy(u, v, BYTES);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      d[i] = shift ? u[i] << 16 | below >> 16 : u[i];
+      below = u[i];
+    }
+    d[N] = below >> 16;
+  }
+};
+
 struct FewArgs {
   const char* w;
   int64_t ldw;
@@ -870,7 +928,7 @@ struct FewArgs {
   float* c;
 };
 
-template <typename E, Epilogue EPI, int MT>
+template <typename E, bool ODD, Epilogue EPI, int MT>
 __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
   using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
   constexpr int ES = sizeof(E), NA = 2, STEP = 128 / ES, KK = STEP / 32;
@@ -879,14 +937,18 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int groups = (f.nv + 31) / 32;
+  // Tokens from t0 on; workgroups of the same v and other tokens follow on the same XCD (every eighth).
+  const int halves = (f.T + 16 * MT - 1) / (16 * MT);
+  const int t0 = static_cast<int>(blockIdx.x / 8 % halves) * 16 * MT;
+  const int block = blockIdx.x / (8 * halves) * 8 + blockIdx.x % 8, blocks = gridDim.x / halves;
   const int full = f.D / STEP;  // whole steps
 
   // Rows past T read the last one again; they are not stored.
   const char* hp[MT];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) hp[j] = f.h + (static_cast<int64_t>(min(16 * j + r, f.T - 1)) * f.ldh + 8 * q) * ES;
+  for (int j = 0; j < MT; ++j) hp[j] = f.h + (static_cast<int64_t>(min(t0 + 16 * j + r, f.T - 1)) * f.ldh + 8 * q) * ES;
   // This wave's tokens at the end.
-  const int t = 16 * wave + r;
+  const int t = t0 + 16 * wave + r;
   const bool mine = wave < MT && t < f.T;
   const int64_t tgt = mine ? f.target[t] : -1;
   const int64_t at_v = tgt - f.v0;  // the target's place in this piece
@@ -930,32 +992,44 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
     }
   }
 
-  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+  for (int grp = block; grp < groups; grp += blocks) {
     const char* wp[NA];
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       wp[i] = f.w + (static_cast<int64_t>(min(32 * grp + 16 * i + r, f.nv - 1)) * f.ldw + 8 * q) * ES;
     f32x4 acc[MT][NA] = {};
+    using R = Raw<8 * ES, ODD>;
     struct Turn {
-      Frag a[NA][KK], b[MT][KK];
+      R a[NA][KK], b[MT][KK];
     };
+    uint32_t sa[NA], sb[MT];  // steps are whole dwords: the same in all of them
+#pragma unroll
+    for (int i = 0; i < NA; ++i) sa[i] = R::shift_of(wp[i]);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) sb[j] = R::shift_of(hp[j]);
     auto load = [&](Turn& x, int step) __attribute__((always_inline)) {
       const int64_t at = static_cast<int64_t>(step) * 128;
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) __builtin_memcpy(&x.a[i][k], wp[i] + at + k * 32 * ES, 8 * ES);
+        for (int i = 0; i < NA; ++i) x.a[i][k].load(wp[i] + at + k * 32 * ES);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) __builtin_memcpy(&x.b[j][k], hp[j] + at + k * 32 * ES, 8 * ES);
+        for (int j = 0; j < MT; ++j) x.b[j][k].load(hp[j] + at + k * 32 * ES);
       }
     };
     auto multiply = [&](const Turn& x) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < KK; ++k)
+      for (int k = 0; k < KK; ++k) {
+        Frag a[NA], b[MT];
+#pragma unroll
+        for (int i = 0; i < NA; ++i) a[i] = x.a[i][k].template get<Frag>(sa[i]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) b[j] = x.b[j][k].template get<Frag>(sb[j]);
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
-          for (int i = 0; i < NA; ++i) acc[j][i] = mma8(x.a[i][k], x.b[j][k], acc[j][i]);
+          for (int i = 0; i < NA; ++i) acc[j][i] = mma8(a[i], b[j], acc[j][i]);
+      }
     };
     Turn now, next;
     int step = wave;
@@ -980,9 +1054,9 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
             v[e] = static_cast<E>(0.0f);
             if (e < n) __builtin_memcpy(&v[e], p + (at + e) * ES, ES);
           }
-          Frag g;
-          __builtin_memcpy(&g, v, 8 * ES);
-          return g;
+          R x;
+          x.set(v, R::shift_of(p));
+          return x;
         };
 #pragma unroll
         for (int i = 0; i < NA; ++i) x.a[i][k] = part(wp[i]);
@@ -1047,7 +1121,7 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
       const float m2 = __shfl_xor(run_m, x), s2 = __shfl_xor(run_s, x);
       join(run_m, run_s, m2, s2);
     }
-    if (q == 0 && mine) f.part[blockIdx.x * static_cast<int64_t>(f.T) + t] = make_float2(run_m, run_s);
+    if (q == 0 && mine) f.part[block * static_cast<int64_t>(f.T) + t] = make_float2(run_m, run_s);
   }
 }
 
@@ -1312,6 +1386,7 @@ struct fconv_xent_plan_s {
   int32_t es;
   // Forward workspace: partial (max, sum) [tiles of V, at most][T], target logits [T].
   size_t fwd_target, fwd_bytes;
+  bool few_fwd, few_bwd;  // at most kFewTokens, by their own kernel
   // bf16 rows that are no multiple of 16 bytes are packed for the tiled kernel
   // where that is quicker than the general one: h, and w piece by piece.
   bool pack_fwd, pack_bwd;
@@ -1357,6 +1432,15 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
   return best;
 }
 
+// Time (us) of the few-token kernel on a piece of the vocabulary: w at 4.1, 3.2
+// or 2.5 TB/s for 16, 32 or 64 tokens (4096 x 60000 and x 30000), where the tiled
+// kernel, with most of its products idle, reaches 5.2 (loss of 64 x 4096 x 30000
+// 95 us, of 65 48); but it has the small and narrow ones (64 x 2896 x 7168: 24,
+// 65: 36).
+double few_us(int64_t T, int64_t V, int64_t D) {
+  return 4.0 + 2.0 * static_cast<double>(V) * static_cast<double>(D) / (T <= 16 ? 4.1e6 : T <= 32 ? 3.2e6 : 2.5e6);
+}
+
 // Time (us) of packing a matrix: a launch, one read and one write.
 double pack_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 4e6; }
 
@@ -1387,7 +1471,10 @@ bool fits_tiles(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>
 
 constexpr int32_t kFewTokens = 64;
 // Workgroups of the few-token forward kernel.
-int64_t few_groups(int32_t V) { return ceil_div(V, 32) < 1024 ? ceil_div(V, 32) : 1024; }
+int64_t few_groups(int32_t V) { return ceil_div(V, 32) < 1024 ? round_up(ceil_div(V, 32), 8) : 1024; }
+
+// Whether rows of bf16 begin between dwords.
+bool odd_rows(const Operand& o) { return (reinterpret_cast<uintptr_t>(o.p) & 3) != 0 || o.ld % 2 != 0; }
 
 hipError_t launch_pack(const void* src, int64_t ld_src, int64_t rows, int32_t cols, char* dst, int64_t ld,
                        hipStream_t s) {
@@ -1410,16 +1497,25 @@ FewArgs few_args(const fconv_xent_plan_s* p, const fconv_xent_args* args) {
   return f;
 }
 
+// `groups` workgroups of v (a multiple of 8), for each 32 tokens with ODD.
+template <typename E, bool ODD, Epilogue EPI>
+hipError_t launch_few_of(const FewArgs& f, int64_t groups, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ODD ? groups * ceil_div(f.T, 32) : groups));
+  if (f.T <= 16) {
+    hipLaunchKernelGGL((xent_few_kernel<E, ODD, EPI, 1>), grid, dim3(256), 0, s, f);
+  } else if (ODD || f.T <= 32) {
+    hipLaunchKernelGGL((xent_few_kernel<E, ODD, EPI, 2>), grid, dim3(256), 0, s, f);
+  } else {
+    if constexpr (!ODD) hipLaunchKernelGGL((xent_few_kernel<E, ODD, EPI, 4>), grid, dim3(256), 0, s, f);
+  }
+  return hipGetLastError();
+}
 template <typename E, Epilogue EPI>
 hipError_t launch_few(const FewArgs& f, int64_t groups, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(groups));
-  if (f.T <= 16)
-    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 1>), grid, dim3(256), 0, s, f);
-  else if (f.T <= 32)
-    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 2>), grid, dim3(256), 0, s, f);
-  else
-    hipLaunchKernelGGL((xent_few_kernel<E, EPI, 4>), grid, dim3(256), 0, s, f);
-  return hipGetLastError();
+  if constexpr (sizeof(E) == 2) {
+    if (odd_rows(Operand{f.w, f.ldw}) || odd_rows(Operand{f.h, f.ldh})) return launch_few_of<E, true, EPI>(f, groups, s);
+  }
+  return launch_few_of<E, false, EPI>(f, groups, s);
 }
 
 template <typename E>
@@ -1430,7 +1526,8 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
   float* target_logit = reinterpret_cast<float*>(ws + p->fwd_target);
   int tiles;
   hipError_t e;
-  if (d.T <= kFewTokens) {
+  const bool fits = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh);
+  if (p->few_fwd || (d.T <= kFewTokens && !fits)) {
     FewArgs f = few_args(p, args);
     f.part = part;
     f.target_logit = target_logit;
@@ -1450,7 +1547,7 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
     if (p->pack_fwd) {
       if ((e = launch_pack(args->h, args->ldh, d.T, d.D, ws + p->fwd_h, p->ld_pack, s)) != hipSuccess) return e;
       g.b = Operand{ws + p->fwd_h, p->ld_pack};
-    } else if (!fits_tiles(args->w, args->ldw) || !fits_tiles(args->h, args->ldh)) {
+    } else if (!fits) {
       edge = 64;
     }
     tiles = static_cast<int>(ceil_div(d.V, edge));
@@ -1509,7 +1606,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
   float* c_max = reinterpret_cast<float*>(ws + p->o_c);
   int32_t* index = reinterpret_cast<int32_t*>(ws + p->o_index);
   int32_t* n_live = reinterpret_cast<int32_t*>(ws + p->o_n);
-  const bool few = d.T <= kFewTokens;
+  const bool few = p->few_bwd || (d.T <= kFewTokens && !p->pack_bwd && !fits_tiles(args->w, args->ldw));
   GatherArgs ga = {};
   if (few) {
     n_live = nullptr;
@@ -1572,7 +1669,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       f.row_map = index;
       f.live_dloss = live_dloss;
       f.c = c_max;
-      e = launch_few<E, kEpiGrad>(f, p->ld_g / 32, s);
+      e = launch_few<E, kEpiGrad>(f, round_up(ceil_div(nv, 32), 8), s);
     } else {
       GemmArgs g = {};
       g.a = Operand{w, ldw};
@@ -1725,7 +1822,11 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       if (piece < d.V) p->fwd_piece = static_cast<int32_t>(piece);
     }
   }
-  p->fwd_target = static_cast<size_t>(d.T <= kFewTokens ? few_groups(d.V) : ceil_div(d.V, 64)) * d.T * 8;
+  p->few_fwd = d.T <= kFewTokens && (!tiled || few_us(d.T, d.V, d.D) < p->logits.us);
+  // Either kernel may run: which one depends on the pointers too.
+  int64_t parts = ceil_div(d.V, 64);
+  if (d.T <= kFewTokens && parts < few_groups(d.V)) parts = few_groups(d.V);
+  p->fwd_target = static_cast<size_t>(parts) * d.T * 8;
   p->fwd_h = (p->fwd_target + static_cast<size_t>(d.T) * 4 + 255) / 256 * 256;
   p->fwd_w = p->fwd_h;
   p->fwd_bytes = p->fwd_h;
@@ -1759,6 +1860,8 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       }
     }
     p->dw = choose(d.D, piece, T, d.dtype == FCONV_BF16, true);
+    // The gather is a launch and some microseconds more.
+    p->few_bwd = T <= kFewTokens && (!tiled || few_us(d.T, piece, d.D) < p->grad.us + 8.0);
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t o = at;

@@ -95,7 +95,8 @@ SIZES = [(1, 1, 1), (1, 64, 500), (2, 8, 70), (3, 33, 17), (16, 100, 300), (17, 
          (64, 64, 64), (65, 130, 257), (130, 511, 129), (33, 8, 5000), (200, 96, 700), (300, 520, 1100),
          (700, 64, 600), (1500, 72, 520)]
 # At most 64 tokens, and the first number above; k of less than a step, whole steps, a ragged rest; many groups of v.
-SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576, 2000), (66, 576, 2000), (5, 40, 70001)]
+SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576, 2000), (66, 576, 2000), (5, 40, 70001),
+          (30, 64, 140000), (3, 1024, 70000)]
 # Rows that are no multiple of 16 bytes, packed for the tiled kernel.
 SIZES += [(513, 1001, 3000), (700, 260, 5000), (1100, 513, 2500)]
 
@@ -106,6 +107,20 @@ def test_loss_and_gradient(T, D, V, dtype):
     dev = device()
     say("xent", T, D, V, dtype)
     _check(*_case(T, D, V, dtype, T + D + V, dev), dtype)
+
+
+@pytest.mark.parametrize("T,D,V,hoff,woff", [(5, 64, 90, 1, 0), (40, 128, 200, 0, 1), (40, 130, 200, 1, 1), (64, 77, 70, 3, 2),
+                                           (90, 128, 200, 1, 0), (90, 65, 300, 0, 3), (90, 192, 130, 2, 1)])
+def test_rows_between_dwords(T, D, V, hoff, woff):
+    # bf16 rows that begin at any element, with an odd and an even distance, of both operands.
+    dev = device()
+    say("odd rows", T, D, V, hoff, woff)
+    for extra in (0, 1):
+        h, w, t, dl = _case(T, D, V, "bf16", 3, dev)
+        hb = torch.full((T, D + hoff + extra), float("nan"), dtype=torch.bfloat16, device=dev)
+        wb = torch.full((V, D + woff + extra), float("nan"), dtype=torch.bfloat16, device=dev)
+        hb[:, hoff:hoff + D], wb[:, woff:woff + D] = h, w
+        _check(hb[:, hoff:hoff + D], wb[:, woff:woff + D], t, dl, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
