@@ -90,14 +90,49 @@ __device__ inline uint16_t f32_to_bf16(float f) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));  // round to nearest even
 }
 
+// BYTES (a multiple of 16) from or to any address.  STREAM: they are not asked
+// for again soon and leave the caches to others.  What is larger than
+// kStreamBytes (the L2s together) goes that way where each access takes whole
+// 64-byte lines: 16384 x 4096 bf16 were quantised in 32 us instead of 43 and
+// written back in 25 instead of 38.  Smaller ones took up to 1 us more, fp32
+// (whose accesses take half lines) 45 us instead of 32.
+constexpr int64_t kStreamBytes = 32 << 20;
+bool streams(const void* p, int64_t ld, int64_t rows, int es) {
+  return es == 2 && rows * ld * es > kStreamBytes && (reinterpret_cast<uintptr_t>(p) & 63) == 0 && ld * es % 64 == 0;
+}
+template <bool STREAM, int BYTES>
+__device__ inline void load_any(const char* p, void* v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+  for (int i = 0; i < BYTES; i += 16) {
+    const u32x4* q = reinterpret_cast<const u32x4*>(p + i);
+    const u32x4 x = STREAM ? __builtin_nontemporal_load(q) : *q;
+    __builtin_memcpy(static_cast<char*>(v) + i, &x, 16);
+  }
+}
+template <bool STREAM, int BYTES>
+__device__ inline void store_any(char* p, const void* v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+  for (int i = 0; i < BYTES; i += 16) {
+    u32x4 x;
+    __builtin_memcpy(&x, static_cast<const char*>(v) + i, 16);
+    u32x4* q = reinterpret_cast<u32x4*>(p + i);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(x, q);
+    else
+      *q = x;
+  }
+}
+
 // Eight values of a row at column c, zeros past `cols` (n < 8 live ones at
 // the tail).  gfx950 reads global memory at any byte alignment.
-template <bool BF16>
+template <bool BF16, bool STREAM = false>
 __device__ inline void load8(const char* p, int n, float v[8]) {
   if constexpr (BF16) {
     if (n >= 8) {
       uint16_t h[8];
-      __builtin_memcpy(h, p, 16);
+      load_any<STREAM, 16>(p, h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = bf16_to_f32(h[i]);
     } else {
@@ -110,7 +145,7 @@ __device__ inline void load8(const char* p, int n, float v[8]) {
     }
   } else {
     if (n >= 8) {
-      __builtin_memcpy(v, p, 32);
+      load_any<STREAM, 32>(p, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -157,7 +192,7 @@ __device__ inline uint32_t quad_max(uint32_t m) {
 // time, four loads in flight per lane; the four lanes of a block agree on its
 // largest magnitude.  The scale bytes of the four k tiles meet in LDS so that
 // a lane's four bytes leave as one dword.
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const char* x, int64_t ldx_bytes,
                                                           int64_t rows, int cols, int kt_n, int ks_n,
                                                           char* codes, char* scales) {
@@ -173,7 +208,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const char* x, int64_t
   for (int i = 0; i < 4; ++i) {
     const int64_t r = rt * 16 + 4 * i + (lane >> 4);
     if (r < rows && c < cols) {
-      load8<BF16>(x + r * ldx_bytes + static_cast<int64_t>(c) * ES, cols - c, v[i]);
+      load8<BF16, STREAM>(x + r * ldx_bytes + static_cast<int64_t>(c) * ES, cols - c, v[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
@@ -201,7 +236,7 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const char* x, int64_t
 
 // The values that codes and scales stand for: the quantisation's work split
 // backwards, a lane writing 8 values.
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(const char* codes, const char* scales,
                                                             int64_t rows, int cols, int kt_n,
                                                             int ks_n, char* y, int64_t ldy_bytes) {
@@ -241,7 +276,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const char* codes, c
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = f32_to_bf16(v[j]);
       if (n >= 8) {
-        __builtin_memcpy(p, h, 16);
+        store_any<STREAM, 16>(p, h);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -249,7 +284,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const char* codes, c
       }
     } else {
       if (n >= 8) {
-        __builtin_memcpy(p, v, 32);
+        store_any<STREAM, 32>(p, v);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -708,8 +743,11 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   }
 }
 
-// Loads of 16 bytes that the compiler may keep in flight.
-__device__ inline i32x4 load16(const char* p) { return *reinterpret_cast<const i32x4*>(p); }
+template <bool STREAM = false>
+__device__ inline i32x4 load16(const char* p) {
+  const i32x4* q = reinterpret_cast<const i32x4*>(p);
+  return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
 
 // Few rows of x.  The time is W's way out of memory, so W goes straight into
 // registers, in the order in which it is stored: no LDS, no barrier before the
@@ -717,9 +755,12 @@ __device__ inline i32x4 load16(const char* p) { return *reinterpret_cast<const i
 // the range's scale tiles (512 columns: 8 KiB of W, all loads in flight, the
 // next turn's while this one is multiplied) and add their sums in LDS, in
 // order.  Four waves, or eight where K is longer than a turn of those.
+// With STREAM W leaves the caches to others (one row of 4096 -> 32768 12.5 us
+// instead of 13.7; but 32 rows of 25088 -> 1024, whose 13 MB stay in the caches
+// from call to call, 17.5 instead of 14.5: above kStreamBytes).
 // With RAW the workgroup quantises x itself, into LDS, before it starts: for
 // the few thousand values of one or two tokens that is quicker than a launch.
-template <bool BF16, int MT, int NW, bool RAW>
+template <bool BF16, int MT, int NW, bool RAW, bool STREAM>
 __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   constexpr int NT = 2, ES = BF16 ? 2 : 4;
   __shared__ f32x4 sums[NW][NT * MT][64];
@@ -762,7 +803,7 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
     for (int k = 0; k < 4; ++k) {
       const int64_t at = static_cast<int64_t>(min(4 * ks + k, a.kt - 1)) * kTileBytes;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) t.w[i][k] = load16(wc[i] + at);
+      for (int i = 0; i < NT; ++i) t.w[i][k] = load16<STREAM>(wc[i] + at);
       if constexpr (!RAW) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) t.x[i][k] = load16(xc[i] + at);
@@ -999,16 +1040,6 @@ int few_raw_bytes(const fconv_mx_plan_s* p) {
 void choose_kernel(fconv_mx_plan_s* p) {
   const int64_t M = p->d.M, N = p->d.N, ks = ceil_div(p->d.K, 512);
   p->ranges = 1;
-  if (M <= 64) {
-    p->kernel = kFew;
-    // Ranges only where a wave would take more than eight turns (K > 32768):
-    // 32 rows of 25088 -> 1024 take 11.8 us in one, 10.1 us in eight and the
-    // join, which does not cover its launch.
-    p->ranges = static_cast<int32_t>(min_of(ceil_div(ks, 64), ceil_div(1024, ceil_div(N, 32))));
-    p->ranges = static_cast<int32_t>(ceil_div(ks, ceil_div(ks, p->ranges)));
-    if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384) p->kernel = kFewRaw;
-    return;
-  }
   // W comes anew for every 16 rows there, so a long K costs more than writing
   // the quantised x (us, against both kernels): 8192 x 64, K 1024 8.7 (15.7),
   // 50000 x 100, K 2000 67 (64), 20480 x 128, K 4388 fp32 140 (97).
@@ -1026,6 +1057,22 @@ void choose_kernel(fconv_mx_plan_s* p) {
   };
   static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 10.0}, {kTile128, 128, 512, 1.05, 0.7, 5.0}};
   double least = 1e300;
+  if (M <= 64) {
+    p->kernel = kFew;
+    // Ranges only where a wave would take more than eight turns (K > 32768):
+    // 32 rows of 25088 -> 1024 take 11.8 us in one, 10.1 us in eight and the
+    // join, which does not cover its launch.
+    p->ranges = static_cast<int32_t>(min_of(ceil_div(ks, 64), ceil_div(1024, ceil_div(N, 32))));
+    p->ranges = static_cast<int32_t>(ceil_div(ks, ceil_div(ks, p->ranges)));
+    if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384) {
+      p->kernel = kFewRaw;
+      return;
+    }
+    // W at 5.2, 4.2 or 3 TB/s for 16, 32 or 64 rows (32768 x 4096: 13.7, 17.7 and
+    // 24.4 us, the 128 tiles 15.9, 16.3 and 16.9).
+    least = 2.0 + 0.53 * static_cast<double>(N) * static_cast<double>(p->d.K) / (M <= 16 ? 5.2e6 : M <= 32 ? 4.2e6 : 3.0e6);
+    if (p->ranges > 1) return;
+  }
   for (const Kind& k : kinds) {
     const int64_t tiles = ceil_div(M, k.edge) * ceil_div(N, k.edge);
     for (int64_t r = 1; r <= ks && r <= 32; ++r) {
@@ -1040,6 +1087,27 @@ void choose_kernel(fconv_mx_plan_s* p) {
         p->ranges = static_cast<int32_t>(r);
       }
     }
+  }
+}
+
+template <bool BF16, bool STREAM>
+void launch_few(const fconv_mx_plan_s* p, const MxArgs& a, bool raw, dim3 grid, hipStream_t s) {
+  if (raw)
+    hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, true, STREAM>), grid, dim3(256), few_raw_bytes(p), s, a);
+  else if (ceil_div(a.ks, a.ranges) <= 4) {
+    if (a.M <= 16)
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, false, STREAM>), grid, dim3(256), 0, s, a);
+    else if (a.M <= 32)
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 4, false, STREAM>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 4, false, STREAM>), grid, dim3(256), 0, s, a);
+  } else {
+    if (a.M <= 16)
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 8, false, STREAM>), grid, dim3(512), 0, s, a);
+    else if (a.M <= 32)
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 8, false, STREAM>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 8, false, STREAM>), grid, dim3(512), 0, s, a);
   }
 }
 
@@ -1058,24 +1126,11 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
     case kTile256: hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), grid, dim3(512), 0, s, a); break;
     case kTile128: hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), grid, dim3(256), 0, s, a); break;
     case kFewRaw:
-      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, true>), few, dim3(256), few_raw_bytes(p), s, a);
-      break;
     case kFew:
-      if (ceil_div(a.ks, a.ranges) <= 4) {
-        if (a.M <= 16)
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, false>), few, dim3(256), 0, s, a);
-        else if (a.M <= 32)
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 4, false>), few, dim3(256), 0, s, a);
-        else
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 4, false>), few, dim3(256), 0, s, a);
-      } else {
-        if (a.M <= 16)
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 8, false>), few, dim3(512), 0, s, a);
-        else if (a.M <= 32)
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 8, false>), few, dim3(512), 0, s, a);
-        else
-          hipLaunchKernelGGL((mx_few_kernel<BF16, 4, 8, false>), few, dim3(512), 0, s, a);
-      }
+      if (codes_bytes(a.N, a.K) > static_cast<size_t>(kStreamBytes))
+        launch_few<BF16, true>(p, a, kernel == kFewRaw, few, s);
+      else
+        launch_few<BF16, false>(p, a, kernel == kFewRaw, few, s);
       break;
     case kRows:
       if (a.N <= 64)
@@ -1121,12 +1176,12 @@ hipError_t launch_quantize(const void* x, int64_t ldx, int32_t rows, int32_t col
   char* codes = static_cast<char*>(mx);
   char* scales = codes + codes_bytes(rows, cols);
   const char* src = static_cast<const char*>(x);
-  if (dtype == FCONV_BF16)
-    hipLaunchKernelGGL(mx_quantize_kernel<true>, dim3(grid), dim3(256), 0, s, src, ldx * 2,
-                       static_cast<int64_t>(rows), cols, kt, ks, codes, scales);
-  else
-    hipLaunchKernelGGL(mx_quantize_kernel<false>, dim3(grid), dim3(256), 0, s, src, ldx * 4,
-                       static_cast<int64_t>(rows), cols, kt, ks, codes, scales);
+  const int es = dtype == FCONV_BF16 ? 2 : 4;
+  const auto kernel = es == 4                          ? mx_quantize_kernel<false, false>
+                      : streams(x, ldx, rows, es) ? mx_quantize_kernel<true, true>
+                                                  : mx_quantize_kernel<true, false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, src, ldx * es, static_cast<int64_t>(rows), cols, kt, ks,
+                     codes, scales);
   return hipGetLastError();
 }
 
@@ -1173,13 +1228,12 @@ fconv_status fconv_mx_dequantize(void* stream, const void* mx, int32_t rows, int
   const int kt = static_cast<int>(ceil_div(cols, 128)), ks = static_cast<int>(ceil_div(cols, 512));
   const unsigned grid = static_cast<unsigned>(ceil_div(rows, 16) * ks);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  char* dst = static_cast<char*>(y);
-  if (dtype == FCONV_BF16)
-    hipLaunchKernelGGL(mx_dequantize_kernel<true>, dim3(grid), dim3(256), 0, s, v.codes, v.scales,
-                       static_cast<int64_t>(rows), cols, kt, ks, dst, ldy * 2);
-  else
-    hipLaunchKernelGGL(mx_dequantize_kernel<false>, dim3(grid), dim3(256), 0, s, v.codes, v.scales,
-                       static_cast<int64_t>(rows), cols, kt, ks, dst, ldy * 4);
+  const int es = dtype == FCONV_BF16 ? 2 : 4;
+  const auto kernel = es == 4                          ? mx_dequantize_kernel<false, false>
+                      : streams(y, ldy, rows, es) ? mx_dequantize_kernel<true, true>
+                                                  : mx_dequantize_kernel<true, false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, v.codes, v.scales, static_cast<int64_t>(rows), cols, kt, ks,
+                     static_cast<char*>(y), ldy * es);
   return hipGetLastError() == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
 }
 

@@ -64,7 +64,9 @@ struct Operand {
   int64_t width;  // kRow: readable elements of a row
 };
 
-enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart };
+// kEpiStream: kEpiOut past the caches.
+enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart, kEpiStream };
+constexpr bool is_out(Epilogue e) { return e == kEpiOut || e == kEpiStream; }
 
 struct GemmArgs {
   Operand a, b;
@@ -123,7 +125,8 @@ __device__ inline void store4(char* p, f32x4 t, int live) {
 // The tiles of two matrix tiles side by side in bf16: t0 holds this lane's four
 // a of the first, t1 of the second.  Rows of 16 lanes exchange halves, so that
 // a lane ends with eight consecutive a and the 16 lanes of each b write 64
-// bytes at once: those of tile q % 2 from a = 8 (q / 2) on.
+// bytes at once: those of tile q % 2 from a = 8 (q / 2) on.  STREAM: past the caches.
+template <bool STREAM = false>
 __device__ inline void store_pair(char* p, f32x4 t0, f32x4 t1) {
   uint32_t v[4];
 #pragma unroll
@@ -134,7 +137,12 @@ __device__ inline void store_pair(char* p, f32x4 t0, f32x4 t1) {
     v[d] = s[0];
     v[2 + d] = s[1];
   }
-  __builtin_memcpy(p, v, 16);
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+  const u32x4 x = {v[0], v[1], v[2], v[3]};
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(p));
+  else
+    *reinterpret_cast<u32x4*>(p) = x;
 }
 __device__ inline int pair_at(int q) { return (q & 1) * 16 + (q >> 1) * 8; }
 
@@ -176,7 +184,7 @@ __device__ inline PerB<EPI, NJ> load_per_b(const GemmArgs& g, int64_t a0, int64_
       const int t = g.live_target[b];
       p.at[j] = static_cast<int>(t - g.v0 - a0);
       p.f[j] = t < 0 ? __builtin_nanf("") : g.lse[b];
-    } else if constexpr (EPI == kEpiOut) {
+    } else if constexpr (is_out(EPI)) {
       p.at[j] = g.row_map ? g.row_map[b] : static_cast<int>(b);
       p.f[j] = g.scale[b * g.scale_step];
     }
@@ -275,14 +283,14 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       }
     }
   } else {
-    using O = std::conditional_t<EPI == kEpiOut, E, float>;
+    using O = std::conditional_t<is_out(EPI), E, float>;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       if (b >= rb) continue;
       int64_t row = b0 + b;
       float scale = 1.0f;
-      if constexpr (EPI == kEpiOut) {
+      if constexpr (is_out(EPI)) {
         row = per.at[j];
         scale = per.f[j];
         if (row < 0) {
@@ -297,7 +305,8 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
         if constexpr (sizeof(O) == 2) {
 #pragma unroll
           for (int i = 0; i < NI; i += 2)
-            store_pair(out + (a_of(i) - 4 * q + pair_at(q)) * sizeof(O), acc[i][j] * scale, acc[i + 1][j] * scale);
+            store_pair<EPI == kEpiStream>(out + (a_of(i) - 4 * q + pair_at(q)) * sizeof(O), acc[i][j] * scale,
+                                          acc[i + 1][j] * scale);
         } else {
 #pragma unroll
           for (int i = 0; i < NI; ++i) store4<O>(out + a_of(i) * sizeof(O), acc[i][j] * scale, 4);
@@ -1462,7 +1471,7 @@ hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
     if (edge != 64) return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(ta), static_cast<unsigned>(tb), static_cast<unsigned>(g.ranges));
-  hipLaunchKernelGGL((xent_gen_kernel<E, OA, OB, EPI>), grid, dim3(256), 0, s, g);
+  hipLaunchKernelGGL((xent_gen_kernel<E, OA, OB, EPI == kEpiStream ? kEpiOut : EPI>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
 
@@ -1712,6 +1721,11 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       h.out = ws + p->o_dh + static_cast<size_t>(h.part_stride) * 4 * i * h.ranges;
     }
     const bool dw_whole = p->dw.ranges == 1;
+    // dw goes past the caches where it is larger than the L2s together and
+    // written in whole lines (64 x 4096 x 30000: both passes 237 us instead of
+    // 264; with rows of 2000 bytes, 1999 x 1000 x 32001, 485 instead of 474).
+    const bool past = p->es == 2 && static_cast<int64_t>(d.V) * d.D * 2 > (32 << 20) && d.D % 64 == 0 &&
+                      args->lddw % 64 == 0 && (reinterpret_cast<uintptr_t>(args->dw) & 127) == 0;
     char* dw = static_cast<char*>(args->dw) + (args->dw ? v0 * args->lddw * p->es : 0);
     GemmArgs c = {};
     c.a = Operand{ws + p->o_rh, p->ld_live, p->ld_live};
@@ -1743,7 +1757,8 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
         e = dh_whole ? launch_gemm<E, kRow, kSum, kEpiOut>(h, dh_edge, s)
                      : launch_gemm<E, kRow, kSum, kEpiPart>(h, dh_edge, s);
       if (e == hipSuccess && args->dw)
-        e = dw_whole ? launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s)
+        e = dw_whole ? past ? launch_gemm<E, kRow, kRow, kEpiStream>(c, p->dw.edge, s)
+                            : launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s)
                      : launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
     }
     if (e == hipSuccess && args->dh && !dh_whole && i == p->pieces - 1)
