@@ -150,6 +150,11 @@ __device__ inline int pair_at(int q) { return (q & 1) * 16 + (q >> 1) * 8; }
 // infinite (inf - inf would be NaN; exp(inf) = inf and exp(-inf) = 0 are right).
 __device__ inline float base_of(float m) { return __builtin_fabsf(m) < __builtin_inff() ? m : 0.0f; }
 __device__ inline float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// exp(x - base), given base * log2 e: one operation less of every logit.  The
+// rounding of base * log2 e is at most one of base itself, as lse's own.
+__device__ inline float exp_from(float x, float base2) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -base2));
+}
 
 // (m, s) of two sets of logits joined; s counts from base_of(m).
 __device__ inline void join(float& m, float& s, float m2, float s2) {
@@ -224,11 +229,11 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
-      const float base = base_of(m);
+      const float base2 = base_of(m) * kLog2e;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += exp_of(acc[i][j][e] - base);
+        for (int e = 0; e < 4; ++e) s += exp_from(acc[i][j][e], base2);
 #pragma unroll
       for (int x = 16; x < 64; x *= 2) {
         const float m2 = __shfl_xor(m, x), s2 = __shfl_xor(s, x);
@@ -249,12 +254,12 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       const int b = b_of(j);
       if (b >= rb) continue;
       const int at = per.at[j];
-      const float lse = per.f[j];
+      const float lse2 = per.f[j] * kLog2e;
       char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_of(acc[i][j][e] - lse);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = exp_from(acc[i][j][e], lse2);
       if (at >= 0 && at < ra) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
@@ -1230,8 +1235,7 @@ __global__ __launch_bounds__(256) void xent_count_kernel(const int64_t* target, 
 }
 
 // Gathers the live tokens among 16, in order: a workgroup counts the live
-// ones before its own and finds the largest |dloss|, then each wave copies the
-// rows of four tokens.
+// ones before its own and finds the largest |dloss|, then copies the rows.
 template <typename E>
 __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16;
@@ -1257,6 +1261,9 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t mine = t0 + lane;
   const int64_t tgt = lane < 16 && mine < g.T ? g.target[mine] : g.ignore;
+  __shared__ float ratios[16];
+  if (wave == 0 && tgt != g.ignore) ratios[lane] = c > 0.0f ? g.dloss[mine] / c : g.dloss[mine];
+  __syncthreads();
   const uint64_t live = __ballot(tgt != g.ignore);
   const int pos = before + __popcll(live & ((1ull << lane) - 1));
   if (wave == 0 && tgt != g.ignore) {
@@ -1269,36 +1276,48 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
     *g.n_live = before + __popcll(live);
     *g.c = c;
   }
-  constexpr int N = 16 / sizeof(E);
-  for (int i = 4 * wave; i < 4 * wave + 4; ++i) {
-    if (t0 + i >= g.T) break;
-    if (live >> i & 1) {
-      const int64_t to = before + __popcll(live & ((1ull << i) - 1));
-      const char* src = g.h + (t0 + i) * g.ldh * static_cast<int64_t>(sizeof(E));
-      const int64_t at = to * g.ld_live * static_cast<int64_t>(sizeof(E));
-      const float ratio = c > 0.0f ? g.dloss[t0 + i] / c : g.dloss[t0 + i];
-      for (int col = lane * N; col < g.ld_live; col += 64 * N) {
-        E v[N];
-        if (col + N <= g.D) {
-          __builtin_memcpy(v, src + col * sizeof(E), 16);
-        } else {
+  // The rows' pieces of 16 bytes, four of a thread in flight.
+  constexpr int N = 16 / sizeof(E), U = 4;
+  const int rows = static_cast<int>(g.T - t0 < 16 ? g.T - t0 : 16);
+  const int per_row = static_cast<int>(g.ld_live / N), total = rows * per_row;
+  for (int first = threadIdx.x; first < total; first += 256 * U) {
+    E v[U][N];
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            v[j] = static_cast<E>(0.0f);
-            if (col + j < g.D) __builtin_memcpy(&v[j], src + (col + j) * sizeof(E), sizeof(E));
-          }
-        }
-        __builtin_memcpy(g.h_live + at + col * sizeof(E), v, 16);
-        if (g.rh_live) {
+    for (int u = 0; u < U; ++u) {
+      const int i = first + 256 * u, row = i / per_row, col = (i - row * per_row) * N;
+      if (i >= total || !(live >> row & 1)) continue;
+      const char* src = g.h + ((t0 + row) * g.ldh + col) * static_cast<int64_t>(sizeof(E));
+      if (col + N <= g.D) {
+        __builtin_memcpy(v[u], src, 16);
+      } else {
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = static_cast<E>(ratio * static_cast<float>(v[j]));
-          __builtin_memcpy(g.rh_live + at + col * sizeof(E), v, 16);
+        for (int j = 0; j < N; ++j) {
+          v[u][j] = static_cast<E>(0.0f);
+          if (col + j < g.D) __builtin_memcpy(&v[u][j], src + j * sizeof(E), sizeof(E));
         }
       }
-    } else if (g.dh) {
-      char* dst = g.dh + (t0 + i) * g.lddh * static_cast<int64_t>(sizeof(E));
-      const E z = static_cast<E>(0.0f);
-      for (int c = lane; c < g.D; c += 64) __builtin_memcpy(dst + c * sizeof(E), &z, sizeof(E));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = first + 256 * u, row = i / per_row, col = (i - row * per_row) * N;
+      if (i >= total) continue;
+      if (live >> row & 1) {
+        const int64_t to = before + __popcll(live & ((1ull << row) - 1));
+        const int64_t at = (to * g.ld_live + col) * static_cast<int64_t>(sizeof(E));
+        __builtin_memcpy(g.h_live + at, v[u], 16);
+        if (g.rh_live) {
+          const float ratio = ratios[row];
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[u][j] = static_cast<E>(ratio * static_cast<float>(v[u][j]));
+          __builtin_memcpy(g.rh_live + at, v[u], 16);
+        }
+      } else if (g.dh) {
+        char* dst = g.dh + ((t0 + row) * g.lddh + col) * static_cast<int64_t>(sizeof(E));
+        const E z = static_cast<E>(0.0f);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (col + j < g.D) __builtin_memcpy(dst + j * sizeof(E), &z, sizeof(E));
+      }
     }
   }
 }
@@ -1413,7 +1432,10 @@ struct fconv_xent_plan_s {
 namespace fconv {
 namespace {
 
-constexpr int64_t kGBytes = 256 << 20;  // of g at a time: it stays in the 256 MB last-level cache
+// Of q at a time.  Fewer pieces mean fewer partial sums of dh; it is far from
+// the caches' size either way (8192 x 512 x 65536, both passes: 128 MB 2355 us,
+// 256 MB 2192, 512 MB 2077, 1 GB 2043).
+constexpr int64_t kGBytes = 512ll << 20;
 
 // The division of a product that takes the least time by a rough account (us):
 // workgroups take turns on the device, each turn as long as its slabs of 64 k
@@ -1833,7 +1855,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->pack_fwd = packed.us + pack_us(d.V, d.D) + pack_us(d.T, d.D) < p->logits.us;
     if (p->pack_fwd) {
       p->logits = packed;
-      const int64_t piece = round_up(kGBytes / 2 / p->ld_pack, 256);
+      const int64_t piece = round_up((128 << 20) / p->ld_pack, 256);
       if (piece < d.V) p->fwd_piece = static_cast<int32_t>(piece);
     }
   }
