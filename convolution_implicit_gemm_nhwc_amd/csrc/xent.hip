@@ -1447,7 +1447,7 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
     int64_t at_once;  // workgroups on the device
     double slab, slab_alone, tile;
   };
-  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.15, 0.95, 3.0}};
+  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.15, 0.7, 2.5}};
   Split best = {64, 1, 1e300};
   for (const Kind& k : kinds) {
     if (k.edge != 64 && !tiled) continue;
@@ -1897,6 +1897,13 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       }
     }
     p->dw = choose(d.D, piece, T, d.dtype == FCONV_BF16, true);
+    // Both gradients in general tiles take one launch, in which they overlap.
+    const Split dh64 = choose(d.D, T, piece, false, true), dw64 = choose(d.D, piece, T, false, false);
+    const double longer = dh64.us > dw64.us ? dh64.us : dw64.us, other = dh64.us + dw64.us - longer;
+    if (!p->pack_bwd && longer + 0.5 * other < p->dh.us + p->dw.us + 4.0) {
+      p->dh = dh64;
+      p->dw = dw64;
+    }
     // The gather is a launch and some microseconds more.
     p->few_bwd = T <= kFewTokens && (!tiled || few_us(d.T, piece, d.D) < p->grad.us + 8.0);
     size_t at = 0;
