@@ -156,6 +156,18 @@ __device__ inline float exp_from(float x, float base2) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -base2));
 }
 
+// base * log2 e for exp_from.  Past 2^126 the product would leave fp32: there
+// the base is taken off the logits first, and what is left counts from 0.
+template <int NI, int NJ>
+__device__ inline float base2_of(f32x4 (&z)[NI][NJ], int j, float base) {
+  if (__builtin_fabsf(base) >= 0x1p126f) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) z[i][j] -= base;
+    base = 0.0f;
+  }
+  return base * kLog2e;
+}
+
 // (m, s) of two sets of logits joined; s counts from base_of(m).
 __device__ inline void join(float& m, float& s, float m2, float s2) {
   const float mm = fmaxf(m, m2), b = base_of(mm);
@@ -229,7 +241,7 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
-      const float base2 = base_of(m) * kLog2e;
+      const float base2 = base2_of(acc, j, base_of(m));
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -254,7 +266,7 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       const int b = b_of(j);
       if (b >= rb) continue;
       const int at = per.at[j];
-      const float lse2 = per.f[j] * kLog2e;
+      const float lse2 = base2_of(acc, j, per.f[j]);
       char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
 #pragma unroll
       for (int i = 0; i < NI; ++i)

@@ -372,3 +372,47 @@ def test_same_bits_on_every_run_streams_and_graphs(T, D, V):
         torch.cuda.synchronize()
         assert torch.equal(l2, loss) and torch.equal(s2, lse) and torch.equal(a2, dh) and torch.equal(b2, dw)
         plan.forward(h, w, t)
+
+
+def _far(T, D, V, dtype, value, seed, dev):
+    """Logits near the end of fp32's range: every row of w has `value` in
+    column 0, times h's 1 there, but for V / 3 rows that have half of it; the
+    other columns' products are lost beside it."""
+    h, w, t, dl = _case(T, D, V, dtype, seed, dev)
+    h[:, 0] = 1.0
+    w[:, 0] = value
+    w[: V // 3, 0] = value / 2
+    return h, w, t, dl
+
+
+@pytest.mark.parametrize("value", [3.0e38, -3.0e38])
+@pytest.mark.parametrize("T,D,V", [(4, 40, 90), (100, 64, 300), (300, 128, 700)])
+def test_logits_near_the_end_of_the_range(T, D, V, value):
+    # All logits are one of two far values, exactly (fp32 loses the rest): the softmax is even over the larger ones.
+    dev = device()
+    for dtype in ("bf16", "fp32"):
+        say("far logits", T, D, V, value, dtype)
+        h, w, t, dl = _far(T, D, V, dtype, value, 3, dev)
+        top = torch.arange(V, device=dev) >= V // 3
+        if value < 0:
+            top = ~top
+        t = torch.where(t == IGN, t, torch.nonzero(top)[t % int(top.sum())].squeeze(1))
+        plan = fc.XentPlan(T, D, V, dtype, ignore_index=IGN)
+        loss, lse = plan.forward(h, w, t)
+        big = w[top][0, 0].float()
+        assert (lse == big).all()  # the logarithm of a count is far below a step
+        assert (loss == 0).all()
+        dh, dw = plan.backward(h, w, t, lse, dl)
+        # exp(z - lse) is 1 for the larger logits, which fp32 cannot tell from lse, 0 for the others.
+        live = t != IGN
+        q = top.double().repeat(T, 1)
+        q[live, t[live]] -= 1
+        q *= torch.where(live, dl.double(), 0).unsqueeze(1)
+        rdw = torch.mm(q.t(), h.double())
+        adw = torch.mm(q.abs().t(), h.double().abs())
+        r = 2.0 ** -8 if dtype == "bf16" else 4 * U
+        assert ((dw.double() - rdw).abs() <= 1.01 * r * (adw + rdw.abs()) + 4 * U * T * adw).all()
+        rdh = torch.mm(q[:, :], w.double())
+        adh = torch.mm(q.abs(), w.double().abs())
+        # Sums past fp32's range are infinities; the other columns are of order one.
+        assert ((dh.double() - rdh).abs()[:, 1:] <= (1.01 * r * (adh + rdh.abs()) + 4 * U * V * adh)[:, 1:]).all()
