@@ -214,3 +214,30 @@ def xent_lib():
             getattr(L, name).restype = st
         _xent_lib = L
     return _xent_lib
+
+
+# --- csrc/call.cpp: the short way through a call --------------------------
+
+_call = None
+
+
+def native():
+    """The module _call.so, built beside the library."""
+    global _call
+    if _call is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are what the module is linked to)
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_call.so")
+        if not os.path.exists(path):
+            raise LibraryMissing("%s not built: python -m convolution_implicit_gemm_nhwc_amd.build" % path)
+        loader = importlib.machinery.ExtensionFileLoader("_call", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_call", loader))
+        loader.exec_module(module)
+        _call = module
+    return _call
+
+
+def address(fn) -> int:
+    """Of a function of the library."""
+    return ctypes.cast(fn, ctypes.c_void_p).value

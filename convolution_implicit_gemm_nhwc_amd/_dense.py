@@ -1,9 +1,12 @@
 """What the bindings of the dense operators share: checks of 2-D tensors, and
-where a call's stream, output and workspace come from.  A call of the smallest
-sizes takes longer here than on the GPU, so the common way through is short."""
+where a call's stream, output and workspace come from.  The common way through a
+call is csrc/call.cpp's; here is the full one, which it leaves to this module
+for another stream or device and for arguments that do not fit."""
 from __future__ import annotations
 
 import torch
+
+from . import _check
 
 TORCH = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
@@ -45,6 +48,8 @@ def vector(t, what, numel, dtype):
 def same_device(first, *others):
     """The device of all of them (None: not given)."""
     at = first.get_device()
+    if at < 0:
+        raise ValueError("tensors must live on the GPU (got %s)" % first.device)
     for t in others:
         if t is not None and t.get_device() != at:
             raise ValueError("tensors on different devices (%s and %s)" % (first.device, t.device))
@@ -95,3 +100,10 @@ def call(run, stream, *tensors):
             return run(handle, device)
     with Launch(device, stream, tensors) as handle:
         return run(handle, device)
+
+
+def done(result, what):
+    """What csrc/call.cpp's way has returned, unless it is a status."""
+    if type(result) is int:
+        _check(result, what)
+    return result

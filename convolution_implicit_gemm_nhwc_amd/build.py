@@ -1,4 +1,5 @@
-"""Build libfconv.so (the C-ABI library with its gfx950 kernels) in-tree.
+"""Build libfconv.so (the C-ABI library with its gfx950 kernels) and _call.so
+(the Python module of csrc/call.cpp) in-tree.
 
     python -m convolution_implicit_gemm_nhwc_amd.build
 
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfconv.so")
+CALL = os.path.join(PKG, "_call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -53,7 +55,29 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     for obj in objs:
         os.remove(obj)
+    build_call(verbose)
     return LIB
+
+
+def build_call(verbose: bool = False) -> str:
+    """The Python module of csrc/call.cpp, against the installed torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = CALL + ".tmp%d" % os.getpid()
+    libs = os.path.join(root, "lib")
+    cmd = [HIPCC, "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", "-shared",
+           "-no-hip-rt", "-DUSE_ROCM", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "call.cpp"), "-o", tmp,
+           "-L" + libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALL)
+    return CALL
 
 
 if __name__ == "__main__":

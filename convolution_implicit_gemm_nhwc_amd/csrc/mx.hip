@@ -1057,7 +1057,7 @@ void choose_kernel(fconv_mx_plan_s* p) {
   };
   static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 10.0}, {kTile128, 128, 512, 1.05, 0.7, 5.0}};
   double least = 1e300;
-  if (M <= 64) {
+  if (M <= 64 && ceil_div(N, 32) <= kMaxGroups) {
     p->kernel = kFew;
     // Ranges only where a wave would take more than eight turns (K > 32768):
     // 32 rows of 25088 -> 1024 take 11.8 us in one, 10.1 us in eight and the
@@ -1160,8 +1160,11 @@ size_t span(int64_t rows, int64_t cols, int64_t ld, int es) {
   return rows <= 0 ? 0 : static_cast<size_t>((rows - 1) * ld + cols) * es;
 }
 
+// Rows of `cols` elements fit into the stride, and the strided matrix into the address space.
+bool bad_ld(int64_t ld, int64_t rows, int64_t cols) { return ld < cols || ld > INT64_MAX / 8 / (rows < 1 ? 1 : rows); }
+
 fconv_status check_matrix(const void* x, int64_t ld, int32_t rows, int32_t cols, int32_t dtype) {
-  if (rows < 0 || cols < 1 || ld < cols) return FCONV_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 1 || bad_ld(ld, rows, cols)) return FCONV_ERR_INVALID_ARG;
   if (dtype != FCONV_BF16 && dtype != FCONV_FP32) return FCONV_ERR_UNSUPPORTED;
   if (cols > kMaxK || ceil_div(rows, 16) * ceil_div(cols, 512) > kMaxGroups) return FCONV_ERR_UNSUPPORTED;
   if (!x && rows > 0) return FCONV_ERR_INVALID_ARG;
@@ -1313,7 +1316,7 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   if (d.M == 0) return FCONV_OK;
   if ((args->x != nullptr) == (args->x_mx != nullptr)) return FCONV_ERR_INVALID_ARG;
   if (!args->w_mx || !args->y || (p->op_bias && !args->bias)) return FCONV_ERR_INVALID_ARG;
-  if ((args->x && args->ldx < d.K) || args->ldy < d.N) return FCONV_ERR_INVALID_ARG;
+  if ((args->x && bad_ld(args->ldx, d.M, d.K)) || bad_ld(args->ldy, d.M, d.N)) return FCONV_ERR_INVALID_ARG;
   // An x that comes quantised needs no place in the workspace.
   int kernel = p->kernel;
   const bool by_itself = args->x && (kernel == kFewRaw || kernel == kRows);

@@ -17,8 +17,8 @@ import ctypes
 import torch
 
 from . import _abi
-from . import _check, DTYPES, OPS
-from ._dense import TORCH, call, matrix, vector
+from . import DTYPES, OPS, _check
+from ._dense import TORCH, call, done, matrix, vector
 
 __all__ = ["MxTensor", "MxQuantPlan", "MxPlan"]
 
@@ -83,10 +83,18 @@ class MxQuantPlan:
             raise ValueError("dtype %r: bf16 or fp32" % (dtype,))
         self._code, self._torch = DTYPES[dtype], TORCH[dtype]
         self.bytes = _mx_bytes(rows, cols)
-        self._lib = _abi.mx_lib()
+        L = self._lib = _abi.mx_lib()
+        self._call = _abi.native()
+        sizes = (rows, cols, self._code, self.bytes)
+        self._quantize = (_abi.address(L.fconv_mx_quantize),) + sizes
+        self._dequantize = (_abi.address(L.fconv_mx_dequantize),) + sizes
 
     def __call__(self, x, stream=None):
         rows, cols = self.rows, self.cols
+        if stream is None:
+            data = self._call.quantize(x, *self._quantize)
+            if data is not None:
+                return MxTensor._of(done(data, "fconv_mx_quantize"), rows, cols)
         ptr, ld = matrix(x, "x", rows, cols, self._torch)
 
         def run(s, device):
@@ -101,6 +109,10 @@ class MxQuantPlan:
         rows, cols = self.rows, self.cols
         if t.rows != rows or t.cols != cols:
             raise ValueError("MxTensor of %s, the plan needs %s" % (t.shape, (rows, cols)))
+        if stream is None:
+            y = self._call.dequantize(t.data, *self._dequantize)
+            if y is not None:
+                return done(y, "fconv_mx_dequantize")
 
         def run(s, device):
             y = torch.empty(rows, cols, dtype=self._torch, device=device)
@@ -137,6 +149,8 @@ class MxPlan:
         _check(L.fconv_mx_plan_workspace_size(self._h, ctypes.byref(n)), "fconv_mx_plan_workspace_size")
         self.workspace_bytes = n.value
         self.kernel_name = L.fconv_mx_plan_kernel_name(self._h).decode()
+        self._call = _abi.native()
+        self._product = (_abi.address(L.fconv_mx_plan_run), self._h.value, M, N, K, d.dtype, _mx_bytes(N, K), n.value)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -148,6 +162,12 @@ class MxPlan:
         """x: a GPU tensor [M, K] (its rows may be apart) or an MxTensor; w: an
         MxTensor [N, K]; bias fp32 [N] with the bias op.  Returns y [M, N] (in
         `out`, whose rows may be apart, if given)."""
+        short = stream is None and out is None and activ_alpha == 0.0 and activ_beta == 0.0
+        if short and not isinstance(x, MxTensor) and isinstance(w, MxTensor) and w.rows == self.N and \
+                w.cols == self.K and self._bias == (bias is not None):
+            y = self._call.product(x, w.data, bias, *self._product)
+            if y is not None:
+                return done(y, "fconv_mx_plan_run")
         a = _abi.MxArgs()
         if isinstance(x, MxTensor):
             if x.rows != self.M or x.cols != self.K:

@@ -13,7 +13,7 @@ import torch
 
 from . import _abi
 from . import _check, DTYPES
-from ._dense import TORCH, call, matrix, vector
+from ._dense import TORCH, call, done, matrix, vector
 
 __all__ = ["XentPlan"]
 
@@ -42,6 +42,10 @@ class XentPlan:
         _check(L.fconv_xent_plan_backward_workspace_size(self._h, ctypes.byref(n)),
                "fconv_xent_plan_backward_workspace_size")
         self.backward_workspace_bytes = n.value
+        self._call = _abi.native()
+        sizes = (self._h.value, T, D, V, d.dtype)
+        self._forward = (_abi.address(L.fconv_xent_plan_forward),) + sizes + (self.forward_workspace_bytes,)
+        self._backward = (_abi.address(L.fconv_xent_plan_backward),) + sizes + (self.backward_workspace_bytes,)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -58,6 +62,10 @@ class XentPlan:
 
     def forward(self, h, w, target, stream=None):
         """(loss, lse), fp32 [T].  h and w may have rows apart."""
+        if stream is None:
+            r = self._call.xent_forward(h, w, target, *self._forward)
+            if r is not None:
+                return done(r, "fconv_xent_plan_forward")
         a = self._inputs(h, w, target)
 
         def run(s, device):
@@ -79,6 +87,11 @@ class XentPlan:
             raise ValueError("backward: no gradient needed")
         if (dh is not None and not need_dh) or (dw is not None and not need_dw):
             raise ValueError("backward: an output given for a gradient that is not needed")
+        # Of no tokens dh has no address: the full way.
+        if stream is None and need_dh and need_dw and dh is None and dw is None and self.T > 0:
+            r = self._call.xent_backward(h, w, target, lse, dloss, *self._backward)
+            if r is not None:
+                return done(r, "fconv_xent_plan_backward")
         a = self._inputs(h, w, target)
         a.lse = vector(lse, "lse", self.T, torch.float32)
         a.dloss = vector(dloss, "dloss", self.T, torch.float32)

@@ -221,3 +221,36 @@ def test_binding_refuses():
         fc.MxPlan(4, 8, 40, "int8")
     with pytest.raises(fc.FconvError):
         fc.MxPlan(4, 0, 40)
+
+
+# --- sizes at the ends of what the checks let through ----------------------
+
+def test_strides_past_the_address_space_are_refused():
+    far = (1 << 62) // 4
+    L = _abi.mx_lib()
+    assert L.fconv_mx_quantize(None, FAKE, far, 9, 64, 1, 2 * FAKE) == INVALID
+    assert L.fconv_mx_dequantize(None, 2 * FAKE, 9, 64, 2, FAKE, far) == INVALID
+    st, h = _create(M=40, N=24, K=96, ops=())
+    assert st == OK
+    a = _abi.MxArgs()
+    a.x, a.w_mx, a.y, a.ldx, a.ldy = FAKE, 2 * FAKE, 4 * FAKE, far, 24
+    assert L.fconv_mx_plan_run(h, None, ctypes.byref(a)) == INVALID
+    a.ldx, a.ldy = 96, far
+    assert L.fconv_mx_plan_run(h, None, ctypes.byref(a)) == INVALID
+    L.fconv_mx_plan_destroy(h)
+
+
+def test_few_rows_of_very_many_outputs_stay_a_legal_launch():
+    # 2^29 outputs would be 2^24 workgroups of the few-rows kernel, 2^32 threads.
+    st, h = _create(M=1, N=1 << 29, K=32, ops=())
+    assert st == OK
+    assert _abi.mx_lib().fconv_mx_plan_kernel_name(h) not in (b"mx_few", b"mx_few_raw")
+    _abi.mx_lib().fconv_mx_plan_destroy(h)
+
+
+def test_quantised_matrices_of_the_host_are_refused():
+    p = fc.MxPlan(4, 8, 40, "fp32", ops=())
+    with pytest.raises(ValueError, match="GPU"):
+        p(_mx(4, 40), _mx(8, 40))
+    with pytest.raises(ValueError, match="GPU"):
+        fc.MxQuantPlan(4, 40, "fp32").dequantize(_mx(4, 40))
