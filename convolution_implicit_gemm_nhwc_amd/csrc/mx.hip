@@ -33,6 +33,7 @@ struct fconv_mx_plan_s {
   int32_t act;      // 0 none, 1 ReLU, 2 leaky, 3 clipped, 4 clamp
   int32_t kt;       // 128-column k tiles
   int32_t kernel;   // fconv::Kernel
+  int32_t rows_nt;  // of the rows kernel: tiles of 16 n for a wave
   int32_t ranges;   // of k, whose partial sums a second kernel joins
   size_t ws_x;      // bytes of the quantised x in the workspace
   size_t ws_bytes;
@@ -77,10 +78,11 @@ MxView view(const void* mx, int64_t rows, int64_t cols) {
   return MxView{c, c + codes_bytes(rows, cols), ceil_div(rows, 16)};
 }
 
-__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const uint32_t n = bytes > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(bytes < 0 ? 0 : bytes);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
-                                           static_cast<int>(n), kBufferDword3);
+// Descriptor of `bytes` bytes from base on (fewer than none: none; at most 2^31 - 1).
+__device__ inline i32x4 make_rsrc(const void* base, int64_t bytes) {
+  const uint64_t at = reinterpret_cast<uintptr_t>(base);
+  const int32_t n = static_cast<int32_t>(bytes > 0x7fffffff ? 0x7fffffff : bytes < 0 ? 0 : bytes);
+  return i32x4{static_cast<int32_t>(at), static_cast<int32_t>(at >> 32 & 0xffff), n, kBufferDword3};
 }
 
 __device__ inline float bf16_to_f32(uint16_t v) {
@@ -417,14 +419,30 @@ __device__ inline void load_bias(const MxArgs& a, const int (&n)[NI], bool whole
   }
 }
 
-// Bias, activation and store of this lane's part of a tile: n[i] .. + 3 of rows
-// m[j] (g = lane / 16; tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is asked once (`whole`): element by
-// element these questions took longer than the rest of the tile's end.
-template <bool BF16, int NI, int NJ>
-__device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
-                              const f32x4 (&bias)[NI], int g, bool whole, int range) {
+// Bias and activation of this lane's part of a tile (not of partial sums).
+template <int NI, int NJ>
+__device__ inline void finish_values(const MxArgs& a, f32x4 (&acc)[NJ][NI], const f32x4 (&bias)[NI]) {
+  if (a.part) return;
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[j][i] += bias[i];
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) activate(acc[j], a.act, a.act_alpha, a.act_beta);
+}
+
+// Stores this lane's part of a tile: n[i] .. + 3 of rows m[j] (g = lane / 16;
+// tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is
+// asked once (`whole`): element by element these questions took longer than the
+// rest of the tile's end.  ALL: the tile lies within M and N and goes to y, and
+// the stores are all there is.
+template <bool BF16, bool ALL, int NI, int NJ>
+__device__ inline void finish_stores(const MxArgs& a, const f32x4 (&acc)[NJ][NI], const int (&n)[NI],
+                                     const int64_t (&m)[NJ], int g, bool whole, int range) {
   constexpr int ES = BF16 ? 2 : 4;
-  if (a.part) {  // rows of ldp, a multiple of 4
+  if (!ALL && a.part) {  // rows of ldp, a multiple of 4
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       if (m[j] >= a.M) continue;
@@ -435,18 +453,11 @@ __device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (
     }
     return;
   }
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[j][i] += bias[i];
-  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    activate(acc[j], a.act, a.act_alpha, a.act_beta);
-    if (m[j] >= a.M) continue;
+    if (!ALL && m[j] >= a.M) continue;
     char* row = a.y + m[j] * a.ldy_bytes;
-    if (whole) {
+    if (ALL || whole) {
       if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < NI; i += 2)
@@ -472,6 +483,13 @@ __device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (
   }
 }
 
+template <bool BF16, int NI, int NJ>
+__device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
+                              const f32x4 (&bias)[NI], int g, bool whole, int range) {
+  finish_values(a, acc, bias);
+  finish_stores<BF16, false>(a, acc, n, m, g, whole, range);
+}
+
 // acc += A B over one k tile: 16 rows of W, 16 rows of X; SEL picks the
 // scale bytes of this k tile.
 template <int SEL>
@@ -482,11 +500,33 @@ __device__ inline f32x4 mma(i32x4 w, i32x4 x, f32x4 acc, int ws, int xs) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, acc, 4, 4, SEL, ws, SEL, xs);
 }
 
-// A wave's copy of 1 KiB into LDS, 16 bytes a lane from base + off (this lane's;
-// zeros past `bytes`).
-__device__ inline void copy_1k(const char* base, int64_t bytes, char* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_ptr_t)lds, 16, off, 0, 0, 0);
+// A wave's copy into LDS, B bytes (4 or 16) a lane from base + off (this lane's;
+// zeros past `bytes`).  In assembly, so that the compiler does not wait for it by
+// its own account, which takes a tile's stores for ones that may not have been
+// issued and so waits for them too.  Whoever reads the copy waits.  (s_nop 4: the
+// descriptor may come from a vector instruction, m0 needs one of the five.)
+template <int B>
+__device__ inline void copy_lds(const void* base, int64_t bytes, char* lds, uint32_t off) {
+  const i32x4 rsrc = make_rsrc(base, bytes);
+  const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr_t)lds));
+  if constexpr (B == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(off), "s"(rsrc) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(off), "s"(rsrc) : "memory");
 }
+
+// This lane's number, computed on the spot: a kernel short of registers keeps
+// neither it nor what follows from it.
+__device__ inline int lane_here() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
+// Immediate of s_waitcnt that waits until at most `n` vector memory operations are out.
+constexpr int vmcnt(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
 
 // Tiled product.  A workgroup owns a (2 H) n x (2 H) m tile in four quadrants;
 // NW waves share each quadrant, two along n, NW / 2 along m.  A slab is two k
@@ -517,6 +557,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   __shared__ __attribute__((aligned(1024))) char wx0[2 * HB], x10[HB], w10[HB];
   __shared__ __attribute__((aligned(1024))) char wx1[2 * HB], x11[HB], w11[HB];
   __shared__ __attribute__((aligned(1024))) char scales[2][4 * RT * kScaleTile];
+  __shared__ __attribute__((aligned(16))) float biases[2][NW * 64];  // of this tile and of the next
 
   // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
   // tiles: eight tile rows of m together, so both panels stay in its L2.
@@ -548,28 +589,27 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   };
   Place at = locate(first_id + slot);
 
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave / (NW / 2), wb = wave % (NW / 2);
   // A wave copies the scales of four row tiles, of W or of X.
   const bool swave = wave < NW / 2;
-  const uint32_t s_off =
-      static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
-  uint32_t first_off[2];  // of this wave's row tile in either half
-#pragma unroll
-  for (int h = 0; h < 2; ++h) first_off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + lane * 16);
+  const uint32_t row_off = static_cast<uint32_t>(wave * row_bytes);  // of this wave's row tile in the first half
   // The next slab to copy: its offset, k tiles, and scale tile counted from the range's first.
   uint32_t off;
   int next_kt, next_ks;
+  int odd = 0;  // which half of `biases` is the tile's
 
   // Past the last k tile the copies bring zeros.
   auto copy = [&](bool x, int h, char* buf) __attribute__((always_inline)) {
     const MxView& v = x ? a.x : a.w;
     const int64_t rt = x ? at.rtx : at.rtw;
+    const int lane = lane_here();
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      copy_1k(v.codes + rt * row_bytes, (v.row_tiles - rt) * row_bytes, buf + (wave * 2 + c) * kTileBytes,
-              next_kt + c < at.kt1 ? first_off[h] + off + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange);
+      copy_lds<16>(v.codes + rt * row_bytes, (v.row_tiles - rt) * row_bytes, buf + (wave * 2 + c) * kTileBytes,
+              lane * 16 + (next_kt + c < at.kt1 ? row_off + static_cast<uint32_t>(h * RT * row_bytes) + off +
+                                                      static_cast<uint32_t>(c * kTileBytes)
+                                                : kOutOfRange));
   };
   auto advance = [&]() __attribute__((always_inline)) {
     next_kt += 2;
@@ -578,7 +618,10 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   auto copy_scales = [&]() __attribute__((always_inline)) {
     const MxView& v = swave ? a.w : a.x;
     const int64_t rt = swave ? at.rtw : at.rtx;
-    copy_1k(v.scales + rt * srow_bytes, (v.row_tiles - rt) * srow_bytes, scales[next_ks & 1] + wave * 1024,
+    const int lane = lane_here();
+    const uint32_t s_off =
+        static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
+    copy_lds<16>(v.scales + rt * srow_bytes, (v.row_tiles - rt) * srow_bytes, scales[next_ks & 1] + wave * 1024,
             at.ks0 + next_ks < a.ks ? s_off + static_cast<uint32_t>(at.ks0 + next_ks) * kScaleTile : kOutOfRange);
     ++next_ks;
   };
@@ -588,6 +631,10 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     next_kt = at.kt0;
     next_ks = 0;
     off = static_cast<uint32_t>(at.kt0) * kTileBytes;
+    odd ^= 1;
+    const int first_n = static_cast<int>(at.rtw) * 16;
+    copy_lds<4>(a.bias + (a.bias ? first_n : 0), a.bias ? static_cast<int64_t>(a.N - first_n) * 4 : 0,
+                reinterpret_cast<char*>(biases[odd] + wave * 64), (wave * 64 + lane_here()) * 4);
     copy_scales();
     copy(false, 0, wx0);
     copy(true, 0, wx0 + HB);
@@ -608,15 +655,24 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   i32x4 fw[MI][2], fe[EARLY + 1], fx[2][MJ][2];
 
   auto read_scales = [&](const char* buf) __attribute__((always_inline)) {
+    const int lane_s = lane_here() * 4;
 #pragma unroll
     for (int i = 0; i < 2 * MI; ++i)
-      sw[i] = *reinterpret_cast<const int*>(buf + (i / MI * RT + wa * MI + i % MI) * kScaleTile + lane * 4);
+      sw[i] = *reinterpret_cast<const int*>(buf + (i / MI * RT + wa * MI + i % MI) * kScaleTile + lane_s);
 #pragma unroll
     for (int j = 0; j < 2 * MJ; ++j)
-      sx[j] = *reinterpret_cast<const int*>(buf + ((2 + j / MJ) * RT + wb * MJ + j % MJ) * kScaleTile + lane * 4);
+      sx[j] = *reinterpret_cast<const int*>(buf + ((2 + j / MJ) * RT + wb * MJ + j % MJ) * kScaleTile + lane_s);
+  };
+  // This lane's place in a half tile, for each slab anew: the compiler kept an
+  // address for every array otherwise, and spilled.
+  int lane_w, lane_x;
+  auto places = [&]() __attribute__((always_inline)) {
+    const int at = lane_here() * 16;
+    lane_w = wa * MI * 2 * kTileBytes + at;
+    lane_x = wb * MJ * 2 * kTileBytes + at;
   };
   auto w_at = [&](const char* buf, int i, int kk) __attribute__((always_inline)) {
-    return *reinterpret_cast<const i32x4*>(buf + ((wa * MI + i) * 2 + kk) * kTileBytes + lane * 16);
+    return *reinterpret_cast<const i32x4*>(buf + (i * 2 + kk) * kTileBytes + lane_w);
   };
   auto read_w_rest = [&](const char* buf) __attribute__((always_inline)) {
 #pragma unroll
@@ -629,7 +685,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int j = 0; j < MJ; ++j)
-        x[j][kk] = *reinterpret_cast<const i32x4*>(buf + ((wb * MJ + j) * 2 + kk) * kTileBytes + lane * 16);
+        x[j][kk] = *reinterpret_cast<const i32x4*>(buf + (j * 2 + kk) * kTileBytes + lane_x);
   };
   auto read_step_ends = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
@@ -660,14 +716,19 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // x0 holds this slab's X0; xb gets X1, then the next slab's X0.
+  // x0 holds this slab's X0; xb gets X1, then the next slab's X0.  OUT: stores of
+  // the tile before that may still be out, all newer than this slab's copies and
+  // the next one's.
   auto slab = [&](char* wx, char* x1, char* w1, const char* wx_next, i32x4 (&x0)[MJ][2], i32x4 (&xb)[MJ][2],
-                  auto sel) __attribute__((always_inline)) {
+                  auto sel, auto out) __attribute__((always_inline)) {
+    constexpr int OUT = decltype(out)::value;
     constexpr bool FIRST = decltype(sel)::value == 0;  // of a pair
+    places();
     if (FIRST) read_scales(scales[(next_ks - 1) & 1]);
     read_w_rest(wx);
     if (FIRST) copy_scales();
-    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F79 : 0x0F78);  // vmcnt(9 or 8): this slab is here
+    // This slab is here: newer are the next one's or the last one's eight, and the scales.
+    __builtin_amdgcn_s_waitcnt(vmcnt((FIRST || OUT ? 9 : 8) + OUT));
     read_step_ends();
     multiply(0, 0, x0, sel);
 
@@ -681,7 +742,8 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
 
     read_w_rest(w1);
     copy(true, 1, x1);
-    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F7B : 0x0F7A);  // vmcnt(11 or 10): the next slab's W0 and X0 are here
+    // The next slab's W0 and X0 are here (after a tile's second slab no stores are out).
+    __builtin_amdgcn_s_waitcnt(vmcnt(FIRST ? 11 + OUT : 10));
     read_step_ends();
     multiply(1, 1, xb, sel);
 
@@ -694,52 +756,83 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     multiply(1, 0, x0, sel);
   };
 
-  begin();
-  for (;;) {
+  // Before a tile's first slab: its copies are here, all but the STORES of the
+  // tile before, which came after them.
+  auto enter = [&](auto out) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2 * MJ; ++j)
 #pragma unroll
       for (int i = 0; i < 2 * MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    __builtin_amdgcn_s_waitcnt(0x0F78);
+    __builtin_amdgcn_s_waitcnt(vmcnt(8 + decltype(out)::value));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    places();
     read_x(fx[0], wx0 + HB);
 #pragma unroll
     for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
     if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
+  };
+  using std::integral_constant;
+  auto pair = [&](auto out) __attribute__((always_inline)) {
+    slab(wx0, x10, w10, wx1, fx[0], fx[1], integral_constant<int, 0>{}, out);
+    slab(wx1, x11, w11, wx0, fx[1], fx[0], integral_constant<int, 2>{}, out);
+  };
+  const integral_constant<int, 0> none;
+  // Stores of a whole tile, a wave's.  Every workgroup's come at once and take
+  // most of two slabs' time: the next tile's first pair runs meanwhile.
+  const integral_constant<int, 4 * MI * MJ / (BF16 ? 2 : 1)> out;
+
+  begin();
+  enter(none);
+  int s = 0;
+  for (;;) {
     const int slabs = (at.kt1 - at.kt0 + 1) / 2;
-    for (int s = 0; s + 1 < slabs; s += 2) {
-      slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
-      slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
-    }
-    if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+    for (; s + 1 < slabs; s += 2) pair(none);
+    if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], integral_constant<int, 0>{}, none);
     if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab have landed
 
-    // The next tile's copies are under way while this one is finished; the bias
-    // comes before them, since loads return in order.
-    int l = lane;
-    asm volatile("" : "+v"(l));  // places computed here, not kept in registers through the products
-    const int g = l >> 4, r = l & 15;
     const Place done = at;
-    int n[2 * MI];
-    int64_t m[2 * MJ];
     f32x4 bias[2 * MI];
+    const float* lane_bias = biases[odd] + (lane_here() >> 4) * 4;
 #pragma unroll
     for (int i = 0; i < 2 * MI; ++i)
-      n[i] = static_cast<int>((done.rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
-#pragma unroll
-    for (int j = 0; j < 2 * MJ; ++j) m[j] = (done.rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
-    const bool whole = (done.rtw + 2 * RT) * 16 <= a.N;
-    load_bias(a, n, whole, bias);
+      bias[i] = *reinterpret_cast<const f32x4*>(lane_bias + (i / MI * RT + wa * MI + i % MI) * 16);
     slot += gridDim.x / 8;
     const bool more = slot < end;
+    // The next tile's copies are under way while this one is finished.
     if (more) {
       at = locate(first_id + slot);
       begin();
     }
-    finish<BF16>(a, acc, n, m, bias, g, whole, done.range);
-    if (!more) break;
+    __builtin_amdgcn_sched_barrier(0);  // the stores come after the copies: the waits count them
+    const bool whole = (done.rtw + 2 * RT) * 16 <= a.N;
+    auto end_tile = [&](auto all) __attribute__((always_inline)) {
+      const int l = lane_here(), g = l >> 4, r = l & 15;
+      int n[2 * MI];
+      int64_t m[2 * MJ];
+#pragma unroll
+      for (int i = 0; i < 2 * MI; ++i)
+        n[i] = static_cast<int>((done.rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
+#pragma unroll
+      for (int j = 0; j < 2 * MJ; ++j) m[j] = (done.rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
+      finish_stores<BF16, decltype(all)::value>(a, acc, n, m, g, whole, done.range);
+    };
+    finish_values(a, acc, bias);
+    if (more && whole && !a.part && (done.rtx + 2 * RT) * 16 <= a.M) {
+      end_tile(integral_constant<bool, true>{});
+    } else {
+      end_tile(integral_constant<bool, false>{});
+      if (!more) break;
+      __builtin_amdgcn_s_waitcnt(0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    enter(out);
+    s = 0;
+    if (at.kt1 - at.kt0 > 2) {
+      pair(out);
+      s = 2;
+    }
   }
 }
 
@@ -903,24 +996,26 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
   finish<BF16>(a, out, n, m, bias, g, nt0 * 16 + 32 <= a.N, range);
 }
 
-// Many rows, few n: x is read once anyway, so it is quantised on its way into
-// the product and never written.  A wave owns 16 rows; its lane holds one
-// block of 32 values of a row and step, which is the matrix core's own order:
-// the block's largest magnitude and its codes need no other lane.  W (NT tiles
-// of 16 n) comes through the caches; the next step's x is loaded meanwhile.
+// Small products, and many rows of few n: x is quantised on its way into the
+// product and never written, which saves a launch and, where n is few, x's way
+// through memory.  A workgroup owns 64 rows and NT tiles of 16 n, a wave 16 of
+// the rows.  A lane holds one block of 32 values of a row and step, which is the
+// matrix core's own order: the block's largest magnitude and its codes need no
+// other lane.  W comes through the caches; the next step's x is loaded meanwhile.
 template <bool BF16, int NT>
 __global__ __launch_bounds__(256) void mx_rows_kernel(MxArgs a) {
   constexpr int ES = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int64_t mt = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (mt * 16 >= a.M) return;
+  const int64_t nt0 = static_cast<int64_t>(blockIdx.y) * NT;
   const int64_t row = mt * 16 + r;
   const char* xp = a.raw + (row < a.M ? row : a.M - 1) * a.ldx_bytes + g * 32 * ES;
   const char* wc[NT];
   const char* wsc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t rt = t < a.w.row_tiles ? t : a.w.row_tiles - 1;
+    const int64_t rt = nt0 + t < a.w.row_tiles ? nt0 + t : a.w.row_tiles - 1;
     wc[t] = a.w.codes + rt * a.kt * kTileBytes + lane * 16;
     wsc[t] = a.w.scales + rt * a.ks * kScaleTile + lane * 4;
   }
@@ -984,11 +1079,12 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxArgs a) {
   }
   int n[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) n[t] = 16 * t + 4 * g;
+  for (int t = 0; t < NT; ++t) n[t] = static_cast<int>(nt0 + t) * 16 + 4 * g;
   const int64_t m[1] = {row};
   f32x4 bias[NT];
-  load_bias(a, n, NT * 16 <= a.N, bias);
-  finish<BF16>(a, acc, n, m, bias, g, NT * 16 <= a.N, 0);
+  const bool whole = (nt0 + NT) * 16 <= a.N;
+  load_bias(a, n, whole, bias);
+  finish<BF16>(a, acc, n, m, bias, g, whole, 0);
 }
 
 // y = act(sum of the ranges, in order, + bias); four n of a row per thread.
@@ -1036,26 +1132,38 @@ int few_raw_bytes(const fconv_mx_plan_s* p) {
   return static_cast<int>(ks_per * 4 * (64 + 4) * p->d.M);
 }
 
-// The product's kernel and ranges of k.
+// Time (us) of the rows kernel with NT tiles of 16 n for a wave.  A step of 128 k
+// takes a wave alone 0.6 (NT 4) or 0.7 us (NT 8); more than a wave for a SIMD add
+// up.  128 to 512 rows of 512 -> 512: 5.7 (NT 4) and 7.0, by the 128 tiles 9.7;
+// 2048 of 1024 -> 1024: 13.5, 10.5 and 12.7; 8192 of 512 -> 512: 15.4, 13.5, 12.1.
+// Rows of fp32, and of bf16 that begin between dwords, take twice as long (896 of
+// 2827 -> 256 fp32 31.6, by the 128 tiles 16.4; 892 of 953 -> 2228 bf16 17.0 and
+// 12.6).
+double rows_us(const fconv_mx_desc& d, int es, int nt) {
+  const double M = d.M, N = d.N, K = d.K, kt = static_cast<double>(ceil_div(d.K, 128));
+  const double full = static_cast<double>(ceil_div(d.M, 16) * ceil_div(d.N, 16 * nt)) / 1024;  // waves for a SIMD
+  const double slow = es == 4 ? 2.1 : d.K % 2 ? 2.0 : 1.0;
+  const double step = slow * (nt == 4 ? (full > 1 ? 0.2 + 0.55 * full : 0.58) : 0.73 * (full > 1 ? full : 1));
+  const double base = nt == 4 ? 2.2 + (full > 1 ? full : 1) : 3.0 + (2.4 * full > 1 ? 2.4 * full : 1);
+  const double memory = 2.0 + (M * K + M * N) * es / 5.2e6;
+  return base + step * kt > memory ? base + step * kt : memory;
+}
+
+// The product's kernel and ranges of k, by the least time of rough accounts (us).
 void choose_kernel(fconv_mx_plan_s* p) {
   const int64_t M = p->d.M, N = p->d.N, ks = ceil_div(p->d.K, 512);
+  const double weights = 0.53 * static_cast<double>(N) * static_cast<double>(p->d.K);
   p->ranges = 1;
-  // W comes anew for every 16 rows there, so a long K costs more than writing
-  // the quantised x (us, against both kernels): 8192 x 64, K 1024 8.7 (15.7),
-  // 50000 x 100, K 2000 67 (64), 20480 x 128, K 4388 fp32 140 (97).
-  if (N <= 128 && M >= 4096 && p->d.K <= 1024) {
-    p->kernel = kRows;
-    return;
+  p->rows_nt = 4;
+  double rows = 1e300;
+  for (int nt = 4; nt <= 8; nt += 4) {
+    const double us = rows_us(p->d, p->esize, nt);
+    if (ceil_div(N, 64) > 65535 || us >= rows) continue;
+    rows = us;
+    p->rows_nt = nt;
   }
-  // The least time by a rough account (us): workgroups take turns on the
-  // device, each as long as its slabs (256 columns) and what a tile costs
-  // beside them; partial sums are written and read once more.
-  struct Kind {
-    int32_t kernel;
-    int64_t edge, at_once;
-    double slab, slab_alone, tile;
-  };
-  static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 10.0}, {kTile128, 128, 512, 1.05, 0.7, 5.0}};
+  // The others quantise x in a launch of its own (2.5 us captured, 3.9 back to back).
+  const double quantise = 3.6 + (p->esize + 0.53) * static_cast<double>(M) * static_cast<double>(p->d.K) / 5e6;
   double least = 1e300;
   if (M <= 64 && ceil_div(N, 32) <= kMaxGroups) {
     p->kernel = kFew;
@@ -1070,16 +1178,28 @@ void choose_kernel(fconv_mx_plan_s* p) {
     }
     // W at 5.2, 4.2 or 3 TB/s for 16, 32 or 64 rows (32768 x 4096: 13.7, 17.7 and
     // 24.4 us, the 128 tiles 15.9, 16.3 and 16.9).
-    least = 2.0 + 0.53 * static_cast<double>(N) * static_cast<double>(p->d.K) / (M <= 16 ? 5.2e6 : M <= 32 ? 4.2e6 : 3.0e6);
+    // One of 25088 -> 1024 is bound by the turns' latency: 11.2 us for 32 rows.
+    const double turns = 3.0 + 3.2e-4 * static_cast<double>(p->d.K);
+    least = 1.5 + weights / (M <= 16 ? 5.2e6 : M <= 32 ? 4.2e6 : 3.0e6);
+    least = quantise + (least > turns ? least : turns);
     if (p->ranges > 1) return;
   }
+  // Tiles: workgroups take turns on the device, each as long as its slabs (256
+  // columns) and what a tile costs beside them; partial sums are written and read
+  // once more.
+  struct Kind {
+    int32_t kernel;
+    int64_t edge, at_once;
+    double slab, slab_alone, tile;
+  };
+  static const Kind kinds[] = {{kTile256, 256, 256, 1.7, 1.4, 10.0}, {kTile128, 128, 512, 1.05, 0.7, 5.0}};
   for (const Kind& k : kinds) {
     const int64_t tiles = ceil_div(M, k.edge) * ceil_div(N, k.edge);
     for (int64_t r = 1; r <= ks && r <= 32; ++r) {
       const int64_t per = ceil_div(ks, r);
       if (ceil_div(ks, per) != r) continue;  // the same ranges as with fewer
-      double us = static_cast<double>(ceil_div(tiles * r, k.at_once)) *
-                  (2.0 * static_cast<double>(per) * (tiles * r > 256 ? k.slab : k.slab_alone) + k.tile);
+      double us = quantise + static_cast<double>(ceil_div(tiles * r, k.at_once)) *
+                                 (2.0 * static_cast<double>(per) * (tiles * r > 256 ? k.slab : k.slab_alone) + k.tile);
       if (r > 1) us += 4.0 + 8.0 * static_cast<double>(r * M) * static_cast<double>(N) / 6e6;
       if (us < least) {
         least = us;
@@ -1087,6 +1207,12 @@ void choose_kernel(fconv_mx_plan_s* p) {
         p->ranges = static_cast<int32_t>(r);
       }
     }
+  }
+  // The tiles' account is the better one where both are close (123 of 256 -> 26939
+  // 10.7 us by the tiles, 12.6 by the rows).
+  if (rows < 0.9 * least) {
+    p->kernel = kRows;
+    p->ranges = 1;
   }
 }
 
@@ -1121,7 +1247,7 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
   const int64_t all = ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.ranges, 8) * 8;
   const dim3 grid(static_cast<unsigned>(all < most ? all : most));
   const dim3 few(static_cast<unsigned>(ceil_div(a.N, 32) * a.ranges));
-  const dim3 rows(static_cast<unsigned>(ceil_div(a.M, 64)));
+  const dim3 rows(static_cast<unsigned>(ceil_div(a.M, 64)), static_cast<unsigned>(ceil_div(a.N, 16 * p->rows_nt)));
   switch (kernel) {
     case kTile256: hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), grid, dim3(512), 0, s, a); break;
     case kTile128: hipLaunchKernelGGL((mx_tile_kernel<BF16, 64, 4>), grid, dim3(256), 0, s, a); break;
@@ -1133,7 +1259,7 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
         launch_few<BF16, false>(p, a, kernel == kFewRaw, few, s);
       break;
     case kRows:
-      if (a.N <= 64)
+      if (p->rows_nt == 4)
         hipLaunchKernelGGL((mx_rows_kernel<BF16, 4>), rows, dim3(256), 0, s, a);
       else
         hipLaunchKernelGGL((mx_rows_kernel<BF16, 8>), rows, dim3(256), 0, s, a);
@@ -1321,7 +1447,7 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   int kernel = p->kernel;
   const bool by_itself = args->x && (kernel == kFewRaw || kernel == kRows);
   if (!args->x && kernel == kFewRaw) kernel = kFew;
-  if (!args->x && kernel == kRows) kernel = kTile128;
+  if (!args->x && kernel == kRows) kernel = d.M <= 64 ? kFew : kTile128;
   const size_t ws = args->x ? p->ws_bytes : p->ws_bytes - p->ws_x;
   if (ws > 0 && (!args->workspace || args->workspace_bytes < p->ws_bytes)) return FCONV_ERR_WORKSPACE;
   if (!aligned(args->x, p->esize) || !aligned(args->y, p->esize) || !aligned(args->x_mx, 16) ||

@@ -191,22 +191,49 @@ struct PerB {  // what it has to know of each b
 template <Epilogue EPI, int NJ, typename FB>
 __device__ inline PerB<EPI, NJ> load_per_b(const GemmArgs& g, int64_t a0, int64_t b0, int ra, int rb, FB b_of) {
   PerB<EPI, NJ> p;
+  int64_t b[NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int64_t b = b0 + min(b_of(j), rb - 1);
-    if constexpr (EPI == kEpiLse) {
-      const int64_t t = g.target[b] - g.v0 - a0;
+  for (int j = 0; j < NJ; ++j) b[j] = b0 + min(b_of(j), rb - 1);
+  if constexpr (EPI == kEpiLse) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t t = g.target[b[j]] - g.v0 - a0;
       p.at[j] = t >= 0 && t < ra ? static_cast<int>(t) : -1;
-    } else if constexpr (EPI == kEpiGrad) {
-      const int t = g.live_target[b];
-      p.at[j] = static_cast<int>(t - g.v0 - a0);
-      p.f[j] = t < 0 ? __builtin_nanf("") : g.lse[b];
-    } else if constexpr (is_out(EPI)) {
-      p.at[j] = g.row_map ? g.row_map[b] : static_cast<int>(b);
-      p.f[j] = g.scale[b * g.scale_step];
+    }
+  } else if constexpr (EPI == kEpiGrad) {
+    // All loads at once: asking for lse where the target is one took eight in a row.
+    int t[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      t[j] = g.live_target[b[j]];
+      p.f[j] = g.lse[b[j]];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      p.at[j] = static_cast<int>(t[j] - g.v0 - a0);
+      p.f[j] = t[j] < 0 ? __builtin_nanf("") : p.f[j];
+    }
+  } else if constexpr (is_out(EPI)) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      p.at[j] = static_cast<int>(b[j]);
+      p.f[j] = g.scale[b[j] * g.scale_step];
+    }
+    if (g.row_map) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) p.at[j] = g.row_map[b[j]];
     }
   }
   return p;
+}
+// The loads are done before what follows.
+template <Epilogue EPI, int NJ>
+__device__ inline void have_per_b(PerB<EPI, NJ>& p) {
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    if constexpr (EPI != kEpiPart) asm volatile("" : "+v"(p.at[j]));
+    if constexpr (EPI != kEpiPart && EPI != kEpiLse) asm volatile("" : "+v"(p.f[j]));
+  }
 }
 
 template <typename E, Epilogue EPI, int NI, int NJ, int EDGE, typename FA, typename FB>
@@ -547,6 +574,96 @@ __global__ __launch_bounds__(256) void xent_gen_grads_kernel(GemmArgs dh, GemmAr
   }
 }
 
+// dh of at most 16 MT tokens over a short vocabulary, sixteen d of all tokens for
+// a workgroup, so that no partial sums go out and no launch joins them: its four
+// waves take turns at steps of 32 v and add their sums in LDS, in order.  A lane
+// picks its eight v of a column out of memory one by one, from any row distance
+// and alignment; rows of g are whole 64s, zeros past the vocabulary.
+template <typename E, int MT>
+__device__ inline void few_dh(const GemmArgs& g, f32x4* sums, int d0) {
+  using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
+  constexpr int ES = sizeof(E), STEPS = 2;  // of a turn, whose loads are in flight together
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int steps = (g.nk + 31) / 32;
+  const int64_t row = g.a.ld * ES;
+  // Columns past the last one read it again; they are not stored.
+  const char* wp = g.a.p + static_cast<int64_t>(min(d0 + r, g.na - 1)) * ES;
+  const char* gp[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+    gp[j] = g.b.p + (static_cast<int64_t>(min(16 * j + r, g.nb - 1)) * g.b.ld + 8 * q) * ES;
+  struct Turn {
+    E a[STEPS][8];
+    Frag b[STEPS][MT];
+  };
+  auto load = [&](Turn& x, int first) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int step = first + 4 * s;
+      if (step >= steps) break;  // uniform
+      const int v = 32 * step + 8 * q;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        __builtin_memcpy(&x.a[s][e], wp + static_cast<int64_t>(min(v + e, g.nk - 1)) * row, ES);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) __builtin_memcpy(&x.b[s][j], gp[j] + static_cast<int64_t>(step) * 32 * ES, 8 * ES);
+    }
+  };
+  f32x4 acc[MT] = {};
+  auto multiply = [&](const Turn& x, int first) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int step = first + 4 * s;
+      if (step >= steps) break;
+      E v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 32 * step + 8 * q + e < g.nk ? x.a[s][e] : static_cast<E>(0.0f);
+      Frag a;
+      __builtin_memcpy(&a, v, sizeof(a));
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = mma8(a, x.b[s][j], acc[j]);
+    }
+  };
+  Turn now, next;
+  constexpr int NEXT = 4 * STEPS;
+  int first = wave;
+  if (first < steps) load(now, first);
+  for (; first < steps; first += 2 * NEXT) {
+    if (first + NEXT < steps) load(next, first + NEXT);
+    multiply(now, first);
+    if (first + NEXT >= steps) break;
+    if (first + 2 * NEXT < steps) load(now, first + 2 * NEXT);
+    multiply(next, first + NEXT);
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) sums[(wave * MT + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  const int t = 16 * wave + r, d = d0 + 4 * q;
+  if (wave >= MT || t >= g.nb || d >= g.na) return;
+  f32x4 sum = sums[wave * 64 + lane];
+#pragma unroll
+  for (int x = 1; x < 4; ++x) sum += sums[(x * MT + wave) * 64 + lane];
+  sum *= g.scale[t];
+  if (g.row_map[t] < 0) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+  store4<E>(g.out + (t * g.ld_out + d) * static_cast<int64_t>(ES), sum, g.na - d);
+}
+
+// The first workgroups take dh, the others (if dw is wanted) dw's tiles.
+template <typename E, int MT>
+__global__ __launch_bounds__(256) void xent_few_grads_kernel(GemmArgs dh, GemmArgs dw) {
+  __shared__ GenLds<E> lds;
+  static_assert(sizeof(lds.buf) >= 4 * MT * 64 * sizeof(f32x4), "the sums fit");
+  const int n_dh = (dh.na + 15) / 16, i = static_cast<int>(blockIdx.x) - n_dh;
+  if (i < 0) {
+    few_dh<E, MT>(dh, reinterpret_cast<f32x4*>(&lds.buf[0][0][0]), static_cast<int>(blockIdx.x) * 16);
+  } else {
+    const int ta = (dw.na + 63) / 64;
+    gen_tile<E, kRow, kRow, kEpiOut>(dw, lds, i % ta, i / ta, 0);
+  }
+}
+
 // -------------------------------------------------------------- tiled kernel
 //
 // bf16, rows and their length multiples of 16 bytes.  A workgroup owns a
@@ -845,7 +962,8 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
     const int r = l & 15, q = l >> 4;
     auto a_of = [&](int i) { return i / MI * H + (wa * MI + i % MI) * 16 + 4 * q; };
     auto b_of = [&](int j) { return j / MJ * H + (wb * MJ + j % MJ) * 16 + r; };
-    const auto per_b = load_per_b<EPI, 2 * MJ>(g, at.a0, at.b0, at.ra, at.rb, b_of);
+    auto per_b = load_per_b<EPI, 2 * MJ>(g, at.a0, at.b0, at.ra, at.rb, b_of);
+    have_per_b<EPI, 2 * MJ>(per_b);
     const Place done = at;
     slot += gridDim.x / 8;
     const bool more = slot < end;
@@ -1513,6 +1631,11 @@ hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
 bool fits_tiles(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
 
 constexpr int32_t kFewTokens = 64;
+// Vocabularies up to this take few_dh: it grows with the vocabulary, the tiles'
+// way costs a launch more (both gradients of 16 x 512 x 1000 10.0 instead of 12.6
+// us, x 2048 12.0 and 13.7, x 4096 15.9 and 15.7; of 64 tokens 14.2 and 14.6, 18.4
+// and 15.8).
+int32_t few_dh_v(int32_t T) { return T <= 32 ? 2048 : 1024; }
 // Workgroups of the few-token forward kernel.
 int64_t few_groups(int32_t V) { return ceil_div(V, 32) < 1024 ? round_up(ceil_div(V, 32), 8) : 1024; }
 
@@ -1778,7 +1901,29 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       c.part_stride = c.ld_out * nv;
       c.out = ws + p->o_dw;
     }
-    if (args->dh && args->dw && dh_edge == 64 && p->dw.edge == 64 && dw_whole) {
+    auto launch_dw = [&](const GemmArgs& c) {
+      return dw_whole ? past ? launch_gemm<E, kRow, kRow, kEpiStream>(c, p->dw.edge, s)
+                             : launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s)
+                      : launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
+    };
+    bool dh_done = false;
+    const bool one_dw = args->dw && p->dw.edge == 64 && dw_whole;  // in a launch with dh
+    if (args->dh && few && d.V <= few_dh_v(d.T)) {
+      h.out = static_cast<char*>(args->dh);
+      h.ld_out = args->lddh;
+      h.row_map = index;
+      h.scale = live_dloss;
+      const dim3 grid(static_cast<unsigned>(ceil_div(d.D, 16) + (one_dw ? ceil_div(d.D, 64) * ceil_div(nv, 64) : 0)));
+      if (d.T <= 16)
+        hipLaunchKernelGGL((xent_few_grads_kernel<E, 1>), grid, dim3(256), 0, s, h, c);
+      else if (d.T <= 32)
+        hipLaunchKernelGGL((xent_few_grads_kernel<E, 2>), grid, dim3(256), 0, s, h, c);
+      else
+        hipLaunchKernelGGL((xent_few_grads_kernel<E, 4>), grid, dim3(256), 0, s, h, c);
+      e = hipGetLastError();
+      if (e == hipSuccess && args->dw && !one_dw) e = launch_dw(c);
+      dh_done = true;
+    } else if (args->dh && one_dw && dh_edge == 64) {
       const int64_t ta = ceil_div(d.D, 64);
       const dim3 grid(static_cast<unsigned>(ta * (ceil_div(d.T, 64) * h.ranges + ceil_div(nv, 64))));
       if (dh_whole)
@@ -1790,12 +1935,9 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       if (args->dh)
         e = dh_whole ? launch_gemm<E, kRow, kSum, kEpiOut>(h, dh_edge, s)
                      : launch_gemm<E, kRow, kSum, kEpiPart>(h, dh_edge, s);
-      if (e == hipSuccess && args->dw)
-        e = dw_whole ? past ? launch_gemm<E, kRow, kRow, kEpiStream>(c, p->dw.edge, s)
-                            : launch_gemm<E, kRow, kRow, kEpiOut>(c, p->dw.edge, s)
-                     : launch_gemm<E, kRow, kRow, kEpiPart>(c, p->dw.edge, s);
+      if (e == hipSuccess && args->dw) e = launch_dw(c);
     }
-    if (e == hipSuccess && args->dh && !dh_whole && i == p->pieces - 1)
+    if (e == hipSuccess && args->dh && !dh_done && !dh_whole && i == p->pieces - 1)
       e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), p->pieces * h.ranges, h.part_stride,
                         h.ld_out, d.T, n_live, index, live_dloss, 1, d.D, static_cast<char*>(args->dh),
                         args->lddh, s);

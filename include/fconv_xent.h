@@ -11,7 +11,8 @@
  * A token whose target is ignore_index has loss 0 and no gradient, whatever
  * its h and dloss; its lse is computed all the same.  A target that is
  * neither that nor in [0, V) gives a NaN loss and NaN gradients.  An lse is
- * +inf where a logit is, -inf where all are, NaN where one is.
+ * +inf where a logit is, -inf where all are, NaN where one is.  A dloss that is
+ * infinite or NaN makes all of dw NaN, and dh of its token.
  *
  * dtype is the type of h, w, dh and dw (FCONV_BF16 or FCONV_FP32); products
  * are summed in fp32 by the matrix cores, loss, lse and dloss are fp32.  With

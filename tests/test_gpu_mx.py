@@ -135,6 +135,10 @@ PRODUCTS += [(1, 32, 16385), (3, 40, 5000), (4, 16400, 520), (16, 16399, 1030), 
              (33, 50, 9001), (40, 4000, 1500), (49, 33, 2049), (64, 64, 25088), (65, 100, 9000), (300, 200, 20000),
              (4096, 1, 33), (5000, 64, 256), (4099, 67, 700), (6000, 128, 1000), (4100, 17, 129), (20, 40, 40000), (2, 33, 70001),
              (4500, 100, 1500)]
+# Small products by the rows kernel: rows and outputs that end inside a tile, one and several blocks of outputs.
+PRODUCTS += [(17, 16, 31), (40, 100, 260), (65, 300, 127), (129, 513, 385), (500, 200, 512), (2000, 1001, 130)]
+# Whole tiles one after another on a workgroup, whose stores overlap the next tile, and ragged ones between them.
+PRODUCTS += [(2304, 9000, 512), (4096, 8192, 260), (2100, 8200, 1030)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])

@@ -144,20 +144,20 @@ def test_plan_refuses():
 
 def test_run_refuses():
     L = _abi.mx_lib()
-    st, h = _create(M=40, N=24, K=96, ops=(3, 8))
+    st, h = _create(M=40, N=24, K=4096, ops=(3, 8))
     assert st == OK
     n = ctypes.c_size_t()
-    assert L.fconv_mx_plan_workspace_size(h, ctypes.byref(n)) == OK
+    assert L.fconv_mx_plan_workspace_size(h, ctypes.byref(n)) == OK and n.value > 0
 
     def run(**kw):
         a = _abi.MxArgs()
-        base = dict(x=FAKE, ldx=96, w_mx=2 * FAKE, bias=3 * FAKE, y=4 * FAKE, ldy=24, workspace=5 * FAKE,
+        base = dict(x=FAKE, ldx=4096, w_mx=2 * FAKE, bias=3 * FAKE, y=4 * FAKE, ldy=24, workspace=5 * FAKE,
                     workspace_bytes=n.value, activ_alpha=0.0, activ_beta=1.0)
         for k, v in dict(base, **kw).items():
             setattr(a, k, v)
         return L.fconv_mx_plan_run(h, None, ctypes.byref(a))
     for kw in (dict(x=None), dict(x_mx=6 * FAKE), dict(w_mx=None), dict(bias=None), dict(y=None),
-               dict(ldx=95), dict(ldy=23), dict(y=FAKE), dict(y=2 * FAKE), dict(y=3 * FAKE),
+               dict(ldx=4095), dict(ldy=23), dict(y=FAKE), dict(y=2 * FAKE), dict(y=3 * FAKE),
                dict(y=5 * FAKE), dict(workspace=FAKE), dict(activ_alpha=2.0),
                dict(activ_alpha=float("nan")), dict(activ_beta=float("inf"))):
         assert run(**kw) == INVALID, kw
