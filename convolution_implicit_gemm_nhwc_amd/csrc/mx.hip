@@ -78,11 +78,10 @@ MxView view(const void* mx, int64_t rows, int64_t cols) {
   return MxView{c, c + codes_bytes(rows, cols), ceil_div(rows, 16)};
 }
 
-// Descriptor of `bytes` bytes from base on (fewer than none: none; at most 2^31 - 1).
-__device__ inline i32x4 make_rsrc(const void* base, int64_t bytes) {
-  const uint64_t at = reinterpret_cast<uintptr_t>(base);
-  const int32_t n = static_cast<int32_t>(bytes > 0x7fffffff ? 0x7fffffff : bytes < 0 ? 0 : bytes);
-  return i32x4{static_cast<int32_t>(at), static_cast<int32_t>(at >> 32 & 0xffff), n, kBufferDword3};
+__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const uint32_t n = bytes > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(bytes < 0 ? 0 : bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(n), kBufferDword3);
 }
 
 __device__ inline float bf16_to_f32(uint16_t v) {
@@ -419,30 +418,14 @@ __device__ inline void load_bias(const MxArgs& a, const int (&n)[NI], bool whole
   }
 }
 
-// Bias and activation of this lane's part of a tile (not of partial sums).
-template <int NI, int NJ>
-__device__ inline void finish_values(const MxArgs& a, f32x4 (&acc)[NJ][NI], const f32x4 (&bias)[NI]) {
-  if (a.part) return;
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[j][i] += bias[i];
-  }
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) activate(acc[j], a.act, a.act_alpha, a.act_beta);
-}
-
-// Stores this lane's part of a tile: n[i] .. + 3 of rows m[j] (g = lane / 16;
-// tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is
-// asked once (`whole`): element by element these questions took longer than the
-// rest of the tile's end.  ALL: the tile lies within M and N and goes to y, and
-// the stores are all there is.
-template <bool BF16, bool ALL, int NI, int NJ>
-__device__ inline void finish_stores(const MxArgs& a, const f32x4 (&acc)[NJ][NI], const int (&n)[NI],
-                                     const int64_t (&m)[NJ], int g, bool whole, int range) {
+// Bias, activation and store of this lane's part of a tile: n[i] .. + 3 of rows
+// m[j] (g = lane / 16; tiles i, i + 1 of even i lie side by side).  Whether the tile ends inside N is asked once (`whole`): element by
+// element these questions took longer than the rest of the tile's end.
+template <bool BF16, int NI, int NJ>
+__device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
+                              const f32x4 (&bias)[NI], int g, bool whole, int range) {
   constexpr int ES = BF16 ? 2 : 4;
-  if (!ALL && a.part) {  // rows of ldp, a multiple of 4
+  if (a.part) {  // rows of ldp, a multiple of 4
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       if (m[j] >= a.M) continue;
@@ -453,12 +436,19 @@ __device__ inline void finish_stores(const MxArgs& a, const f32x4 (&acc)[NJ][NI]
     }
     return;
   }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[j][i] += bias[i];
+  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    if (!ALL && m[j] >= a.M) continue;
+    activate(acc[j], a.act, a.act_alpha, a.act_beta);
+    if (m[j] >= a.M) continue;
     char* row = a.y + m[j] * a.ldy_bytes;
-    if (ALL || whole) {
-      if constexpr (BF16) {
+    if (whole) {
+      if constexpr (BF16 && NI % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < NI; i += 2)
           store_pair(row + static_cast<int64_t>(n[i] - 4 * g + (g & 1) * 16 + (g >> 1) * 8) * ES, acc[j][i],
@@ -483,13 +473,6 @@ __device__ inline void finish_stores(const MxArgs& a, const f32x4 (&acc)[NJ][NI]
   }
 }
 
-template <bool BF16, int NI, int NJ>
-__device__ inline void finish(const MxArgs& a, f32x4 (&acc)[NJ][NI], const int (&n)[NI], const int64_t (&m)[NJ],
-                              const f32x4 (&bias)[NI], int g, bool whole, int range) {
-  finish_values(a, acc, bias);
-  finish_stores<BF16, false>(a, acc, n, m, g, whole, range);
-}
-
 // acc += A B over one k tile: 16 rows of W, 16 rows of X; SEL picks the
 // scale bytes of this k tile.
 template <int SEL>
@@ -500,33 +483,11 @@ __device__ inline f32x4 mma(i32x4 w, i32x4 x, f32x4 acc, int ws, int xs) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, acc, 4, 4, SEL, ws, SEL, xs);
 }
 
-// A wave's copy into LDS, B bytes (4 or 16) a lane from base + off (this lane's;
-// zeros past `bytes`).  In assembly, so that the compiler does not wait for it by
-// its own account, which takes a tile's stores for ones that may not have been
-// issued and so waits for them too.  Whoever reads the copy waits.  (s_nop 4: the
-// descriptor may come from a vector instruction, m0 needs one of the five.)
-template <int B>
-__device__ inline void copy_lds(const void* base, int64_t bytes, char* lds, uint32_t off) {
-  const i32x4 rsrc = make_rsrc(base, bytes);
-  const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr_t)lds));
-  if constexpr (B == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off), "s"(rsrc) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off), "s"(rsrc) : "memory");
+// A wave's copy of 1 KiB into LDS, 16 bytes a lane from base + off (this lane's;
+// zeros past `bytes`).
+__device__ inline void copy_1k(const char* base, int64_t bytes, char* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, bytes), (lds_ptr_t)lds, 16, off, 0, 0, 0);
 }
-
-// This lane's number, computed on the spot: a kernel short of registers keeps
-// neither it nor what follows from it.
-__device__ inline int lane_here() {
-  int l;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-  return l;
-}
-
-// Immediate of s_waitcnt that waits until at most `n` vector memory operations are out.
-constexpr int vmcnt(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
 
 // Tiled product.  A workgroup owns a (2 H) n x (2 H) m tile in four quadrants;
 // NW waves share each quadrant, two along n, NW / 2 along m.  A slab is two k
@@ -557,7 +518,6 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   __shared__ __attribute__((aligned(1024))) char wx0[2 * HB], x10[HB], w10[HB];
   __shared__ __attribute__((aligned(1024))) char wx1[2 * HB], x11[HB], w11[HB];
   __shared__ __attribute__((aligned(1024))) char scales[2][4 * RT * kScaleTile];
-  __shared__ __attribute__((aligned(16))) float biases[2][NW * 64];  // of this tile and of the next
 
   // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
   // tiles: eight tile rows of m together, so both panels stay in its L2.
@@ -589,27 +549,28 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   };
   Place at = locate(first_id + slot);
 
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave / (NW / 2), wb = wave % (NW / 2);
   // A wave copies the scales of four row tiles, of W or of X.
   const bool swave = wave < NW / 2;
-  const uint32_t row_off = static_cast<uint32_t>(wave * row_bytes);  // of this wave's row tile in the first half
+  const uint32_t s_off =
+      static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
+  uint32_t first_off[2];  // of this wave's row tile in either half
+#pragma unroll
+  for (int h = 0; h < 2; ++h) first_off[h] = static_cast<uint32_t>((h * RT + wave) * row_bytes + lane * 16);
   // The next slab to copy: its offset, k tiles, and scale tile counted from the range's first.
   uint32_t off;
   int next_kt, next_ks;
-  int odd = 0;  // which half of `biases` is the tile's
 
   // Past the last k tile the copies bring zeros.
   auto copy = [&](bool x, int h, char* buf) __attribute__((always_inline)) {
     const MxView& v = x ? a.x : a.w;
     const int64_t rt = x ? at.rtx : at.rtw;
-    const int lane = lane_here();
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      copy_lds<16>(v.codes + rt * row_bytes, (v.row_tiles - rt) * row_bytes, buf + (wave * 2 + c) * kTileBytes,
-              lane * 16 + (next_kt + c < at.kt1 ? row_off + static_cast<uint32_t>(h * RT * row_bytes) + off +
-                                                      static_cast<uint32_t>(c * kTileBytes)
-                                                : kOutOfRange));
+      copy_1k(v.codes + rt * row_bytes, (v.row_tiles - rt) * row_bytes, buf + (wave * 2 + c) * kTileBytes,
+              next_kt + c < at.kt1 ? first_off[h] + off + static_cast<uint32_t>(c * kTileBytes) : kOutOfRange);
   };
   auto advance = [&]() __attribute__((always_inline)) {
     next_kt += 2;
@@ -618,10 +579,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   auto copy_scales = [&]() __attribute__((always_inline)) {
     const MxView& v = swave ? a.w : a.x;
     const int64_t rt = swave ? at.rtw : at.rtx;
-    const int lane = lane_here();
-    const uint32_t s_off =
-        static_cast<uint32_t>((4 * (wave % (NW / 2)) + (lane >> 4)) * srow_bytes + (lane & 15) * 16);
-    copy_lds<16>(v.scales + rt * srow_bytes, (v.row_tiles - rt) * srow_bytes, scales[next_ks & 1] + wave * 1024,
+    copy_1k(v.scales + rt * srow_bytes, (v.row_tiles - rt) * srow_bytes, scales[next_ks & 1] + wave * 1024,
             at.ks0 + next_ks < a.ks ? s_off + static_cast<uint32_t>(at.ks0 + next_ks) * kScaleTile : kOutOfRange);
     ++next_ks;
   };
@@ -631,10 +589,6 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     next_kt = at.kt0;
     next_ks = 0;
     off = static_cast<uint32_t>(at.kt0) * kTileBytes;
-    odd ^= 1;
-    const int first_n = static_cast<int>(at.rtw) * 16;
-    copy_lds<4>(a.bias + (a.bias ? first_n : 0), a.bias ? static_cast<int64_t>(a.N - first_n) * 4 : 0,
-                reinterpret_cast<char*>(biases[odd] + wave * 64), (wave * 64 + lane_here()) * 4);
     copy_scales();
     copy(false, 0, wx0);
     copy(true, 0, wx0 + HB);
@@ -655,24 +609,15 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
   i32x4 fw[MI][2], fe[EARLY + 1], fx[2][MJ][2];
 
   auto read_scales = [&](const char* buf) __attribute__((always_inline)) {
-    const int lane_s = lane_here() * 4;
 #pragma unroll
     for (int i = 0; i < 2 * MI; ++i)
-      sw[i] = *reinterpret_cast<const int*>(buf + (i / MI * RT + wa * MI + i % MI) * kScaleTile + lane_s);
+      sw[i] = *reinterpret_cast<const int*>(buf + (i / MI * RT + wa * MI + i % MI) * kScaleTile + lane * 4);
 #pragma unroll
     for (int j = 0; j < 2 * MJ; ++j)
-      sx[j] = *reinterpret_cast<const int*>(buf + ((2 + j / MJ) * RT + wb * MJ + j % MJ) * kScaleTile + lane_s);
-  };
-  // This lane's place in a half tile, for each slab anew: the compiler kept an
-  // address for every array otherwise, and spilled.
-  int lane_w, lane_x;
-  auto places = [&]() __attribute__((always_inline)) {
-    const int at = lane_here() * 16;
-    lane_w = wa * MI * 2 * kTileBytes + at;
-    lane_x = wb * MJ * 2 * kTileBytes + at;
+      sx[j] = *reinterpret_cast<const int*>(buf + ((2 + j / MJ) * RT + wb * MJ + j % MJ) * kScaleTile + lane * 4);
   };
   auto w_at = [&](const char* buf, int i, int kk) __attribute__((always_inline)) {
-    return *reinterpret_cast<const i32x4*>(buf + (i * 2 + kk) * kTileBytes + lane_w);
+    return *reinterpret_cast<const i32x4*>(buf + ((wa * MI + i) * 2 + kk) * kTileBytes + lane * 16);
   };
   auto read_w_rest = [&](const char* buf) __attribute__((always_inline)) {
 #pragma unroll
@@ -685,7 +630,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int j = 0; j < MJ; ++j)
-        x[j][kk] = *reinterpret_cast<const i32x4*>(buf + (j * 2 + kk) * kTileBytes + lane_x);
+        x[j][kk] = *reinterpret_cast<const i32x4*>(buf + ((wb * MJ + j) * 2 + kk) * kTileBytes + lane * 16);
   };
   auto read_step_ends = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
@@ -716,19 +661,14 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // x0 holds this slab's X0; xb gets X1, then the next slab's X0.  OUT: stores of
-  // the tile before that may still be out, all newer than this slab's copies and
-  // the next one's.
+  // x0 holds this slab's X0; xb gets X1, then the next slab's X0.
   auto slab = [&](char* wx, char* x1, char* w1, const char* wx_next, i32x4 (&x0)[MJ][2], i32x4 (&xb)[MJ][2],
-                  auto sel, auto out) __attribute__((always_inline)) {
-    constexpr int OUT = decltype(out)::value;
+                  auto sel) __attribute__((always_inline)) {
     constexpr bool FIRST = decltype(sel)::value == 0;  // of a pair
-    places();
     if (FIRST) read_scales(scales[(next_ks - 1) & 1]);
     read_w_rest(wx);
     if (FIRST) copy_scales();
-    // This slab is here: newer are the next one's or the last one's eight, and the scales.
-    __builtin_amdgcn_s_waitcnt(vmcnt((FIRST || OUT ? 9 : 8) + OUT));
+    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F79 : 0x0F78);  // vmcnt(9 or 8): this slab is here
     read_step_ends();
     multiply(0, 0, x0, sel);
 
@@ -742,8 +682,7 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
 
     read_w_rest(w1);
     copy(true, 1, x1);
-    // The next slab's W0 and X0 are here (after a tile's second slab no stores are out).
-    __builtin_amdgcn_s_waitcnt(vmcnt(FIRST ? 11 + OUT : 10));
+    __builtin_amdgcn_s_waitcnt(FIRST ? 0x0F7B : 0x0F7A);  // vmcnt(11 or 10): the next slab's W0 and X0 are here
     read_step_ends();
     multiply(1, 1, xb, sel);
 
@@ -756,83 +695,52 @@ __global__ __launch_bounds__(NW * 64, 2) void mx_tile_kernel(MxArgs a) {
     multiply(1, 0, x0, sel);
   };
 
-  // Before a tile's first slab: its copies are here, all but the STORES of the
-  // tile before, which came after them.
-  auto enter = [&](auto out) __attribute__((always_inline)) {
+  begin();
+  for (;;) {
 #pragma unroll
     for (int j = 0; j < 2 * MJ; ++j)
 #pragma unroll
       for (int i = 0; i < 2 * MI; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    __builtin_amdgcn_s_waitcnt(vmcnt(8 + decltype(out)::value));
+    __builtin_amdgcn_s_waitcnt(0x0F78);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    places();
     read_x(fx[0], wx0 + HB);
 #pragma unroll
     for (int i = 0; i < EARLY; ++i) fw[i][0] = w_at(wx0, i, 0);
     if (NW == 8 && wa == 1) __builtin_amdgcn_s_barrier();
-  };
-  using std::integral_constant;
-  auto pair = [&](auto out) __attribute__((always_inline)) {
-    slab(wx0, x10, w10, wx1, fx[0], fx[1], integral_constant<int, 0>{}, out);
-    slab(wx1, x11, w11, wx0, fx[1], fx[0], integral_constant<int, 2>{}, out);
-  };
-  const integral_constant<int, 0> none;
-  // Stores of a whole tile, a wave's.  Every workgroup's come at once and take
-  // most of two slabs' time: the next tile's first pair runs meanwhile.
-  const integral_constant<int, 4 * MI * MJ / (BF16 ? 2 : 1)> out;
-
-  begin();
-  enter(none);
-  int s = 0;
-  for (;;) {
     const int slabs = (at.kt1 - at.kt0 + 1) / 2;
-    for (; s + 1 < slabs; s += 2) pair(none);
-    if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], integral_constant<int, 0>{}, none);
+    for (int s = 0; s + 1 < slabs; s += 2) {
+      slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
+      slab(wx1, x11, w11, wx0, fx[1], fx[0], std::integral_constant<int, 2>{});
+    }
+    if (slabs & 1) slab(wx0, x10, w10, wx1, fx[0], fx[1], std::integral_constant<int, 0>{});
     if (NW == 8 && wa == 0) __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_s_waitcnt(0);  // copies past the last slab have landed
 
+    // The next tile's copies are under way while this one is finished; the bias
+    // comes before them, since loads return in order.
+    int l = lane;
+    asm volatile("" : "+v"(l));  // places computed here, not kept in registers through the products
+    const int g = l >> 4, r = l & 15;
     const Place done = at;
+    int n[2 * MI];
+    int64_t m[2 * MJ];
     f32x4 bias[2 * MI];
-    const float* lane_bias = biases[odd] + (lane_here() >> 4) * 4;
 #pragma unroll
     for (int i = 0; i < 2 * MI; ++i)
-      bias[i] = *reinterpret_cast<const f32x4*>(lane_bias + (i / MI * RT + wa * MI + i % MI) * 16);
+      n[i] = static_cast<int>((done.rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
+#pragma unroll
+    for (int j = 0; j < 2 * MJ; ++j) m[j] = (done.rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
+    const bool whole = (done.rtw + 2 * RT) * 16 <= a.N;
+    load_bias(a, n, whole, bias);
     slot += gridDim.x / 8;
     const bool more = slot < end;
-    // The next tile's copies are under way while this one is finished.
     if (more) {
       at = locate(first_id + slot);
       begin();
     }
-    __builtin_amdgcn_sched_barrier(0);  // the stores come after the copies: the waits count them
-    const bool whole = (done.rtw + 2 * RT) * 16 <= a.N;
-    auto end_tile = [&](auto all) __attribute__((always_inline)) {
-      const int l = lane_here(), g = l >> 4, r = l & 15;
-      int n[2 * MI];
-      int64_t m[2 * MJ];
-#pragma unroll
-      for (int i = 0; i < 2 * MI; ++i)
-        n[i] = static_cast<int>((done.rtw + i / MI * RT + wa * MI + i % MI) * 16 + 4 * g);
-#pragma unroll
-      for (int j = 0; j < 2 * MJ; ++j) m[j] = (done.rtx + j / MJ * RT + wb * MJ + j % MJ) * 16 + r;
-      finish_stores<BF16, decltype(all)::value>(a, acc, n, m, g, whole, done.range);
-    };
-    finish_values(a, acc, bias);
-    if (more && whole && !a.part && (done.rtx + 2 * RT) * 16 <= a.M) {
-      end_tile(integral_constant<bool, true>{});
-    } else {
-      end_tile(integral_constant<bool, false>{});
-      if (!more) break;
-      __builtin_amdgcn_s_waitcnt(0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    enter(out);
-    s = 0;
-    if (at.kt1 - at.kt0 > 2) {
-      pair(out);
-      s = 2;
-    }
+    finish<BF16>(a, acc, n, m, bias, g, whole, done.range);
+    if (!more) break;
   }
 }
 
@@ -844,24 +752,25 @@ __device__ inline i32x4 load16(const char* p) {
 
 // Few rows of x.  The time is W's way out of memory, so W goes straight into
 // registers, in the order in which it is stored: no LDS, no barrier before the
-// end.  A workgroup owns 32 n and one range of k; its NW waves take turns at
+// end.  A workgroup owns 16 NT n and one range of k; its NW waves take turns at
 // the range's scale tiles (512 columns: 8 KiB of W, all loads in flight, the
 // next turn's while this one is multiplied) and add their sums in LDS, in
-// order.  Four waves, or eight where K is longer than a turn of those.
+// order.  Four waves, or eight where K is longer than a turn of those; sixteen
+// and 16 n, see few_deep.
 // With STREAM W leaves the caches to others (one row of 4096 -> 32768 12.5 us
 // instead of 13.7; but 32 rows of 25088 -> 1024, whose 13 MB stay in the caches
 // from call to call, 17.5 instead of 14.5: above kStreamBytes).
 // With RAW the workgroup quantises x itself, into LDS, before it starts: for
 // the few thousand values of one or two tokens that is quicker than a launch.
-template <bool BF16, int MT, int NW, bool RAW, bool STREAM>
+template <bool BF16, int MT, int NW, bool RAW, bool STREAM, int NT = 2>
 __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
-  constexpr int NT = 2, ES = BF16 ? 2 : 4;
+  constexpr int ES = BF16 ? 2 : 4;
   __shared__ f32x4 sums[NW][NT * MT][64];
   extern __shared__ __attribute__((aligned(16))) char raw_codes[];  // RAW: [k tile][block][M] of 16 bytes, then scales
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, r = lane & 15;
-  const int groups = (a.N + 31) / 32;
+  const int groups = (a.N + 16 * NT - 1) / (16 * NT);
   const int range = blockIdx.x / groups;
   const int64_t nt0 = static_cast<int64_t>(blockIdx.x % groups) * NT;
   const int ks_per = (a.ks + a.ranges - 1) / a.ranges;
@@ -989,11 +898,14 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
 #pragma unroll
     for (int w = 1; w < NW; ++w) out[0][i] += sums[w][wave * NT + i][lane];
   }
-  const int n[NT] = {static_cast<int>(nt0 * 16 + 4 * g), static_cast<int>(nt0 * 16 + 16 + 4 * g)};
+  int n[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) n[i] = static_cast<int>(nt0 + i) * 16 + 4 * g;
   const int64_t m[1] = {wave * 16 + r};
   f32x4 bias[NT];
-  load_bias(a, n, nt0 * 16 + 32 <= a.N, bias);
-  finish<BF16>(a, out, n, m, bias, g, nt0 * 16 + 32 <= a.N, range);
+  const bool whole = (nt0 + NT) * 16 <= a.N;
+  load_bias(a, n, whole, bias);
+  finish<BF16>(a, out, n, m, bias, g, whole, range);
 }
 
 // Small products, and many rows of few n: x is quantised on its way into the
@@ -1216,11 +1128,22 @@ void choose_kernel(fconv_mx_plan_s* p) {
   }
 }
 
+// Few outputs of a long K leave most CUs idle, and a wave's turns come one after
+// another: sixteen waves for 16 n.  @@
+bool few_deep(const fconv_mx_plan_s* p) {
+  return p->d.M <= 32 && ceil_div(p->d.N, 16) <= 256 && ceil_div(ceil_div(p->d.K, 512), p->ranges) >= 16;
+}
+
 template <bool BF16, bool STREAM>
 void launch_few(const fconv_mx_plan_s* p, const MxArgs& a, bool raw, dim3 grid, hipStream_t s) {
   if (raw)
     hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, true, STREAM>), grid, dim3(256), few_raw_bytes(p), s, a);
-  else if (ceil_div(a.ks, a.ranges) <= 4) {
+  else if (few_deep(p)) {
+    if (a.M <= 16)
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 16, false, STREAM, 1>), grid, dim3(1024), 0, s, a);
+    else
+      hipLaunchKernelGGL((mx_few_kernel<BF16, 2, 16, false, STREAM, 1>), grid, dim3(1024), 0, s, a);
+  } else if (ceil_div(a.ks, a.ranges) <= 4) {
     if (a.M <= 16)
       hipLaunchKernelGGL((mx_few_kernel<BF16, 1, 4, false, STREAM>), grid, dim3(256), 0, s, a);
     else if (a.M <= 32)
@@ -1246,7 +1169,7 @@ hipError_t launch_product(const fconv_mx_plan_s* p, MxArgs a, int kernel, hipStr
   const int64_t most = kernel == kTile256 ? 256 : 512;
   const int64_t all = ceil_div(static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.ranges, 8) * 8;
   const dim3 grid(static_cast<unsigned>(all < most ? all : most));
-  const dim3 few(static_cast<unsigned>(ceil_div(a.N, 32) * a.ranges));
+  const dim3 few(static_cast<unsigned>(ceil_div(a.N, kernel == kFew && few_deep(p) ? 16 : 32) * a.ranges));
   const dim3 rows(static_cast<unsigned>(ceil_div(a.M, 64)), static_cast<unsigned>(ceil_div(a.N, 16 * p->rows_nt)));
   switch (kernel) {
     case kTile256: hipLaunchKernelGGL((mx_tile_kernel<BF16, 128, 8>), grid, dim3(512), 0, s, a); break;

@@ -156,6 +156,17 @@ __device__ inline float exp_from(float x, float base2) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -base2));
 }
 
+// f over the four lanes l, l ^ 16, l ^ 32, l ^ 48, the same in all of them.
+template <typename F>
+__device__ inline float across(float x, F f) {
+  const uint32_t a = __builtin_bit_cast(uint32_t, x);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, static_cast<uint32_t>(p[0])),
+                                                    __builtin_bit_cast(float, static_cast<uint32_t>(p[1]))));
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return f(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])), __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
+}
+
 // base * log2 e for exp_from.  Past 2^126 the product would leave fp32: there
 // the base is taken off the logits first, and what is left counts from 0.
 template <int NI, int NJ>
@@ -268,16 +279,15 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
+      // The four lanes of a token agree on the largest first: their sums then add
+      // up without another exponential.
+      m = across(m, [](float x, float y) { return fmaxf(x, y); });
       const float base2 = base2_of(acc, j, base_of(m));
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s += exp_from(acc[i][j][e], base2);
-#pragma unroll
-      for (int x = 16; x < 64; x *= 2) {
-        const float m2 = __shfl_xor(m, x), s2 = __shfl_xor(s, x);
-        join(m, s, m2, s2);
-      }
+      s = across(s, [](float x, float y) { return x + y; });
       if (q == 0) red[wa * EDGE + b] = make_float2(m, s);
     }
     __syncthreads();
@@ -1192,12 +1202,13 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
         const int64_t at = static_cast<int64_t>(full) * STEP + k * 32;
         const int n = static_cast<int>(f.D - at) - 8 * q;
         auto part = [&](const char* p) __attribute__((always_inline)) {
+          // The row's last element stands in for those past it: asking first cost
+          // a branch for each.
           E v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = static_cast<E>(0.0f);
-            if (e < n) __builtin_memcpy(&v[e], p + (at + e) * ES, ES);
-          }
+          for (int e = 0; e < 8; ++e) __builtin_memcpy(&v[e], p + (at + (e < n ? e : n - 1)) * ES, ES);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : static_cast<E>(0.0f);
           R x;
           x.set(v, R::shift_of(p));
           return x;
@@ -1377,13 +1388,34 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
       if (i < own) n += b.x;
       m = max(m, b.y);
     }
-    for (int64_t t = own * 1024 + threadIdx.x; t < t0; t += 256) n += g.target[t] != g.ignore;
+    // At most 1023 tokens before its own in the block; all loads at once.
+    int64_t tgt[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = own * 1024 + 256 * i + threadIdx.x;
+      tgt[i] = g.target[t < t0 ? t : t0];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += own * 1024 + 256 * i + threadIdx.x < t0 && tgt[i] != g.ignore;
   } else {
-    for (int64_t t = threadIdx.x; t < g.T; t += 256)
-      if (g.target[t] != g.ignore) {
-        n += t < t0;
-        m = max(m, abs_bits(g.dloss[t]));
+    // Eight tokens of a thread in flight: one after the other they took most of the kernel's time.
+    for (int64_t first = threadIdx.x; first < g.T; first += 256 * 8) {
+      int64_t tgt[8];
+      float dl[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t t = first + 256 * i, at = t < g.T ? t : first;
+        tgt[i] = g.target[at];
+        dl[i] = g.dloss[at];
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t t = first + 256 * i;
+        if (t >= g.T || tgt[i] == g.ignore) continue;
+        n += t < t0;
+        m = max(m, abs_bits(dl[i]));
+      }
+    }
   }
   const int2 stats = block_stats(n, m);
   const int before = stats.x;
@@ -1594,13 +1626,22 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
 }
 
 // Time (us) of the few-token kernel on a piece of the vocabulary: w at 4.1, 3.2
-// or 2.5 TB/s for 16, 32 or 64 tokens (4096 x 60000 and x 30000), where the tiled
-// kernel, with most of its products idle, reaches 5.2 (loss of 64 x 4096 x 30000
-// 95 us, of 65 48); but it has the small and narrow ones (64 x 2896 x 7168: 24,
-// 65: 36).
-double few_us(int64_t T, int64_t V, int64_t D) {
-  return 4.0 + 2.0 * static_cast<double>(V) * static_cast<double>(D) / (T <= 16 ? 4.1e6 : T <= 32 ? 3.2e6 : 2.5e6);
+// or 2.5 TB/s for 16, 32 or 64 tokens (4096 x 60000 and x 30000), or what each 32
+// v cost a workgroup (fitted over D 72 .. 1024, V 600 .. 33000; `grad`: q is
+// written too).
+double few_us(int64_t T, int64_t V, int64_t D, bool grad) {
+  const int k = T <= 16 ? 0 : T <= 32 ? 1 : 2;
+  static const double rate[] = {4.1e6, 3.2e6, 2.5e6}, base[] = {0.0042, 0.0055, 0.0085},
+                      per_d[] = {0.8e-5, 1.0e-5, 1.85e-5}, store[] = {0.003, 0.004, 0.006};
+  const double memory = 4.0 + 2.0 * static_cast<double>(V) * static_cast<double>(D) / rate[k];
+  const double each = base[k] + per_d[k] * static_cast<double>(D) + (grad ? store[k] : 0.0);
+  const double work = 2.6 + static_cast<double>(ceil_div(V, 32)) * each + (D % 64 ? 1.0 : 0.0);
+  return memory > work ? memory : work;
 }
+// What choose() leaves out of the tiles' time for few tokens: nothing hides a
+// slab's latency where a workgroup is alone on its CU (59 x 1024 x 4544: 13 us
+// for 16 slabs).
+double few_tiles_us(const Split& s, int64_t D) { return s.edge == 64 ? 0.3 * static_cast<double>(ceil_div(D, 64)) : 0.0; }
 
 // Time (us) of packing a matrix: a launch, one read and one write.
 double pack_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 4e6; }
@@ -1693,7 +1734,7 @@ hipError_t run_forward(const fconv_xent_plan_s* p, const fconv_xent_args* args, 
   int tiles;
   hipError_t e;
   const bool fits = fits_tiles(args->w, args->ldw) && fits_tiles(args->h, args->ldh);
-  if (p->few_fwd || (d.T <= kFewTokens && !fits)) {
+  if (p->few_fwd || (d.T <= kFewTokens && !fits && p->logits.edge != 64)) {
     FewArgs f = few_args(p, args);
     f.part = part;
     f.target_logit = target_logit;
@@ -1772,7 +1813,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
   float* c_max = reinterpret_cast<float*>(ws + p->o_c);
   int32_t* index = reinterpret_cast<int32_t*>(ws + p->o_index);
   int32_t* n_live = reinterpret_cast<int32_t*>(ws + p->o_n);
-  const bool few = p->few_bwd || (d.T <= kFewTokens && !p->pack_bwd && !fits_tiles(args->w, args->ldw));
+  const bool few = p->few_bwd || (d.T <= kFewTokens && !p->pack_bwd && p->grad.edge != 64 && !fits_tiles(args->w, args->ldw));
   GatherArgs ga = {};
   if (few) {
     n_live = nullptr;
@@ -2013,7 +2054,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       if (piece < d.V) p->fwd_piece = static_cast<int32_t>(piece);
     }
   }
-  p->few_fwd = d.T <= kFewTokens && (!tiled || few_us(d.T, d.V, d.D) < p->logits.us);
+  p->few_fwd = d.T <= kFewTokens && few_us(d.T, d.V, d.D, false) < p->logits.us + few_tiles_us(p->logits, d.D);
   // Either kernel may run: which one depends on the pointers too.
   int64_t parts = ceil_div(d.V, 64);
   if (d.T <= kFewTokens && parts < few_groups(d.V)) parts = few_groups(d.V);
@@ -2059,7 +2100,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       p->dw = dw64;
     }
     // The gather is a launch and some microseconds more.
-    p->few_bwd = T <= kFewTokens && (!tiled || few_us(d.T, piece, d.D) < p->grad.us + 8.0);
+    p->few_bwd = T <= kFewTokens && few_us(d.T, piece, d.D, true) < p->grad.us + few_tiles_us(p->grad, d.D) + 8.0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t o = at;
