@@ -1044,6 +1044,14 @@ int few_raw_bytes(const fconv_mx_plan_s* p) {
   return static_cast<int>(ks_per * 4 * (64 + 4) * p->d.M);
 }
 
+// Few outputs of a long K leave most CUs idle, and a wave's turns come one after
+// another: sixteen waves for 16 n (32 rows of 25088 -> 1024 12.1 us instead of
+// 14.5, of 8192 -> 1024 7.8 and 8.9, 16 of 16384 -> 4096 10.7 and 12.3, with the
+// quantisation).
+bool few_deep(const fconv_mx_plan_s* p) {
+  return p->d.M <= 32 && ceil_div(p->d.N, 16) <= 256 && ceil_div(ceil_div(p->d.K, 512), p->ranges) >= 16;
+}
+
 // Time (us) of the rows kernel with NT tiles of 16 n for a wave.  A step of 128 k
 // takes a wave alone 0.6 (NT 4) or 0.7 us (NT 8); more than a wave for a SIMD add
 // up.  128 to 512 rows of 512 -> 512: 5.7 (NT 4) and 7.0, by the 128 tiles 9.7;
@@ -1070,7 +1078,9 @@ void choose_kernel(fconv_mx_plan_s* p) {
   double rows = 1e300;
   for (int nt = 4; nt <= 8; nt += 4) {
     const double us = rows_us(p->d, p->esize, nt);
-    if (ceil_div(N, 64) > 65535 || us >= rows) continue;
+    // A longer K reads x and W past what the account knows (8924 of 5696 -> 138
+    // 84 us, by the tiles 48).
+    if (ceil_div(N, 64) > 65535 || p->d.K > 2048 || us >= rows) continue;
     rows = us;
     p->rows_nt = nt;
   }
@@ -1079,19 +1089,20 @@ void choose_kernel(fconv_mx_plan_s* p) {
   double least = 1e300;
   if (M <= 64 && ceil_div(N, 32) <= kMaxGroups) {
     p->kernel = kFew;
-    // Ranges only where a wave would take more than eight turns (K > 32768):
-    // 32 rows of 25088 -> 1024 take 11.8 us in one, 10.1 us in eight and the
-    // join, which does not cover its launch.
+    // Ranges only where K > 32768: 32 rows of 25088 -> 1024 in eight of them gained
+    // less than the launch that joins them takes.
     p->ranges = static_cast<int32_t>(min_of(ceil_div(ks, 64), ceil_div(1024, ceil_div(N, 32))));
     p->ranges = static_cast<int32_t>(ceil_div(ks, ceil_div(ks, p->ranges)));
-    if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384) {
+    // At most 20 scale tiles: its four waves take them in turns (one row of 16384 ->
+    // 1024 9.9 us, of 9984 7.3).
+    if (M <= 16 && M * ceil_div(ks, p->ranges) * 512 <= 16384 && ceil_div(ks, p->ranges) <= 20) {
       p->kernel = kFewRaw;
       return;
     }
     // W at 5.2, 4.2 or 3 TB/s for 16, 32 or 64 rows (32768 x 4096: 13.7, 17.7 and
     // 24.4 us, the 128 tiles 15.9, 16.3 and 16.9).
-    // One of 25088 -> 1024 is bound by the turns' latency: 11.2 us for 32 rows.
-    const double turns = 3.0 + 3.2e-4 * static_cast<double>(p->d.K);
+    // A long K of few outputs is bound by the turns' latency.
+    const double turns = 3.0 + (few_deep(p) ? 2.4e-4 : 3.2e-4) * static_cast<double>(p->d.K);
     least = 1.5 + weights / (M <= 16 ? 5.2e6 : M <= 32 ? 4.2e6 : 3.0e6);
     least = quantise + (least > turns ? least : turns);
     if (p->ranges > 1) return;
@@ -1126,12 +1137,6 @@ void choose_kernel(fconv_mx_plan_s* p) {
     p->kernel = kRows;
     p->ranges = 1;
   }
-}
-
-// Few outputs of a long K leave most CUs idle, and a wave's turns come one after
-// another: sixteen waves for 16 n.  @@
-bool few_deep(const fconv_mx_plan_s* p) {
-  return p->d.M <= 32 && ceil_div(p->d.N, 16) <= 256 && ceil_div(ceil_div(p->d.K, 512), p->ranges) >= 16;
 }
 
 template <bool BF16, bool STREAM>

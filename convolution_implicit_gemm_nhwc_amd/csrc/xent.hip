@@ -1018,7 +1018,6 @@ struct Raw<BYTES, false> {
   __device__ F get(uint32_t) const {
     return __builtin_bit_cast(F, d);
   }
-  __device__ void set(const void* v, uint32_t) { __builtin_memcpy(&d, v, BYTES); }
 };
 
 template <int BYTES>
@@ -1045,18 +1044,52 @@ struct Raw<BYTES, true> {
     __builtin_memcpy(&f, v, BYTES);
     return f;
   }
-  // As if `v` had been loaded.
-  __device__ void set(const void* v, uint32_t shift) {
-    uint32_t u[N], below = 0;
-    __builtin_memcpy(u, v, BYTES);
+};
+
+// n (8 or more, or less than none) elements of a row of at least eight from p on,
+// zeros past them: the last eight, shifted down.  One by one they cost a load and
+// a branch each.
+template <typename F, typename R, int ES>
+__device__ inline F row_end(const char* p, int n) {
+  constexpr int N = 2 * ES, PER = 4 / ES;  // dwords of eight elements, elements of a dword
+  const char* at = n >= 8 ? p : p + (n - 8) * ES;
+  R x;
+  x.load(at);
+  const F f = x.template get<F>(R::shift_of(at));
+  uint32_t d[N];
+  __builtin_memcpy(d, &f, sizeof(d));
+  const int s = n >= 8 ? 0 : n > 0 ? 8 - n : 8;
+#pragma unroll
+  for (int by = 8; by >= PER; by /= 2)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      d[i] = shift ? u[i] << 16 | below >> 16 : u[i];
-      below = u[i];
+      const uint32_t v = i + by / PER < N ? d[i + by / PER] : 0u;
+      d[i] = s & by ? v : d[i];
     }
-    d[N] = below >> 16;
+  if constexpr (PER == 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t v = d[i] >> 16 | (i + 1 < N ? d[i + 1] << 16 : 0u);
+      d[i] = s & 1 ? v : d[i];
+    }
   }
-};
+  F r;
+  __builtin_memcpy(&r, d, sizeof(r));
+  return r;
+}
+// The same of a shorter row.
+template <typename F, typename E>
+__device__ inline F row_end_short(const char* p, int n) {
+  E v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = static_cast<E>(0.0f);
+    if (e < n) __builtin_memcpy(&v[e], p + e * sizeof(E), sizeof(E));
+  }
+  F r;
+  __builtin_memcpy(&r, v, sizeof(r));
+  return r;
+}
 
 struct FewArgs {
   const char* w;
@@ -1083,7 +1116,7 @@ struct FewArgs {
 };
 
 template <typename E, bool ODD, Epilogue EPI, int MT>
-__global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
+__global__ __launch_bounds__(256, 2) void xent_few_kernel(FewArgs f) {
   using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
   constexpr int ES = sizeof(E), NA = 2, STEP = 128 / ES, KK = STEP / 32;
   __shared__ f32x4 sums[4][MT * NA][64];
@@ -1195,30 +1228,24 @@ __global__ __launch_bounds__(256) void xent_few_kernel(FewArgs f) {
       if (step + 8 < full) load(now, step + 8);
       multiply(next);
     }
-    if (full % 4 == wave && full * STEP < f.D) {  // the rest of k, element by element
-      Turn x;
+    if (full % 4 == wave && full * STEP < f.D) {  // the rest of k
 #pragma unroll
       for (int k = 0; k < KK; ++k) {
         const int64_t at = static_cast<int64_t>(full) * STEP + k * 32;
-        const int n = static_cast<int>(f.D - at) - 8 * q;
+        const int n = static_cast<int>(f.D - at) - 8 * q;  // elements of this lane's eight
         auto part = [&](const char* p) __attribute__((always_inline)) {
-          // The row's last element stands in for those past it: asking first cost
-          // a branch for each.
-          E v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) __builtin_memcpy(&v[e], p + (at + (e < n ? e : n - 1)) * ES, ES);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : static_cast<E>(0.0f);
-          R x;
-          x.set(v, R::shift_of(p));
-          return x;
+          return f.D >= 8 ? row_end<Frag, R, ES>(p + at * ES, n) : row_end_short<Frag, E>(p + at * ES, n);
         };
+        Frag a[NA], b[MT];
 #pragma unroll
-        for (int i = 0; i < NA; ++i) x.a[i][k] = part(wp[i]);
+        for (int i = 0; i < NA; ++i) a[i] = part(wp[i]);
 #pragma unroll
-        for (int j = 0; j < MT; ++j) x.b[j][k] = part(hp[j]);
+        for (int j = 0; j < MT; ++j) b[j] = part(hp[j]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < NA; ++i) acc[j][i] = mma8(a[i], b[j], acc[j][i]);
       }
-      multiply(x);
     }
     __syncthreads();  // the sums of the group before are used
 #pragma unroll
@@ -2099,8 +2126,8 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
       p->dh = dh64;
       p->dw = dw64;
     }
-    // The gather is a launch and some microseconds more.
-    p->few_bwd = T <= kFewTokens && few_us(d.T, piece, d.D, true) < p->grad.us + few_tiles_us(p->grad, d.D) + 8.0;
+    // The gather is a launch and some microseconds more, and its rows are read again.
+    p->few_bwd = T <= kFewTokens && few_us(d.T, piece, d.D, true) < p->grad.us + few_tiles_us(p->grad, d.D) + 10.0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t o = at;

@@ -250,3 +250,36 @@ def test_same_bits_on_every_run_streams_and_graphs():
             torch.cuda.synchronize()
             assert torch.equal(y0, y2)
             plan(x, wq)
+
+
+def test_both_ways_through_a_call_agree():
+    # Without a stream a call goes through csrc/call.cpp, with one through _dense.py; also what the first leaves to the second.
+    dev = device()
+    say("ways")
+    x = _x(40, 100, "fp32", 1, dev)
+    q = fc.MxQuantPlan(40, 100, "fp32")
+    here = torch.cuda.current_stream()
+    a, b = q(x), q(x, stream=here)
+    # The gap between the last row's codes and whole tiles holds zeros in both.
+    assert torch.equal(a.data, b.data)
+    assert torch.equal(q.dequantize(a), q.dequantize(b, stream=here))
+    w = fc.MxQuantPlan(24, 100, "fp32")(_x(24, 100, "fp32", 2, dev))
+    p = fc.MxPlan(40, 24, 100, "fp32", ops=("bias", "clamp"))
+    bias = torch.ones(24, device=dev)
+    y = p(x, w, bias=bias)  # both bounds 0
+    assert torch.equal(y, p(x, w, bias=bias, stream=here)) and (y == 0).all()
+    y = p(x, w, bias=bias, activ_alpha=-1.0, activ_beta=1.0)
+    assert torch.equal(y, p(x, w, bias=bias, activ_alpha=-1.0, activ_beta=1.0, stream=here)) and (y != 0).any()
+    nhwc = x.view(2, 4, 5, 100)
+    assert torch.equal(p(nhwc, w, bias=bias), p(x, w, bias=bias))
+    param = torch.nn.Parameter(x)
+    assert torch.equal(q(param).data, a.data)
+    for bad, match in ((x.bfloat16(), "dtype"), (x[:39], "shape"), (x.cpu(), "GPU"), (x.t(), "shape")):
+        with pytest.raises(ValueError, match=match):
+            q(bad)
+        with pytest.raises(ValueError, match=match):
+            p(bad, w, bias=bias)
+    with pytest.raises(ValueError, match="different devices|GPU"):
+        p(x, w, bias=bias.cpu())
+    with pytest.raises(ValueError, match="elements"):
+        p(x, w, bias=bias[:23])

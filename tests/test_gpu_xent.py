@@ -97,6 +97,8 @@ SIZES = [(1, 1, 1), (1, 64, 500), (2, 8, 70), (3, 33, 17), (16, 100, 300), (17, 
 # At most 64 tokens, and the first number above; k of less than a step, whole steps, a ragged rest; many groups of v.
 SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576, 2000), (66, 576, 2000), (5, 40, 70001),
           (30, 64, 140000), (3, 1024, 70000)]
+# Few tokens and k of less than eight, of eight and a little, of whole steps and a ragged end; a vocabulary of dh's own kernel.
+SIZES += [(2, 3, 40), (9, 9, 1000), (20, 71, 300), (34, 199, 2048), (64, 452, 1024), (17, 600, 2049), (40, 515, 1025)]
 # Rows that are no multiple of 16 bytes, packed for the tiled kernel.
 SIZES += [(513, 1001, 3000), (700, 260, 5000), (1100, 513, 2500)]
 
@@ -416,3 +418,24 @@ def test_logits_near_the_end_of_the_range(T, D, V, value):
         adh = torch.mm(q.abs(), w.double().abs())
         # Sums past fp32's range are infinities; the other columns are of order one.
         assert ((dh.double() - rdh).abs()[:, 1:] <= (1.01 * r * (adh + rdh.abs()) + 4 * U * V * adh)[:, 1:]).all()
+
+
+def test_both_ways_through_a_call_agree():
+    # Without a stream a call goes through csrc/call.cpp, with one or with given outputs through _dense.py.
+    dev = device()
+    say("ways")
+    h, w, t, dl = _case(30, 64, 300, "bf16", 9, dev)
+    plan = fc.XentPlan(30, 64, 300, "bf16")
+    here = torch.cuda.current_stream()
+    loss, lse = plan.forward(h, w, t)
+    l2, s2 = plan.forward(h, w, t, stream=here)
+    assert torch.equal(loss, l2) and torch.equal(lse, s2)
+    dh, dw = plan.backward(h, w, t, lse, dl)
+    a, b = plan.backward(h, w, t, lse, dl, dh=torch.empty_like(dh), dw=torch.empty_like(dw))
+    assert torch.equal(dh, a) and torch.equal(dw, b)
+    for bad, match in ((dict(h=h.float()), "dtype"), (dict(h=h[:29]), "shape"), (dict(w=w.cpu()), "GPU"),
+                       (dict(target=t.int()), "dtype"), (dict(target=t[:7]), "elements")):
+        with pytest.raises(ValueError, match=match):
+            plan.forward(**dict(dict(h=h, w=w, target=t), **bad))
+    with pytest.raises(ValueError, match="dtype"):
+        plan.backward(h, w, t, lse, dl.double())
