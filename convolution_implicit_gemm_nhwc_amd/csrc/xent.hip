@@ -1402,11 +1402,12 @@ __global__ __launch_bounds__(256) void xent_count_kernel(const int64_t* target, 
   if (threadIdx.x == 0) blocks[blockIdx.x] = all;
 }
 
-// Gathers the live tokens among 16, in order: a workgroup counts the live
+// Gathers the live tokens among ROWS, in order: a workgroup counts the live
 // ones before its own and finds the largest |dloss|, then copies the rows.
-template <typename E>
+// Sixteen rows, or four where those would leave CUs idle.
+template <typename E, int ROWS>
 __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * ROWS;
   int n = 0, m = 0;
   if (g.blocks) {
     const int64_t own = t0 / 1024, blocks = (g.T + 1023) / 1024;
@@ -1449,8 +1450,8 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
   const float c = __builtin_bit_cast(float, stats.y);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t mine = t0 + lane;
-  const int64_t tgt = lane < 16 && mine < g.T ? g.target[mine] : g.ignore;
-  __shared__ float ratios[16];
+  const int64_t tgt = lane < ROWS && mine < g.T ? g.target[mine] : g.ignore;
+  __shared__ float ratios[ROWS];
   if (wave == 0 && tgt != g.ignore) ratios[lane] = c > 0.0f ? g.dloss[mine] / c : g.dloss[mine];
   __syncthreads();
   const uint64_t live = __ballot(tgt != g.ignore);
@@ -1461,13 +1462,13 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
     g.live_lse[pos] = g.lse[mine];
     g.live_dloss[pos] = g.dloss[mine];
   }
-  if (threadIdx.x == 0 && t0 + 16 >= g.T) {
+  if (threadIdx.x == 0 && t0 + ROWS >= g.T) {
     *g.n_live = before + __popcll(live);
     *g.c = c;
   }
   // The rows' pieces of 16 bytes, four of a thread in flight.
   constexpr int N = 16 / sizeof(E), U = 4;
-  const int rows = static_cast<int>(g.T - t0 < 16 ? g.T - t0 : 16);
+  const int rows = static_cast<int>(g.T - t0 < ROWS ? g.T - t0 : ROWS);
   const int per_row = static_cast<int>(g.ld_live / N), total = rows * per_row;
   for (int first = threadIdx.x; first < total; first += 256 * U) {
     E v[U][N];
@@ -1541,30 +1542,45 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const char* src, int64_t
   }
 }
 
-// C[row, a] = sum of the ranges' partial sums, in order; four a per thread.
-template <typename E>
+// C[row, a] = sum of the ranges' partial sums, in order; four a per thread.  Many
+// ranges are shared by PARTS threads, whose sums meet in LDS, in order: one after
+// another 64 of them took 6 us.
+template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void xent_sum_kernel(const float* part, int ranges, int64_t stride,
                                                        int64_t ld, int rows, const int32_t* n_live,
                                                        const int32_t* row_map, const float* scale,
                                                        int scale_step, int cols, char* out,
                                                        int64_t ld_out) {
-  const int quads = (cols + 3) / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  constexpr int QUADS = 256 / PARTS;
+  __shared__ f32x4 sums[PARTS > 1 ? 256 : 1];
+  const int quads = (cols + 3) / 4, own = threadIdx.x / QUADS;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * QUADS + threadIdx.x % QUADS;
   const int64_t row = i / quads;
   const int c = static_cast<int>(i - row * quads) * 4;
-  if (row >= (n_live ? *n_live : rows)) return;
+  const bool live = row < (n_live ? *n_live : rows);
   f32x4 s = {};
-  const float* p0 = part + row * ld + c;  // rows of ld floats, a multiple of 4
-  // Eight loads in flight; those past the last range read it again.
-  for (int k = 0; k < ranges; k += 8) {
-    f32x4 v[8];
+  if (live) {
+    const int per = (ranges + PARTS - 1) / PARTS, first = own * per, last = min(first + per, ranges);
+    const float* p0 = part + row * ld + c;  // rows of ld floats, a multiple of 4
+    // Eight loads in flight; those past the last range read it again.
+    for (int k = first; k < last; k += 8) {
+      f32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = *reinterpret_cast<const f32x4*>(p0 + (k + i < ranges ? k + i : ranges - 1) * stride);
+      for (int i = 0; i < 8; ++i)
+        v[i] = *reinterpret_cast<const f32x4*>(p0 + (k + i < last ? k + i : last - 1) * stride);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (k + i < ranges) s += v[i];
+      for (int i = 0; i < 8; ++i)
+        if (k + i < last) s += v[i];
+    }
   }
+  if constexpr (PARTS > 1) {
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (own > 0) return;
+#pragma unroll
+    for (int p = 1; p < PARTS; ++p) s += sums[p * QUADS + threadIdx.x];
+  }
+  if (!live) return;
   s *= scale[row * scale_step];
   int64_t to = row_map ? row_map[row] : row;
   if (to < 0) {
@@ -1641,7 +1657,7 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
   for (const Kind& k : kinds) {
     if (k.edge != 64 && !tiled) continue;
     const int64_t tiles = ceil_div(na, k.edge) * ceil_div(nb, k.edge), slabs = ceil_div(nk, 64);
-    for (int32_t r = 1; r <= (split ? 64 : 1) && (r == 1 || slabs / r >= 2); ++r) {
+    for (int32_t r = 1; r <= (split ? 128 : 1) && (r == 1 || slabs / r >= 2); ++r) {
       const int64_t n = tiles * r;
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
@@ -1818,9 +1834,13 @@ template <typename E>
 hipError_t launch_sum(const float* part, int ranges, int64_t stride, int64_t ld, int rows,
                       const int32_t* n_live, const int32_t* row_map, const float* scale, int scale_step,
                       int cols, char* out, int64_t ld_out, hipStream_t s) {
-  const int64_t threads = static_cast<int64_t>(rows) * ((cols + 3) / 4);
-  hipLaunchKernelGGL(xent_sum_kernel<E>, dim3(static_cast<unsigned>(ceil_div(threads, 256))), dim3(256), 0, s,
-                     part, ranges, stride, ld, rows, n_live, row_map, scale, scale_step, cols, out, ld_out);
+  const int64_t quads = static_cast<int64_t>(rows) * ((cols + 3) / 4);
+  if (ranges > 8 && quads <= 1 << 16)
+    hipLaunchKernelGGL((xent_sum_kernel<E, 8>), dim3(static_cast<unsigned>(ceil_div(quads, 32))), dim3(256), 0, s,
+                       part, ranges, stride, ld, rows, n_live, row_map, scale, scale_step, cols, out, ld_out);
+  else
+    hipLaunchKernelGGL((xent_sum_kernel<E, 1>), dim3(static_cast<unsigned>(ceil_div(quads, 256))), dim3(256), 0, s,
+                       part, ranges, stride, ld, rows, n_live, row_map, scale, scale_step, cols, out, ld_out);
   return hipGetLastError();
 }
 
@@ -1874,7 +1894,10 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       if ((e = hipGetLastError()) != hipSuccess) return e;
       ga.blocks = blocks;
     }
-    hipLaunchKernelGGL(xent_gather_kernel<E>, dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s, ga);
+    if (d.T <= 4096)
+      hipLaunchKernelGGL((xent_gather_kernel<E, 4>), dim3(static_cast<unsigned>(ceil_div(d.T, 4))), dim3(256), 0, s, ga);
+    else
+      hipLaunchKernelGGL((xent_gather_kernel<E, 16>), dim3(static_cast<unsigned>(ceil_div(d.T, 16))), dim3(256), 0, s, ga);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
 

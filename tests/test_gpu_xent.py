@@ -99,6 +99,8 @@ SIZES += [(16, 64, 33), (33, 127, 40), (48, 257, 65), (63, 1000, 999), (64, 576,
           (30, 64, 140000), (3, 1024, 70000)]
 # Few tokens and k of less than eight, of eight and a little, of whole steps and a ragged end; a vocabulary of dh's own kernel.
 SIZES += [(2, 3, 40), (9, 9, 1000), (20, 71, 300), (34, 199, 2048), (64, 452, 1024), (17, 600, 2049), (40, 515, 1025)]
+# Tokens counted in blocks, gathered by four and by sixteen; many ranges of few outputs.
+SIZES += [(2049, 40, 300), (4100, 24, 260), (3, 40, 60000), (20, 72, 40000)]
 # Rows that are no multiple of 16 bytes, packed for the tiled kernel.
 SIZES += [(513, 1001, 3000), (700, 260, 5000), (1100, 513, 2500)]
 
