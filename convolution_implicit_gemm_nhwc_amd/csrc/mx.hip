@@ -762,8 +762,10 @@ __device__ inline i32x4 load16(const char* p) {
 // from call to call, took 3 us longer: above kStreamBytes).
 // With RAW the workgroup quantises x itself, into LDS, before it starts: for
 // the few thousand values of one or two tokens that is quicker than a launch.
+// 64 rows by four waves: two waves a SIMD, where the compiler's 268 registers left
+// one (64 rows of 1024 -> 32768 12.1 us instead of 14.5, -> 2048 7.2 and 7.0).
 template <bool BF16, int MT, int NW, bool RAW, bool STREAM, int NT = 2>
-__global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
+__global__ __launch_bounds__(NW * 64, MT == 4 && NW == 4 ? 2 : 1) void mx_few_kernel(MxArgs a) {
   constexpr int ES = BF16 ? 2 : 4;
   __shared__ f32x4 sums[NW][NT * MT][64];
   extern __shared__ __attribute__((aligned(16))) char raw_codes[];  // RAW: [k tile][block][M] of 16 bytes, then scales
@@ -914,8 +916,11 @@ __global__ __launch_bounds__(NW * 64) void mx_few_kernel(MxArgs a) {
 // the rows.  A lane holds one block of 32 values of a row and step, which is the
 // matrix core's own order: the block's largest magnitude and its codes need no
 // other lane.  W comes through the caches; the next step's x is loaded meanwhile.
+// Three waves a SIMD (two with NT 8) in 145 registers, where the compiler took 180
+// by itself: 100352 rows of 256 -> 64 16.1 us instead of 17.9, 200704 of 128 -> 64
+// 18.9 and 22.0; four waves spill (28.5 us).
 template <bool BF16, int NT>
-__global__ __launch_bounds__(256) void mx_rows_kernel(MxArgs a) {
+__global__ __launch_bounds__(256, NT == 4 ? 3 : 2) void mx_rows_kernel(MxArgs a) {
   constexpr int ES = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int64_t mt = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
