@@ -25,11 +25,18 @@ loss without the logits, and 4-bit weights and activations.
 from __future__ import annotations
 
 import ctypes
+import importlib
+import importlib.util
 
 from . import _abi
 
-__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS", "MxTensor", "MxQuantPlan", "MxPlan",
-           "XentPlan"]
+# The output layer's plans take torch tensors only.  Their modules import torch and are loaded on first
+# use, so that the package can be imported, built and used with raw addresses where torch is not installed.
+_WITH_TORCH = {"MxTensor": ".mx", "MxQuantPlan": ".mx", "MxPlan": ".mx", "XentPlan": ".xent"}
+
+__all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS"]
+if importlib.util.find_spec("torch") is not None:
+    __all__ += list(_WITH_TORCH)
 
 DTYPES = {"int8": _abi.FCONV_INT8, "bf16": _abi.FCONV_BF16, "fp32": _abi.FCONV_FP32}
 OPS = {"scale": _abi.OP_SCALE, "side": _abi.OP_SIDE, "bias": _abi.OP_BIAS,
@@ -309,5 +316,13 @@ def autotune_cache_clear():
     _abi.lib().fconv_autotune_cache_clear()
 
 
-from .mx import MxPlan, MxQuantPlan, MxTensor  # noqa: E402
-from .xent import XentPlan  # noqa: E402
+def __getattr__(name):
+    if name not in _WITH_TORCH:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    value = getattr(importlib.import_module(_WITH_TORCH[name], __name__), name)
+    globals()[name] = value
+    return value
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_WITH_TORCH))

@@ -1,5 +1,6 @@
 """Build libfconv.so (the C-ABI library with its gfx950 kernels) and _call.so
-(the Python module of csrc/call.cpp) in-tree.
+(the Python module of csrc/call.cpp) in-tree.  _call.so is linked to torch and
+left out where torch is not installed: nothing that needs it works there.
 
     python -m convolution_implicit_gemm_nhwc_amd.build
 
@@ -13,6 +14,7 @@ Kernels are compiled ahead of time for gfx950 only.  Flags:
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -55,7 +57,13 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     for obj in objs:
         os.remove(obj)
-    build_call(verbose)
+    if importlib.util.find_spec("torch") is not None:
+        build_call(verbose)
+    else:
+        if os.path.exists(CALL):  # of other sources
+            os.remove(CALL)
+        print("torch is not installed: %s not built (MxPlan, MxQuantPlan, XentPlan need it)" % CALL,
+              file=sys.stderr, flush=True)
     return LIB
 
 
