@@ -6,9 +6,17 @@ from __future__ import annotations
 
 import torch
 
-from . import _check
+from . import DTYPES, _check
 
 TORCH = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def type_name(dtype):
+    """"int8", "bf16" or "fp32", of a name or of its fconv_dtype code."""
+    for name, code in DTYPES.items():
+        if dtype == name or (type(dtype) is int and dtype == code):
+            return name
+    raise ValueError("dtype %r: %s, or their codes" % (dtype, ", ".join(DTYPES)))
 
 
 def matrix(t, what, rows, cols, dtype):

@@ -18,7 +18,7 @@ import torch
 
 from . import _abi
 from . import DTYPES, OPS, _check
-from ._dense import TORCH, call, done, matrix, vector
+from ._dense import TORCH, call, done, matrix, type_name, vector
 
 __all__ = ["MxTensor", "MxQuantPlan", "MxPlan"]
 
@@ -78,6 +78,7 @@ class MxQuantPlan:
     """Quantises [rows, cols] matrices of dtype "bf16" or "fp32", and back."""
 
     def __init__(self, rows, cols, dtype="bf16"):
+        dtype = type_name(dtype)
         self.rows, self.cols, self.dtype = rows, cols, dtype
         if dtype not in TORCH:
             raise ValueError("dtype %r: bf16 or fp32" % (dtype,))
@@ -128,9 +129,10 @@ class MxPlan:
     type of x and y; ops: [bias], [relu | leaky_relu | clipped_relu | clamp]."""
 
     def __init__(self, M, N, K, dtype="bf16", ops=("bias",)):
+        dtype = type_name(dtype)
         d = _abi.MxDesc()
         d.M, d.N, d.K = M, N, K
-        d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
+        d.dtype = DTYPES[dtype]
         codes = [OPS[o] if isinstance(o, str) else int(o) for o in ops]
         if len(codes) > _abi.FCONV_MAX_OPS:
             raise ValueError("too many ops")

@@ -13,7 +13,7 @@ import torch
 
 from . import _abi
 from . import _check, DTYPES
-from ._dense import TORCH, call, done, matrix, vector
+from ._dense import TORCH, call, done, matrix, type_name, vector
 
 __all__ = ["XentPlan"]
 
@@ -24,9 +24,10 @@ class XentPlan:
     ignore_index have loss 0 and no gradient; a target outside [0, V) gives NaN."""
 
     def __init__(self, T, D, V, dtype="bf16", ignore_index=-100):
+        dtype = type_name(dtype)
         d = _abi.XentDesc()
         d.T, d.D, d.V = T, D, V
-        d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
+        d.dtype = DTYPES[dtype]
         d.ignore_index = ignore_index
         self.desc = d
         self.T, self.D, self.V, self.dtype, self.ignore_index = T, D, V, dtype, ignore_index
