@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import importlib
 import importlib.util
+import operator
 
 from . import _abi
 
@@ -55,6 +56,16 @@ class FconvError(RuntimeError):
 def _check(status: int, what: str):
     if status != _abi.FCONV_OK:
         raise FconvError(status, what)
+
+
+def _whole(what, *values, bits=32):
+    """Whole numbers as a descriptor holds them.  Its fields would take a longer
+    one's low bits without a word, and the plan would be of another size."""
+    out = tuple(operator.index(v) for v in values)
+    for v in out:
+        if not -(1 << bits - 1) <= v < 1 << bits - 1:
+            raise ValueError("%s: %d does not fit in %d bits" % (what, v, bits))
+    return out
 
 
 def _addr(t):
@@ -112,8 +123,8 @@ class Plan:
                  ops=("scale", "bias"), cudnn7_order=False):
         sh, sw = (stride, stride) if isinstance(stride, int) else stride
         d = _abi.FconvDesc()
-        d.N, d.H, d.W, d.C, d.K, d.R, d.S = N, H, W, C, K, R, S
-        d.stride_h, d.stride_w = sh, sw
+        d.N, d.H, d.W, d.C, d.K, d.R, d.S = _whole("sizes", N, H, W, C, K, R, S)
+        d.stride_h, d.stride_w = _whole("stride", sh, sw)
         d.padding = PADDINGS[padding.upper()] if isinstance(padding, str) else padding
         d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
         codes = [OPS[o] if isinstance(o, str) else int(o) for o in ops]
@@ -252,8 +263,8 @@ class WgradPlan:
                  out_fp32=False):
         sh, sw = (stride, stride) if isinstance(stride, int) else stride
         d = _abi.FconvDesc()
-        d.N, d.H, d.W, d.C, d.K, d.R, d.S = N, H, W, C, K, R, S
-        d.stride_h, d.stride_w = sh, sw
+        d.N, d.H, d.W, d.C, d.K, d.R, d.S = _whole("sizes", N, H, W, C, K, R, S)
+        d.stride_h, d.stride_w = _whole("stride", sh, sw)
         d.padding = PADDINGS[padding.upper()] if isinstance(padding, str) else padding
         d.dtype = DTYPES[dtype] if isinstance(dtype, str) else dtype
         d.n_ops = 0

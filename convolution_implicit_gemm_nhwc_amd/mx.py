@@ -17,13 +17,14 @@ import ctypes
 import torch
 
 from . import _abi
-from . import DTYPES, OPS, _check
+from . import DTYPES, OPS, _check, _whole
 from ._dense import TORCH, call, done, matrix, type_name, vector
 
 __all__ = ["MxTensor", "MxQuantPlan", "MxPlan"]
 
 
 def _mx_bytes(rows, cols):
+    rows, cols = _whole("rows and cols", rows, cols)
     n = ctypes.c_size_t()
     _check(_abi.mx_lib().fconv_mx_bytes(rows, cols, ctypes.byref(n)), "fconv_mx_bytes")
     return n.value
@@ -78,6 +79,7 @@ class MxQuantPlan:
     """Quantises [rows, cols] matrices of dtype "bf16" or "fp32", and back."""
 
     def __init__(self, rows, cols, dtype="bf16"):
+        rows, cols = _whole("rows and cols", rows, cols)
         dtype = type_name(dtype)
         self.rows, self.cols, self.dtype = rows, cols, dtype
         if dtype not in TORCH:
@@ -131,7 +133,7 @@ class MxPlan:
     def __init__(self, M, N, K, dtype="bf16", ops=("bias",)):
         dtype = type_name(dtype)
         d = _abi.MxDesc()
-        d.M, d.N, d.K = M, N, K
+        d.M, d.N, d.K = M, N, K = _whole("M, N and K", M, N, K)
         d.dtype = DTYPES[dtype]
         codes = [OPS[o] if isinstance(o, str) else int(o) for o in ops]
         if len(codes) > _abi.FCONV_MAX_OPS:

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _abi
-from . import _check, DTYPES
+from . import DTYPES, _check, _whole
 from ._dense import TORCH, call, done, matrix, type_name, vector
 
 __all__ = ["XentPlan"]
@@ -26,9 +26,9 @@ class XentPlan:
     def __init__(self, T, D, V, dtype="bf16", ignore_index=-100):
         dtype = type_name(dtype)
         d = _abi.XentDesc()
-        d.T, d.D, d.V = T, D, V
+        d.T, d.D, d.V = T, D, V = _whole("T, D and V", T, D, V)
         d.dtype = DTYPES[dtype]
-        d.ignore_index = ignore_index
+        d.ignore_index, = _whole("ignore_index", ignore_index, bits=64)
         self.desc = d
         self.T, self.D, self.V, self.dtype, self.ignore_index = T, D, V, dtype, ignore_index
         self._h = ctypes.c_void_p()

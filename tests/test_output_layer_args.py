@@ -33,3 +33,27 @@ def test_a_type_is_a_name_or_its_code(plan, name, code, dtype):
 def test_other_types_are_refused_by_name(plan, bad):
     with pytest.raises(ValueError, match="dtype"):
         MAKE[plan](bad)
+
+
+@pytest.mark.parametrize("make", [
+    lambda n: fc.MxQuantPlan(n, 40), lambda n: fc.MxQuantPlan(4, n),
+    lambda n: fc.MxPlan(n, 8, 40), lambda n: fc.MxPlan(4, n, 40), lambda n: fc.MxPlan(4, 8, n),
+    lambda n: fc.MxTensor(torch.zeros(1280, dtype=torch.uint8), n, 40),
+    lambda n: fc.MxTensor.from_codes(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8), n),
+    lambda n: fc.XentPlan(n, 40, 9), lambda n: fc.XentPlan(4, n, 9), lambda n: fc.XentPlan(4, 40, n),
+    lambda n: fc.Plan(n, 6, 5, 16, 24, 3, 3), lambda n: fc.Plan(2, 6, 5, 16, 24, 3, n),
+    lambda n: fc.Plan(2, 6, 5, 16, 24, 3, 3, stride=(n, 1)), lambda n: fc.WgradPlan(n, 6, 5, 16, 24, 3, 3)])
+def test_sizes_past_32_bits_are_refused(make):
+    # The descriptors hold 32 bits: 2^32 + 1 was taken for 1.
+    with pytest.raises(ValueError, match="32 bits"):
+        make((1 << 32) + 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        make(-(1 << 40))
+    with pytest.raises(TypeError):
+        make(3.0)
+
+
+def test_ignore_index_past_64_bits_is_refused():
+    assert fc.XentPlan(4, 40, 9, ignore_index=(1 << 63) - 1).ignore_index == (1 << 63) - 1
+    with pytest.raises(ValueError, match="64 bits"):
+        fc.XentPlan(4, 40, 9, ignore_index=(1 << 64) - 100)
