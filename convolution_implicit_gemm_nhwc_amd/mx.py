@@ -38,9 +38,16 @@ class MxTensor:
 
     def __init__(self, data, rows, cols):
         self.data, self.rows, self.cols = data, rows, cols
-        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < _mx_bytes(rows, cols):
+        self.address(_mx_bytes(rows, cols))
+
+    def address(self, nbytes):
+        """Of the buffer, which has to hold `nbytes`: asked at each use, since a
+        kernel reads that much whatever `data` has become."""
+        data = self.data
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < nbytes:
             raise ValueError("data: %d bytes needed (uint8, contiguous), got %s of %s"
-                             % (_mx_bytes(rows, cols), tuple(data.shape), data.dtype))
+                             % (nbytes, tuple(data.shape), data.dtype))
+        return data.data_ptr()
 
     @property
     def shape(self):
@@ -116,10 +123,11 @@ class MxQuantPlan:
             y = self._call.dequantize(t.data, *self._dequantize)
             if y is not None:
                 return done(y, "fconv_mx_dequantize")
+        ptr = t.address(self.bytes)
 
         def run(s, device):
             y = torch.empty(rows, cols, dtype=self._torch, device=device)
-            _check(self._lib.fconv_mx_dequantize(s, t.data.data_ptr(), rows, cols, self._code, y.data_ptr(), cols),
+            _check(self._lib.fconv_mx_dequantize(s, ptr, rows, cols, self._code, y.data_ptr(), cols),
                    "fconv_mx_dequantize")
             return y
         return call(run, stream, t.data)
@@ -154,7 +162,8 @@ class MxPlan:
         self.workspace_bytes = n.value
         self.kernel_name = L.fconv_mx_plan_kernel_name(self._h).decode()
         self._call = _abi.native()
-        self._product = (_abi.address(L.fconv_mx_plan_run), self._h.value, M, N, K, d.dtype, _mx_bytes(N, K), n.value)
+        self._x_bytes, self._w_bytes = _mx_bytes(M, K), _mx_bytes(N, K)
+        self._product = (_abi.address(L.fconv_mx_plan_run), self._h.value, M, N, K, d.dtype, self._w_bytes, n.value)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -176,15 +185,15 @@ class MxPlan:
         if isinstance(x, MxTensor):
             if x.rows != self.M or x.cols != self.K:
                 raise ValueError("x: MxTensor of %s, the plan needs %s" % (x.shape, (self.M, self.K)))
+            a.x_mx = x.address(self._x_bytes)
             x = x.data
-            a.x_mx = x.data_ptr()
         else:
             a.x, a.ldx = matrix(x, "x", self.M, self.K, self._torch)
         if not isinstance(w, MxTensor) or w.rows != self.N or w.cols != self.K:
             raise ValueError("w: an MxTensor of %s needed" % ((self.N, self.K),))
         if self._bias != (bias is not None):
             raise ValueError("bias: the plan has %s bias op" % ("a" if self._bias else "no"))
-        a.w_mx = w.data.data_ptr()
+        a.w_mx = w.address(self._w_bytes)
         if bias is not None:
             a.bias = vector(bias, "bias", self.N, torch.float32)
         a.activ_alpha, a.activ_beta = activ_alpha, activ_beta

@@ -57,3 +57,23 @@ def test_ignore_index_past_64_bits_is_refused():
     assert fc.XentPlan(4, 40, 9, ignore_index=(1 << 63) - 1).ignore_index == (1 << 63) - 1
     with pytest.raises(ValueError, match="64 bits"):
         fc.XentPlan(4, 40, 9, ignore_index=(1 << 64) - 100)
+
+
+def _mx(rows, cols, nbytes):
+    return fc.MxTensor(torch.zeros(nbytes, dtype=torch.uint8), rows, cols)
+
+
+@pytest.mark.parametrize("data", [torch.zeros(1279, dtype=torch.uint8), torch.zeros(1280, dtype=torch.int8),
+                                  torch.zeros(2560, dtype=torch.uint8)[::2]])
+def test_a_buffer_that_was_exchanged_is_looked_at_again(data):
+    # The size was asked only when the MxTensor was made; kernels read it all.
+    p = fc.MxPlan(4, 8, 40, "fp32", ops=())
+    x, w = _mx(4, 40, 1280), _mx(8, 40, 1280)
+    x.data = data
+    with pytest.raises(ValueError, match="1280 bytes"):
+        p(x, w)
+    x, w.data = _mx(4, 40, 1280), data
+    with pytest.raises(ValueError, match="1280 bytes"):
+        p(x, w)
+    with pytest.raises(ValueError, match="1280 bytes"):
+        fc.MxQuantPlan(8, 40, "fp32").dequantize(w)
