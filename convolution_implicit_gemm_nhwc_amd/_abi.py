@@ -130,7 +130,7 @@ FCONV_MX_MAX_K = 1 << 22
 # Every symbol include/fconv_mx.h declares.
 MX_EXPORTS = ("fconv_mx_bytes", "fconv_mx_quantize", "fconv_mx_dequantize", "fconv_mx_layout",
               "fconv_mx_plan_create", "fconv_mx_plan_workspace_size", "fconv_mx_plan_run",
-              "fconv_mx_plan_kernel_name", "fconv_mx_plan_destroy")
+              "fconv_mx_plan_kernel_name", "fconv_mx_plan_quantized_kernel_name", "fconv_mx_plan_destroy")
 
 
 class MxDesc(ctypes.Structure):
@@ -165,8 +165,9 @@ def mx_lib():
         L.fconv_mx_plan_destroy.argtypes = [P]
         for name in MX_EXPORTS:
             getattr(L, name).restype = st
-        L.fconv_mx_plan_kernel_name.argtypes = [P]
-        L.fconv_mx_plan_kernel_name.restype = ctypes.c_char_p
+        for name in ("fconv_mx_plan_kernel_name", "fconv_mx_plan_quantized_kernel_name"):
+            getattr(L, name).argtypes = [P]
+            getattr(L, name).restype = ctypes.c_char_p
         _mx_lib = L
     return _mx_lib
 

@@ -33,11 +33,11 @@ struct fconv_mx_plan_s {
   int32_t act;      // 0 none, 1 ReLU, 2 leaky, 3 clipped, 4 clamp
   int32_t kt;       // 128-column k tiles
   int32_t kernel;   // fconv::Kernel
+  int32_t kernel_mx;  // of a run whose x comes quantised
   int32_t rows_nt;  // of the rows kernel: tiles of 16 n for a wave
   int32_t ranges;   // of k, whose partial sums a second kernel joins
   size_t ws_x;      // bytes of the quantised x in the workspace
   size_t ws_bytes;
-  const char* kernel_name;
 };
 
 namespace fconv {
@@ -1352,7 +1352,8 @@ fconv_status fconv_mx_plan_create(const fconv_mx_desc* desc, fconv_mx_plan* out)
     p->ws_x = (codes_bytes(d.M, d.K) + scales_bytes(d.M, d.K) + 255) / 256 * 256;
   p->ws_bytes = p->ws_x;
   if (p->ranges > 1) p->ws_bytes += static_cast<size_t>(p->ranges) * d.M * ceil_div(d.N, 4) * 16;
-  p->kernel_name = kKernelNames[p->kernel];
+  // What quantises x itself has no form for one that is quantised.
+  p->kernel_mx = p->kernel == kFewRaw ? kFew : p->kernel != kRows ? p->kernel : d.M <= 64 ? kFew : kTile128;
   *out = p;
   return FCONV_OK;
 }
@@ -1377,10 +1378,8 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   if (!args->w_mx || !args->y || (p->op_bias && !args->bias)) return FCONV_ERR_INVALID_ARG;
   if ((args->x && bad_ld(args->ldx, d.M, d.K)) || bad_ld(args->ldy, d.M, d.N)) return FCONV_ERR_INVALID_ARG;
   // An x that comes quantised needs no place in the workspace.
-  int kernel = p->kernel;
+  const int kernel = args->x ? p->kernel : p->kernel_mx;
   const bool by_itself = args->x && (kernel == kFewRaw || kernel == kRows);
-  if (!args->x && kernel == kFewRaw) kernel = kFew;
-  if (!args->x && kernel == kRows) kernel = d.M <= 64 ? kFew : kTile128;
   const size_t ws = args->x ? p->ws_bytes : p->ws_bytes - p->ws_x;
   if (ws > 0 && (!args->workspace || args->workspace_bytes < p->ws_bytes)) return FCONV_ERR_WORKSPACE;
   if (!aligned(args->x, p->esize) || !aligned(args->y, p->esize) || !aligned(args->x_mx, 16) ||
@@ -1434,7 +1433,10 @@ fconv_status fconv_mx_plan_run(fconv_mx_plan p, void* stream, const fconv_mx_arg
   return e == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
 }
 
-const char* fconv_mx_plan_kernel_name(fconv_mx_plan p) { return p ? p->kernel_name : nullptr; }
+const char* fconv_mx_plan_kernel_name(fconv_mx_plan p) { return p ? fconv::kKernelNames[p->kernel] : nullptr; }
+const char* fconv_mx_plan_quantized_kernel_name(fconv_mx_plan p) {
+  return p ? fconv::kKernelNames[p->kernel_mx] : nullptr;
+}
 
 fconv_status fconv_mx_plan_destroy(fconv_mx_plan p) {
   delete p;

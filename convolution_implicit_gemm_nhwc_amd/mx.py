@@ -136,7 +136,9 @@ class MxQuantPlan:
 class MxPlan:
     """y[m, n] = act(sum_k X[m, k] W[n, k] + bias[n]) with X and W in MXFP4.
     A dense layer, or a 1x1 convolution over M = N*H*W pixels.  dtype is the
-    type of x and y; ops: [bias], [relu | leaky_relu | clipped_relu | clamp]."""
+    type of x and y; ops: [bias], [relu | leaky_relu | clipped_relu | clamp].
+    kernel_name is the kernel of a tensor x, quantized_kernel_name that of an
+    MxTensor."""
 
     def __init__(self, M, N, K, dtype="bf16", ops=("bias",)):
         dtype = type_name(dtype)
@@ -161,6 +163,7 @@ class MxPlan:
         _check(L.fconv_mx_plan_workspace_size(self._h, ctypes.byref(n)), "fconv_mx_plan_workspace_size")
         self.workspace_bytes = n.value
         self.kernel_name = L.fconv_mx_plan_kernel_name(self._h).decode()
+        self.quantized_kernel_name = L.fconv_mx_plan_quantized_kernel_name(self._h).decode()
         self._call = _abi.native()
         self._x_bytes, self._w_bytes = _mx_bytes(M, K), _mx_bytes(N, K)
         self._product = (_abi.address(L.fconv_mx_plan_run), self._h.value, M, N, K, d.dtype, self._w_bytes, n.value)

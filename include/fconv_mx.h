@@ -114,8 +114,10 @@ FCONV_API fconv_status fconv_mx_plan_workspace_size(fconv_mx_plan plan, size_t* 
 FCONV_API fconv_status fconv_mx_plan_run(fconv_mx_plan plan, void* stream,
                                          const fconv_mx_args* args);
 
-/* Name of the product kernel the plan launches; NULL for a NULL plan. */
+/* Name of the product kernel that a run launches, given x or given x_mx; NULL
+ * for a NULL plan. */
 FCONV_API const char* fconv_mx_plan_kernel_name(fconv_mx_plan plan);
+FCONV_API const char* fconv_mx_plan_quantized_kernel_name(fconv_mx_plan plan);
 FCONV_API fconv_status fconv_mx_plan_destroy(fconv_mx_plan plan);
 
 #ifdef __cplusplus

@@ -77,3 +77,13 @@ def test_a_buffer_that_was_exchanged_is_looked_at_again(data):
         p(x, w)
     with pytest.raises(ValueError, match="1280 bytes"):
         fc.MxQuantPlan(8, 40, "fp32").dequantize(w)
+
+
+@pytest.mark.parametrize("M,N,K,given,quantized", [(1, 1000, 512, "mx_few_raw", "mx_few"), (500, 200, 512, "mx_rows", "mx_tile_128"),
+                                                   (40, 100, 260, "mx_rows", "mx_few"), (32, 1024, 25088, "mx_few", "mx_few"),
+                                                   (8192, 8192, 4096, "mx_tile_256", "mx_tile_256")])
+def test_kernel_names_of_a_tensor_and_of_a_quantised_x(M, N, K, given, quantized):
+    # A run whose x comes quantised was said to take a kernel that quantises x itself.
+    p = fc.MxPlan(M, N, K, "bf16")
+    assert (p.kernel_name, p.quantized_kernel_name) == (given, quantized)
+    assert _abi.mx_lib().fconv_mx_plan_quantized_kernel_name(None) is None
