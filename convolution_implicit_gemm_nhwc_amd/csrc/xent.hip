@@ -64,9 +64,10 @@ struct Operand {
   int64_t width;  // kRow: readable elements of a row
 };
 
-// kEpiStream: kEpiOut past the caches.
-enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart, kEpiStream };
+// kEpiStream: kEpiOut past the caches.  kEpiAdd: kEpiPart added to what is there.
+enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart, kEpiStream, kEpiAdd };
 constexpr bool is_out(Epilogue e) { return e == kEpiOut || e == kEpiStream; }
+constexpr bool is_part(Epilogue e) { return e == kEpiPart || e == kEpiAdd; }
 
 struct GemmArgs {
   Operand a, b;
@@ -76,7 +77,8 @@ struct GemmArgs {
   const int32_t* n_live;
   int32_t ranges;   // of k; the partial sums of each go out apart
   // kEpiLse: partial (max, sum) at [tile of a][ld_out + b]; kEpiGrad: g;
-  // kEpiOut: C; kEpiPart: fp32 C of this range at range * nb_max * ld_out.
+  // kEpiOut: C; kEpiPart, kEpiAdd: fp32 C of this range at range * part_stride,
+  // whose rows are whole 16 bytes.
   char* out;
   int64_t ld_out;
   int64_t part_stride;        // elements between ranges
@@ -242,8 +244,8 @@ template <Epilogue EPI, int NJ>
 __device__ inline void have_per_b(PerB<EPI, NJ>& p) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    if constexpr (EPI != kEpiPart) asm volatile("" : "+v"(p.at[j]));
-    if constexpr (EPI != kEpiPart && EPI != kEpiLse) asm volatile("" : "+v"(p.f[j]));
+    if constexpr (!is_part(EPI)) asm volatile("" : "+v"(p.at[j]));
+    if constexpr (!is_part(EPI) && EPI != kEpiLse) asm volatile("" : "+v"(p.f[j]));
   }
 }
 
@@ -338,8 +340,23 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
     }
   } else {
     using O = std::conditional_t<is_out(EPI), E, float>;
+    // kEpiAdd: what is there, the next b's on its way while this one is added to
+    // (rows past the last one, and places past a row's end, read others again).
+    f32x4 old[EPI == kEpiAdd ? 2 : 1][NI];
+    auto load_old = [&](int j) __attribute__((always_inline)) {
+      const char* p = g.out + (range * g.part_stride + (b0 + min(b_of(j), rb - 1)) * g.ld_out + a0) * 4;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        old[j & 1][i] = *reinterpret_cast<const f32x4*>(p + (a_of(i) < ra ? a_of(i) : 0) * 4);
+    };
+    if constexpr (EPI == kEpiAdd) load_old(0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
+      if constexpr (EPI == kEpiAdd) {
+        if (j + 1 < NJ) load_old(j + 1);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i][j] += old[j & 1][i];
+      }
       const int b = b_of(j);
       if (b >= rb) continue;
       int64_t row = b0 + b;
@@ -353,7 +370,7 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
           for (int i = 0; i < NI; ++i) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
       }
-      char* out = g.out + ((EPI == kEpiPart ? range * g.part_stride : 0) + row * g.ld_out + a0) *
+      char* out = g.out + ((is_part(EPI) ? range * g.part_stride : 0) + row * g.ld_out + a0) *
                               static_cast<int64_t>(sizeof(O));
       if (whole) {
         if constexpr (sizeof(O) == 2) {
@@ -1638,7 +1655,7 @@ struct fconv_xent_plan_s {
 namespace fconv {
 namespace {
 
-// Of q at a time.  Fewer pieces mean fewer partial sums of dh; it is far from
+// Of q at a time.  Fewer pieces mean that dh's sums are added to less often; it is far from
 // the caches' size either way (8192 x 512 x 65536, both passes: 128 MB 2355 us,
 // 256 MB 2192, 512 MB 2077, 1 GB 2043).
 constexpr int64_t kGBytes = 512ll << 20;
@@ -1647,6 +1664,8 @@ constexpr int64_t kGBytes = 512ll << 20;
 // workgroups take turns on the device, each turn as long as its slabs of 64 k
 // and what a tile costs beside them; the ranges' partial sums are written and
 // read once more.
+// Those fill at most kGBytes, as a piece of q does: what a call needs beside its
+// inputs and outputs stays linear in the tokens and in the vocabulary.
 Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
   struct Kind {
     int32_t edge;
@@ -1658,7 +1677,7 @@ Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
   for (const Kind& k : kinds) {
     if (k.edge != 64 && !tiled) continue;
     const int64_t tiles = ceil_div(na, k.edge) * ceil_div(nb, k.edge), slabs = ceil_div(nk, 64);
-    for (int32_t r = 1; r <= (split ? 128 : 1) && (r == 1 || slabs / r >= 2); ++r) {
+    for (int32_t r = 1; r <= (split ? 128 : 1) && (r == 1 || (slabs / r >= 2 && r * na * nb * 4 <= kGBytes)); ++r) {
       const int64_t n = tiles * r;
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
@@ -1947,7 +1966,8 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     }
     if (e != hipSuccess) return e;
 
-    // dh of this piece: written at once, or as partial sums that the last piece joins.
+    // dh of this piece: written at once, or as the ranges' partial sums, to which
+    // every further piece adds its own and which are joined after the last one.
     const bool dh_whole = p->pieces * p->dh.ranges == 1;
     const int dh_edge = w_fits ? p->dh.edge : 64;
     GemmArgs h = {};
@@ -1967,7 +1987,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
     } else {
       h.ld_out = round_up(d.D, 4);
       h.part_stride = h.ld_out * d.T;
-      h.out = ws + p->o_dh + static_cast<size_t>(h.part_stride) * 4 * i * h.ranges;
+      h.out = ws + p->o_dh;
     }
     const bool dw_whole = p->dw.ranges == 1;
     // dw goes past the caches where it is larger than the L2s together and
@@ -2020,17 +2040,20 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
       const dim3 grid(static_cast<unsigned>(ta * (ceil_div(d.T, 64) * h.ranges + ceil_div(nv, 64))));
       if (dh_whole)
         hipLaunchKernelGGL((xent_gen_grads_kernel<E, kEpiOut>), grid, dim3(256), 0, s, h, c);
+      else if (i > 0)
+        hipLaunchKernelGGL((xent_gen_grads_kernel<E, kEpiAdd>), grid, dim3(256), 0, s, h, c);
       else
         hipLaunchKernelGGL((xent_gen_grads_kernel<E, kEpiPart>), grid, dim3(256), 0, s, h, c);
       e = hipGetLastError();
     } else {
       if (args->dh)
         e = dh_whole ? launch_gemm<E, kRow, kSum, kEpiOut>(h, dh_edge, s)
+            : i > 0  ? launch_gemm<E, kRow, kSum, kEpiAdd>(h, dh_edge, s)
                      : launch_gemm<E, kRow, kSum, kEpiPart>(h, dh_edge, s);
       if (e == hipSuccess && args->dw) e = launch_dw(c);
     }
     if (e == hipSuccess && args->dh && !dh_done && !dh_whole && i == p->pieces - 1)
-      e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), p->pieces * h.ranges, h.part_stride,
+      e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dh), h.ranges, h.part_stride,
                         h.ld_out, d.T, n_live, index, live_dloss, 1, d.D, static_cast<char*>(args->dh),
                         args->lddh, s);
     if (e == hipSuccess && args->dw && !dw_whole)
@@ -2170,8 +2193,7 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->o_blocks = take(ceil_div(T, 1024) * 8);
     p->o_rh = take(static_cast<size_t>(T) * p->ld_live * p->es);
     p->o_w = take(p->pack_bwd ? static_cast<size_t>(piece) * p->ld_pack * 2 : 0);
-    const size_t dh_parts = static_cast<size_t>(p->pieces) * p->dh.ranges;
-    p->o_dh = take(dh_parts > 1 ? dh_parts * T * ld4 : 0);
+    p->o_dh = take(p->pieces > 1 || p->dh.ranges > 1 ? static_cast<size_t>(p->dh.ranges) * T * ld4 : 0);
     p->o_dw = take(p->dw.ranges > 1 ? static_cast<size_t>(p->dw.ranges) * piece * ld4 : 0);
     p->bwd_bytes = at;
   }
