@@ -47,7 +47,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int64_t kMaxGroups = (1 << 23) - 8;  // a launch's threads stay below 2^32
+// What the launches' grids and their whole numbers hold.  Tiles of 64 x 64 logits:
+// those of 128 are counted in 32 bits.  Elements of dh, and of a piece's w: a thread
+// of a join takes four of them, and a launch's threads stay below 2^32.  Tokens:
+// tiles of 64 in grid.y.
+constexpr int64_t kMaxTiles = 1ll << 28, kMaxSum = 1ll << 33, kMaxGridY = 65535;
 constexpr int64_t kMaxLd = 1 << 21;
 constexpr int32_t kMaxD = 1 << 20, kMaxTV = 1 << 24;
 
@@ -1608,14 +1612,13 @@ __global__ __launch_bounds__(256) void xent_sum_kernel(const float* part, int ra
   store4<E>(out + (to * ld_out + c) * static_cast<int64_t>(sizeof(E)), s, cols - c);
 }
 
-// Zeros (dw of no tokens).
+// Zeros (dw of no tokens), of any number of elements.
 template <typename E>
 __global__ __launch_bounds__(256) void xent_zero_kernel(char* out, int64_t ld, int64_t rows, int cols) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = i / cols;
-  if (row >= rows) return;
   const E z = static_cast<E>(0.0f);
-  __builtin_memcpy(out + (row * ld + i % cols) * static_cast<int64_t>(sizeof(E)), &z, sizeof(E));
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256)
+      __builtin_memcpy(out + (row * ld + c) * static_cast<int64_t>(sizeof(E)), &z, sizeof(E));
 }
 
 }  // namespace
@@ -1871,8 +1874,7 @@ hipError_t run_backward(const fconv_xent_plan_s* p, const fconv_xent_args* args,
   hipError_t e;
   if (d.T == 0) {
     if (!args->dw) return hipSuccess;
-    const int64_t n = static_cast<int64_t>(d.V) * d.D;
-    hipLaunchKernelGGL(xent_zero_kernel<E>, dim3(static_cast<unsigned>(ceil_div(n, 256))), dim3(256), 0, s,
+    hipLaunchKernelGGL(xent_zero_kernel<E>, dim3(d.V < 4096 ? d.V : 4096), dim3(256), 0, s,
                        static_cast<char*>(args->dw), args->lddw, static_cast<int64_t>(d.V), d.D);
     return hipGetLastError();
   }
@@ -2106,10 +2108,8 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
   if (d.flags) return FCONV_ERR_UNSUPPORTED;
   if (d.T < 0 || d.D < 1 || d.V < 1) return FCONV_ERR_INVALID_ARG;
   if (d.D > kMaxD || d.T > kMaxTV || d.V > kMaxTV) return FCONV_ERR_UNSUPPORTED;
-  // Every launch stays below kMaxGroups workgroups (and 65535 in grid.y).
-  if (ceil_div(d.T, 64) > 65535 || ceil_div(d.V, 64) * ceil_div(d.T, 64) > kMaxGroups ||
-      ceil_div(d.D, 64) * ceil_div(d.T, 64) > kMaxGroups || ceil_div(d.V, 256) * d.D > kMaxGroups ||
-      ceil_div(d.T, 256) * d.D > kMaxGroups)
+  if (ceil_div(d.T, 64) > kMaxGridY || ceil_div(d.V, 64) * ceil_div(d.T, 64) > kMaxTiles ||
+      static_cast<int64_t>(d.T) * d.D > kMaxSum)
     return FCONV_ERR_UNSUPPORTED;
   fconv_xent_plan_s* p = new (std::nothrow) fconv_xent_plan_s();
   if (!p) return FCONV_ERR_INVALID_ARG;
@@ -2146,7 +2146,8 @@ fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan
     p->ld_live = round_up(d.D, 64);
     int64_t piece = kGBytes / (T * p->es) / 256 * 256;
     if (piece < 256) piece = 256;
-    if (piece > 65535 * 64) piece = 65535 * 64;  // grid.y of dw
+    if (piece > kMaxGridY * 64) piece = kMaxGridY * 64;  // grid.y of dw
+    if (piece > kMaxSum / d.D / 256 * 256) piece = kMaxSum / d.D / 256 * 256;
     if (piece > d.V) piece = d.V;
     p->pieces = static_cast<int32_t>(ceil_div(d.V, piece));
     // Pieces of about the same length.

@@ -69,7 +69,8 @@ typedef struct {
 
 /* Host only.  T may be 0 (backward then writes dw = 0).  Errors:
  * FCONV_ERR_INVALID_ARG (NULL, T < 0, D < 1, V < 1), FCONV_ERR_UNSUPPORTED
- * (dtype, flags, D above 2^20, T or V above 2^24). */
+ * (dtype, flags, D above 2^20, V above 2^24, T above 4194240, T * D above 2^33,
+ * or more than 2^28 tiles of 64 x 64 logits: T * V above about 2^40). */
 FCONV_API fconv_status fconv_xent_plan_create(const fconv_xent_desc* desc, fconv_xent_plan* out);
 FCONV_API fconv_status fconv_xent_plan_forward_workspace_size(fconv_xent_plan plan, size_t* bytes);
 FCONV_API fconv_status fconv_xent_plan_backward_workspace_size(fconv_xent_plan plan, size_t* bytes);

@@ -30,7 +30,7 @@ def case(T, D, V, dtype, dev, seed=1):
     return h, w, t, dl
 
 
-def _sums(a, b, n):
+def sum_error(a, b, n):
     """4 u n s of a [m, n] times b [n, k], s the root mean square of a sum's products."""
     return 4 * U * n * torch.mm(a * a, b * b).div_(max(n, 1)).sqrt_()
 
@@ -50,7 +50,7 @@ def check(h, w, t, dl, loss, lse, dh, dw, dtype, chunk):
         hd, keep = h[s].double(), t[s] != IGN
         z = torch.mm(hd, wd.t())
         l = torch.logsumexp(z, 1)
-        ez = _sums(hd, wd.t(), D)
+        ez = sum_error(hd, wd.t(), D)
         p = (z - l.unsqueeze(1)).exp_()
         # exp's argument: two roundings of z - max; the sum of V terms is tree-like.
         el = (p * ez).sum(1) * 1.01 + (p * (2 * (z - z.amax(1, keepdim=True)).abs() + 4)).sum(1) * U \
@@ -67,7 +67,7 @@ def check(h, w, t, dl, loss, lse, dh, dw, dtype, chunk):
         eq = (ep * 1.01 + (rq + 2 * U) * q.abs()) * d.abs()
         g = q * d
         rdh = torch.mm(g, wd)
-        edh = 1.01 * torch.mm(eq, wd.abs()) + _sums(g, wd, V) + ro * rdh.abs() + 1e-37
+        edh = 1.01 * torch.mm(eq, wd.abs()) + sum_error(g, wd, V) + ro * rdh.abs() + 1e-37
         assert bool(((dh[s].double() - rdh).abs() <= edh).all())
         hk = torch.where(keep.unsqueeze(1), hd, 0)
         rdw += torch.mm(g.t(), hk)
