@@ -179,7 +179,10 @@ FCONV_XENT_MAX_LD = 1 << 21
 # Every symbol include/fconv_xent.h declares.
 XENT_EXPORTS = ("fconv_xent_plan_create", "fconv_xent_plan_forward_workspace_size",
                 "fconv_xent_plan_backward_workspace_size", "fconv_xent_plan_forward",
-                "fconv_xent_plan_backward", "fconv_xent_plan_destroy")
+                "fconv_xent_plan_backward", "fconv_xent_plan_kernel_name", "fconv_xent_plan_division",
+                "fconv_xent_plan_destroy")
+
+XENT_PRODUCTS = ("logits", "grad", "dh", "dw")  # FCONV_XENT_LOGITS ..
 
 
 class XentDesc(ctypes.Structure):
@@ -211,8 +214,12 @@ def xent_lib():
         L.fconv_xent_plan_forward.argtypes = [P, P, ctypes.POINTER(XentArgs)]
         L.fconv_xent_plan_backward.argtypes = [P, P, ctypes.POINTER(XentArgs)]
         L.fconv_xent_plan_destroy.argtypes = [P]
+        i32 = ctypes.POINTER(ctypes.c_int32)
+        L.fconv_xent_plan_kernel_name.argtypes = [P, ctypes.c_int32]
+        L.fconv_xent_plan_division.argtypes = [P, ctypes.c_int32, i32, i32]
         for name in XENT_EXPORTS:
             getattr(L, name).restype = st
+        L.fconv_xent_plan_kernel_name.restype = ctypes.c_char_p
         _xent_lib = L
     return _xent_lib
 

@@ -2261,6 +2261,32 @@ fconv_status fconv_xent_plan_backward(fconv_xent_plan p, void* stream, const fco
   return e == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
 }
 
+const char* fconv_xent_plan_kernel_name(fconv_xent_plan p, int32_t product) {
+  using namespace fconv;
+  if (!p || p->d.T == 0 || product < FCONV_XENT_LOGITS || product > FCONV_XENT_DW) return nullptr;
+  const Split* const splits[] = {&p->logits, &p->grad, &p->dh, &p->dw};
+  const bool packed = product == FCONV_XENT_LOGITS ? p->pack_fwd : product != FCONV_XENT_DW && p->pack_bwd;
+  if (product == FCONV_XENT_LOGITS && p->few_fwd) return "xent_few";
+  if (product == FCONV_XENT_GRAD && p->few_bwd) return "xent_few";
+  if (product == FCONV_XENT_DH && p->few_bwd && p->d.V <= few_dh_v(p->d.T)) return "xent_few_grads";
+  const int edge = splits[product]->edge;
+  if (edge == 64) return packed ? "xent_gen_64_packed" : "xent_gen_64";
+  if (edge == 128) return packed ? "xent_tile_128_packed" : "xent_tile_128";
+  return packed ? "xent_tile_256_packed" : "xent_tile_256";
+}
+
+fconv_status fconv_xent_plan_division(fconv_xent_plan p, int32_t product, int32_t* pieces, int32_t* ranges) {
+  using namespace fconv;
+  if (!p || !pieces || !ranges || product < FCONV_XENT_LOGITS || product > FCONV_XENT_DW) return FCONV_ERR_INVALID_ARG;
+  const bool logits = product == FCONV_XENT_LOGITS;
+  *pieces = p->d.T == 0 ? 0 : logits ? static_cast<int32_t>(ceil_div(p->d.V, p->fwd_piece)) : p->pieces;
+  *ranges = p->d.T == 0                  ? 0
+            : product == FCONV_XENT_DH ? p->dh.ranges
+            : product == FCONV_XENT_DW ? p->dw.ranges
+                                       : 1;
+  return FCONV_OK;
+}
+
 fconv_status fconv_xent_plan_destroy(fconv_xent_plan p) {
   delete p;
   return FCONV_OK;

@@ -54,6 +54,18 @@ class XentPlan:
             self._destroy(h)
             self._h = None
 
+    def kernel_name(self, product):
+        """Of "logits", "grad" (the backward pass's logits), "dh" or "dw"; None without tokens."""
+        name = self._lib.fconv_xent_plan_kernel_name(self._h, _abi.XENT_PRODUCTS.index(product))
+        return name and name.decode()
+
+    def division(self, product):
+        """(pieces of the vocabulary, ranges of the sum) of a product."""
+        pieces, ranges = ctypes.c_int32(), ctypes.c_int32()
+        _check(self._lib.fconv_xent_plan_division(self._h, _abi.XENT_PRODUCTS.index(product), ctypes.byref(pieces),
+                                                  ctypes.byref(ranges)), "fconv_xent_plan_division")
+        return pieces.value, ranges.value
+
     def _inputs(self, h, w, target):
         a = _abi.XentArgs()
         a.h, a.ldh = matrix(h, "h", self.T, self.D, self._torch)

@@ -83,6 +83,17 @@ FCONV_API fconv_status fconv_xent_plan_forward(fconv_xent_plan plan, void* strea
 FCONV_API fconv_status fconv_xent_plan_backward(fconv_xent_plan plan, void* stream,
                                                 const fconv_xent_args* args);
 
+/* The products of a plan: the forward pass's logits, the backward pass's (which
+ * leave it as softmax - onehot), dh and dw.  Name of the kernel, "_packed" where
+ * rows of w are copied to 16-byte boundaries first, of a run whose operands are
+ * aligned as torch allocates them with dense rows; NULL for a NULL plan, another
+ * product, or a plan of no tokens. */
+enum { FCONV_XENT_LOGITS, FCONV_XENT_GRAD, FCONV_XENT_DH, FCONV_XENT_DW };
+FCONV_API const char* fconv_xent_plan_kernel_name(fconv_xent_plan plan, int32_t product);
+/* Pieces of the vocabulary that the product is taken in, and ranges of its sum. */
+FCONV_API fconv_status fconv_xent_plan_division(fconv_xent_plan plan, int32_t product, int32_t* pieces,
+                                                int32_t* ranges);
+
 FCONV_API fconv_status fconv_xent_plan_destroy(fconv_xent_plan plan);
 
 #ifdef __cplusplus
