@@ -44,13 +44,19 @@ FCONV_API fconv_status fconv_mx_bytes(int32_t rows, int32_t cols, size_t* bytes)
 
 /* x [rows, cols] (fconv_dtype FCONV_BF16 or FCONV_FP32; row r at element
  * r * ldx, ldx >= cols) into the buffer `mx`.  Rows of any alignment that the
- * element type has.  `mx` is 16-byte aligned and does not overlap x. */
+ * element type has.  `mx` is 16-byte aligned and does not overlap x.  This one
+ * and the two below: FCONV_ERR_INVALID_ARG (rows < 0, cols < 1, a stride below
+ * cols or past the address space, NULL, an overlap), FCONV_ERR_UNSUPPORTED
+ * (dtype, cols above 2^22, more than 2^23 - 8 tiles of 16 rows x 512 columns),
+ * FCONV_ERR_MISALIGNED, FCONV_ERR_DEVICE; rows of 0 are a no-op. */
 FCONV_API fconv_status fconv_mx_quantize(void* stream, const void* x, int64_t ldx, int32_t rows,
                                          int32_t cols, int32_t dtype, void* mx);
 
 /* The values that `mx` stands for, into y [rows, cols] (row r at r * ldy),
  * exact in fp32; in bf16 exact too, except below its smallest normal, where
- * they round to nearest even. */
+ * they round to nearest even.  Scale bytes 253 and 254, which quantisation
+ * never makes, can stand for magnitudes of 2^128 and more: those become
+ * infinities. */
 FCONV_API fconv_status fconv_mx_dequantize(void* stream, const void* mx, int32_t rows,
                                            int32_t cols, int32_t dtype, void* y, int64_t ldy);
 
@@ -102,8 +108,8 @@ typedef struct {
 
 /* Host only.  M may be 0 (every run is then a no-op).  Errors:
  * FCONV_ERR_INVALID_ARG (NULL, M < 0, N < 1, K < 1),
- * FCONV_ERR_UNSUPPORTED (dtype, ops, flags, K above 2^22, or 2^23 or more output
- * tiles of 128 x 128 or row tiles x scale tiles of x). */
+ * FCONV_ERR_UNSUPPORTED (dtype, ops, flags, K above 2^22, or more than 2^23 - 8 output
+ * tiles of 128 x 128 or tiles of 16 rows x 512 columns of x). */
 FCONV_API fconv_status fconv_mx_plan_create(const fconv_mx_desc* desc, fconv_mx_plan* out);
 FCONV_API fconv_status fconv_mx_plan_workspace_size(fconv_mx_plan plan, size_t* bytes);
 
