@@ -800,8 +800,7 @@ __global__ __launch_bounds__(NW * 64, MT == 4 && NW == 4 ? 2 : 1) void mx_few_ke
     i32x4 w[NT][4], x[RAW ? 1 : MT][4];
     int ws[NT], xs[RAW ? 1 : MT];
   };
-  // k tiles past the last one read the last one again, against zeros of x (the
-  // tail of `multiply`).
+  // k tiles past the last one read the last one again; `multiply` skips them.
   auto load = [&](Turn& t, int ks) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -872,11 +872,11 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
   Feed<OB, H, NW> fb;
   fa.init(g.a, wave, lane);
   fb.init(g.b, wave, lane);
-    // Past the last slab the copies bring zeros that nobody uses.
-    auto advance = [&]() __attribute__((always_inline)) {
-      fa.next();
-      fb.next();
-    };
+  // Past the last slab the copies bring zeros that nobody uses.
+  auto advance = [&]() __attribute__((always_inline)) {
+    fa.next();
+    fb.next();
+  };
   // The first two slabs of a tile.
   auto begin = [&](const Place& p) __attribute__((always_inline)) {
     fa.start(g.a, p.a0, OA == kRow ? g.a.width - p.a0 : p.ra, p.k0, p.k1);
@@ -892,77 +892,77 @@ __global__ __launch_bounds__(NW * 64, 2) void xent_tile_kernel(GemmArgs g) {
     fa.copy(1, a11, wave);
     advance();
   };
-    Frags<OA, H, MI> pa;
-    Frags<OB, H, MJ> pb;
-    pa.init(wa, lane);
-    pb.init(wb, lane);
-    // Fragments [tile][step] of a half of A, but for the first EARLY tiles' first
-    // step of A1, which are read while A0 is in use; and of the halves of B.
-    constexpr int EARLY = MI == 4 ? 2 : 0;
-    bf16x8 xa[MI][2], xe[EARLY + 1], xb[2][MJ][2];
-    auto read_b = [&](bf16x8 (&x)[MJ][2], const char* buf) __attribute__((always_inline)) {
+  Frags<OA, H, MI> pa;
+  Frags<OB, H, MJ> pb;
+  pa.init(wa, lane);
+  pb.init(wb, lane);
+  // Fragments [tile][step] of a half of A, but for the first EARLY tiles' first
+  // step of A1, which are read while A0 is in use; and of the halves of B.
+  constexpr int EARLY = MI == 4 ? 2 : 0;
+  bf16x8 xa[MI][2], xe[EARLY + 1], xb[2][MJ][2];
+  auto read_b = [&](bf16x8 (&x)[MJ][2], const char* buf) __attribute__((always_inline)) {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int j = 0; j < MJ; ++j) x[j][kk] = pb.one(buf, j, kk);
-    };
-    auto read_a_rest = [&](const char* buf) __attribute__((always_inline)) {
+      for (int j = 0; j < MJ; ++j) x[j][kk] = pb.one(buf, j, kk);
+  };
+  auto read_a_rest = [&](const char* buf) __attribute__((always_inline)) {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int i = kk == 0 ? EARLY : 0; i < MI; ++i) xa[i][kk] = pa.one(buf, i, kk);
-    };
-    auto read_step_ends = [&]() __attribute__((always_inline)) {
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    auto multiply = [&](int i2, int j2, const bf16x8 (&b)[MJ][2]) __attribute__((always_inline)) {
-      __builtin_amdgcn_s_setprio(1);
+      for (int i = kk == 0 ? EARLY : 0; i < MI; ++i) xa[i][kk] = pa.one(buf, i, kk);
+  };
+  auto read_step_ends = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's LDS reads are done
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](int i2, int j2, const bf16x8 (&b)[MJ][2]) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int j = 0; j < MJ; ++j)
-            acc[i2 * MI + i][j2 * MJ + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                i2 == 1 && kk == 0 && i < EARLY ? xe[i] : xa[i][kk], b[j][kk], acc[i2 * MI + i][j2 * MJ + j], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // b0 holds this slab's B0 and gets nothing; b1 gets B1, then the next slab's B0.
-    auto slab = [&](char* ab, char* b1b, char* a1b, const char* ab_next, bf16x8 (&b0)[MJ][2], bf16x8 (&b1)[MJ][2])
-                    __attribute__((always_inline)) {
-      read_a_rest(ab);
-      __builtin_amdgcn_s_waitcnt(0x0F78);  // vmcnt(8): this slab is here
-      read_step_ends();
-      multiply(0, 0, b0);
+        for (int j = 0; j < MJ; ++j)
+          acc[i2 * MI + i][j2 * MJ + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              i2 == 1 && kk == 0 && i < EARLY ? xe[i] : xa[i][kk], b[j][kk], acc[i2 * MI + i][j2 * MJ + j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // b0 holds this slab's B0 and gets nothing; b1 gets B1, then the next slab's B0.
+  auto slab = [&](char* ab, char* b1b, char* a1b, const char* ab_next, bf16x8 (&b0)[MJ][2], bf16x8 (&b1)[MJ][2])
+                  __attribute__((always_inline)) {
+    read_a_rest(ab);
+    __builtin_amdgcn_s_waitcnt(0x0F78);  // vmcnt(8): this slab is here
+    read_step_ends();
+    multiply(0, 0, b0);
 
-      read_b(b1, b1b);
+    read_b(b1, b1b);
 #pragma unroll
-      for (int i = 0; i < EARLY; ++i) xe[i] = pa.one(a1b, i, 0);
-      fa.copy(0, ab, wave);
-      fb.copy(0, ab + HB, wave);
-      read_step_ends();
-      multiply(0, 1, b1);
+    for (int i = 0; i < EARLY; ++i) xe[i] = pa.one(a1b, i, 0);
+    fa.copy(0, ab, wave);
+    fb.copy(0, ab + HB, wave);
+    read_step_ends();
+    multiply(0, 1, b1);
 
-      read_a_rest(a1b);
-      fb.copy(1, b1b, wave);
-      __builtin_amdgcn_s_waitcnt(0x0F7A);  // vmcnt(10): the next slab's A0 and B0 are here
-      read_step_ends();
-      multiply(1, 1, b1);
+    read_a_rest(a1b);
+    fb.copy(1, b1b, wave);
+    __builtin_amdgcn_s_waitcnt(0x0F7A);  // vmcnt(10): the next slab's A0 and B0 are here
+    read_step_ends();
+    multiply(1, 1, b1);
 
-      read_b(b1, ab_next + HB);
+    read_b(b1, ab_next + HB);
 #pragma unroll
-      for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab_next, i, 0);
-      fa.copy(1, a1b, wave);
-      advance();
-      read_step_ends();
-      multiply(1, 0, b0);
-    };
+    for (int i = 0; i < EARLY; ++i) xa[i][0] = pa.one(ab_next, i, 0);
+    fa.copy(1, a1b, wave);
+    advance();
+    read_step_ends();
+    multiply(1, 0, b0);
+  };
 
   if (at.slabs > 0) begin(at);
   for (;;) {
