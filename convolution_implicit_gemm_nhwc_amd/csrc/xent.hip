@@ -162,6 +162,12 @@ __device__ inline float exp_from(float x, float base2) {
   return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, -base2));
 }
 
+// A token's factor of dh.  An infinite dloss has NaN gradients: times a sum of
+// products of both signs it would be an infinity here and a NaN there.
+__device__ inline float dh_factor(float dloss) {
+  return __builtin_fabsf(dloss) < __builtin_inff() ? dloss : __builtin_nanf("");
+}
+
 // f over the four lanes l, l ^ 16, l ^ 32, l ^ 48, the same in all of them.
 template <typename F>
 __device__ inline float across(float x, F f) {
@@ -1174,7 +1180,7 @@ __global__ __launch_bounds__(256, 2) void xent_few_kernel(FewArgs f) {
     if (blockIdx.x == 0 && wave == 0) {
       if (lane < f.T) {
         f.row_map[lane] = live ? lane : -1 - lane;
-        f.live_dloss[lane] = live ? f.dloss[lane] : 0.0f;
+        f.live_dloss[lane] = live ? dh_factor(f.dloss[lane]) : 0.0f;
       }
       if (lane == 0) *f.c = c;
     }
@@ -1482,7 +1488,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
     g.index[pos] = static_cast<int32_t>(mine);
     g.live_target[pos] = tgt >= 0 && tgt < g.V ? static_cast<int32_t>(tgt) : -1;
     g.live_lse[pos] = g.lse[mine];
-    g.live_dloss[pos] = g.dloss[mine];
+    g.live_dloss[pos] = dh_factor(g.dloss[mine]);
   }
   if (threadIdx.x == 0 && t0 + ROWS >= g.T) {
     *g.n_live = before + __popcll(live);
