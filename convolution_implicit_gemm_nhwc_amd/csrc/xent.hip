@@ -16,10 +16,12 @@
 // infinities) reaches a sum.
 //
 // Roundings of bf16 inputs' gradients.  q is rounded to bf16 (the matrix
-// cores' type): at most 2^-9 of a value below 1, where dloss q, at the same
-// cost, would be off by as much as 2^-8 and, with the mean's equal dloss, by
-// the same factor in every token (measured on 32 tokens of 1000 classes: error of dw
-// 0.0037 against 0.0018).
+// cores' type), by half a step, 2^-8 of itself, at most.  dloss q, at the same cost,
+// would be off by as much and, with the mean's equal dloss, by the same factor
+// in every token (measured on 32 tokens of 1000 classes: error of dw 0.0037 against
+// 0.0018).  Two bf16 parts of q would take 10 T D V operations instead of 6; the
+// gradients' error against 64 bits is 0.0017 of their norm either way, that of
+// their own rounding to bf16 (perf/operators.py's cases, with q in fp32 and here).
 // r h is rounded to bf16 too, exactly where all dloss are equal.
 //
 // Every product has the form C[b, a] = sum_k A(a, k) B(b, k) with a contiguous
@@ -725,8 +727,10 @@ __global__ __launch_bounds__(256) void xent_few_grads_kernel(GemmArgs dh, GemmAr
 // reads, in phase 2 for A0 and B0 of the next slab and in phase 0 for this
 // one's others.
 //
-// Measured: 8192 x 4096 x 32768 logits 1.60 ms, 1.38 PFLOP/s; the matrix cores
-// are busy 74% of the cycles, at 1.86 GHz: power bounds the clock.
+// Measured: 8192 x 4096 x 32768 logits 1.60 to 1.68 ms from box to box, 1.31 to
+// 1.38 PFLOP/s; the matrix cores are busy 71% of the cycles, at 1.8 GHz: power
+// bounds the clock.  Of its gradient's products the logits 66% (q is written), dh
+// 66%, dw 71%.
 //
 // LDS order.  kSum: rows of 64 k (128 bytes), the 16-byte piece c of row r at
 // c ^ (r % 8): eight consecutive lanes of a fragment read hit eight places.
