@@ -33,7 +33,8 @@ from . import _abi
 
 # The output layer's plans take torch tensors only.  Their modules import torch and are loaded on first
 # use, so that the package can be imported, built and used with raw addresses where torch is not installed.
-_WITH_TORCH = {"MxTensor": ".mx", "MxQuantPlan": ".mx", "MxPlan": ".mx", "XentPlan": ".xent"}
+_WITH_TORCH = {"MxTensor": ".mx", "MxQuantPlan": ".mx", "MxPlan": ".mx", "XentPlan": ".xent",
+               "GatedPlan": ".gated"}
 
 __all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS"]
 if importlib.util.find_spec("torch") is not None:

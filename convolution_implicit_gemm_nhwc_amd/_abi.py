@@ -224,6 +224,56 @@ def xent_lib():
     return _xent_lib
 
 
+# --- include/fconv_gated.h (bound on first use, as above) -------------------
+
+# Every symbol include/fconv_gated.h declares.
+GATED_EXPORTS = ("fconv_gated_plan_create", "fconv_gated_plan_kept_size",
+                 "fconv_gated_plan_forward_workspace_size", "fconv_gated_plan_backward_workspace_size",
+                 "fconv_gated_plan_forward", "fconv_gated_plan_backward", "fconv_gated_plan_kernel_name",
+                 "fconv_gated_plan_ranges", "fconv_gated_plan_destroy")
+
+ACTIVATIONS = ("silu", "gelu", "gelu_tanh", "relu")  # FCONV_ACT_SILU ..
+GATED_PRODUCTS = ("forward", "dx", "dw")  # FCONV_GATED_FORWARD ..
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "F", "dtype", "activation")] + \
+               [("flags", ctypes.c_uint32)]
+
+
+class GatedArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("kept", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p),
+                ("lddw", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+_gated_lib = None
+
+
+def gated_lib():
+    """The loaded library with the symbols of include/fconv_gated.h declared."""
+    global _gated_lib
+    if _gated_lib is None:
+        L = lib()
+        P, i32, size = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)
+        L.fconv_gated_plan_create.argtypes = [ctypes.POINTER(GatedDesc), ctypes.POINTER(P)]
+        for name in ("kept", "forward_workspace", "backward_workspace"):
+            getattr(L, "fconv_gated_plan_%s_size" % name).argtypes = [P, size]
+        L.fconv_gated_plan_forward.argtypes = [P, P, ctypes.POINTER(GatedArgs)]
+        L.fconv_gated_plan_backward.argtypes = [P, P, ctypes.POINTER(GatedArgs)]
+        L.fconv_gated_plan_kernel_name.argtypes = [P, i32]
+        L.fconv_gated_plan_ranges.argtypes = [P, i32, ctypes.POINTER(i32)]
+        L.fconv_gated_plan_destroy.argtypes = [P]
+        for name in GATED_EXPORTS:
+            getattr(L, name).restype = ctypes.c_int
+        L.fconv_gated_plan_kernel_name.restype = ctypes.c_char_p
+        _gated_lib = L
+    return _gated_lib
+
+
 # --- csrc/call.cpp: the short way through a call --------------------------
 
 _call = None

@@ -28,7 +28,7 @@ CALL = os.path.join(PKG, "_call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["plan.cpp", "conv.hip", "wgrad.hip", "mx.hip", "xent.hip"]
+SOURCES = ["plan.cpp", "conv.hip", "wgrad.hip", "mx.hip", "xent.hip", "gated.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-fast-math",
           "-Wall", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,596 @@
+// Gated feed-forward layer on gfx950 (CDNA4), its gradients, and their C ABI
+// (include/fconv_gated.h).
+//
+//   [g u] = x w^T     y = act(g) u     dg = dy u act'(g)     du = dy act(g)
+//   dx = [dg du] w    dw = [dg du]^T x
+//
+// The products as gemm.h has them, C[b, a] = sum_k A(a, k) B(b, k):
+//   forward  a = f, b = t, k = d: A = w, B = x, both with k contiguous; a tile
+//            holds the same f of g and of u, so y leaves the registers as a product
+//   dx       a = d, b = t, k = g's f, then u's: A = w with a contiguous, B = [dg du]
+//   dw       a = d, b = g's f, then u's, k = t: A = x, B = [dg du], a and b contiguous
+//
+// g and u are kept in the operands' type for the gradients: computing them again
+// would take half as much as the gradients' own products (4 T D F operations
+// beside 8), reading them back takes 4 T F bytes of bf16.  Their rounding is off
+// by 2^-9 of themselves on average, half of what a bf16 gradient's own rounding is.
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <new>
+#include <type_traits>
+
+#include "fconv_gated.h"
+#include "gemm.h"
+
+namespace fconv {
+namespace {
+
+static_assert(kSilu == FCONV_ACT_SILU && kGelu == FCONV_ACT_GELU && kGeluTanh == FCONV_ACT_GELU_TANH &&
+                  kActRelu == FCONV_ACT_RELU,
+              "activations as the header counts them");
+
+// ------------------------------------------------------------- few tokens
+//
+// At most 64 tokens: the time is w's way out of memory, so fragments of both
+// operands go straight into registers, from any address, without LDS or
+// barriers.  A workgroup owns 16 f of both projections and up to 64 tokens (32
+// with ODD, whose fragments take more registers); its NW waves take turns at
+// steps of 128 bytes of k, the next turn's loads in flight, and add their sums
+// in LDS, in order; wave j then finishes tokens 16 j .. + 15.
+struct GatedFew {
+  const char* w;
+  int64_t ldw;
+  const char* x;
+  int64_t ldx;
+  char* y;
+  int64_t ldy;
+  char* kept;
+  int64_t ld_kept;
+  int32_t T, D, F, act;
+};
+
+template <typename E, bool ODD, int MT, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
+  using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
+  using R = Raw<8 * sizeof(E), ODD>;
+  constexpr int ES = sizeof(E), STEP = 128 / ES, KK = STEP / 32;
+  __shared__ f32x4 sums[NW][MT * 2][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  // Tokens from t0 on; workgroups of the same f and other tokens follow on the same XCD (every eighth).
+  const int halves = (f.T + 16 * MT - 1) / (16 * MT);
+  const int t0 = static_cast<int>(blockIdx.x / 8 % halves) * 16 * MT;
+  const int f0 = static_cast<int>(blockIdx.x / (8 * halves) * 8 + blockIdx.x % 8) * 16;
+  if (f0 >= f.F) return;
+  const int full = f.D / STEP;  // whole steps
+
+  // Rows past the last one read it again; they are not stored.
+  const char *xp[MT], *wp[2];
+  uint32_t sa[2], sb[MT];  // steps are whole dwords: the same in all of them
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    xp[j] = f.x + (static_cast<int64_t>(min(t0 + 16 * j + r, f.T - 1)) * f.ldx + 8 * q) * ES;
+    sb[j] = R::shift_of(xp[j]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    wp[i] = f.w + ((static_cast<int64_t>(i) * f.F + min(f0 + r, f.F - 1)) * f.ldw + 8 * q) * ES;
+    sa[i] = R::shift_of(wp[i]);
+  }
+  f32x4 acc[MT][2] = {};
+  struct Turn {
+    R a[2][KK], b[MT][KK];
+  };
+  auto load = [&](Turn& x, int step) __attribute__((always_inline)) {
+    const int64_t at = static_cast<int64_t>(step) * 128;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x.a[i][k].load(wp[i] + at + k * 32 * ES);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) x.b[j][k].load(xp[j] + at + k * 32 * ES);
+    }
+  };
+  auto multiply = [&](const Turn& x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      Frag a[2], b[MT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = x.a[i][k].template get<Frag>(sa[i]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) b[j] = x.b[j][k].template get<Frag>(sb[j]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[j][i] = mma8(a[i], b[j], acc[j][i]);
+    }
+  };
+  Turn now, next;
+  int step = wave;
+  if (step < full) load(now, step);
+  for (; step < full; step += 2 * NW) {
+    if (step + NW < full) load(next, step + NW);
+    multiply(now);
+    if (step + NW >= full) break;
+    if (step + 2 * NW < full) load(now, step + 2 * NW);
+    multiply(next);
+  }
+  if (full % NW == wave && full * STEP < f.D) {  // the rest of k
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int64_t at = static_cast<int64_t>(full) * STEP + k * 32;
+      const int n = static_cast<int>(f.D - at) - 8 * q;  // elements of this lane's eight
+      auto part = [&](const char* p) __attribute__((always_inline)) {
+        return f.D >= 8 ? row_end<Frag, R, ES>(p + at * ES, n) : row_end_short<Frag, E>(p + at * ES, n);
+      };
+      Frag a[2], b[MT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i] = part(wp[i]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) b[j] = part(xp[j]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[j][i] = mma8(a[i], b[j], acc[j][i]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sums[wave][j * 2 + i][lane] = acc[j][i];
+  __syncthreads();
+  const int t = t0 + 16 * wave + r, at = f0 + 4 * q;
+  if (wave >= MT || t >= f.T || at >= f.F) return;
+  f32x4 z[2][1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    z[i][0] = sums[0][wave * 2 + i][lane];
+#pragma unroll
+    for (int x = 1; x < NW; ++x) z[i][0] += sums[x][wave * 2 + i][lane];
+  }
+  if (f.kept) {
+    char* row = f.kept + (2 * t * f.ld_kept + at) * ES;
+    store4<E>(row, z[0][0], f.F - at);
+    store4<E>(row + f.ld_kept * ES, z[1][0], f.F - at);
+  }
+  activate(z, 0, f.act);
+  store4<E>(f.y + (t * f.ldy + at) * ES, z[0][0] * z[1][0], f.F - at);
+}
+
+// ----------------------------------------------------------------- dg and du
+//
+// [dg du] in rows of ld_dz, zeros past 2 F up to a multiple of eight (the tiled
+// kernel multiplies whole pieces of 16 bytes of them by zeros).  A thread takes
+// eight f of a row: 3 T F elements are read and 2 T F written.
+struct GatedDz {
+  const char* kept;
+  int64_t ld_kept;
+  const char* dy;
+  int64_t lddy;
+  char* dz;
+  int64_t ld_dz;
+  int32_t T, F, act;
+};
+
+template <typename E>
+__device__ inline void dz_values(const E* g, const E* u, const E* dy, E* dg, E* du, int act) {
+  auto by = [&](auto grad) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 a = grad(static_cast<float>(g[e]));
+      const float d = static_cast<float>(dy[e]);
+      dg[e] = static_cast<E>(d * static_cast<float>(u[e]) * a.y);
+      du[e] = static_cast<E>(d * a.x);
+    }
+  };
+  switch (act) {
+    case kSilu: return by(act_grad<kSilu>);
+    case kGelu: return by(act_grad<kGelu>);
+    case kGeluTanh: return by(act_grad<kGeluTanh>);
+    default: return by(act_grad<kActRelu>);
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
+  constexpr int64_t ES = sizeof(E);
+  const uint32_t per_row = static_cast<uint32_t>(z.ld_kept / 8);
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;  // below 2^30: T F is at most 2^32
+  const int64_t row = i / per_row;
+  if (row >= z.T) return;
+  const int c = static_cast<int>(i - static_cast<uint32_t>(row) * per_row) * 8;
+  const int n = min(z.F - c, 8);
+  E g[8], u[8], dy[8], dg[8], du[8];
+  const char* kept = z.kept + (2 * row * z.ld_kept + c) * ES;
+  __builtin_memcpy(g, __builtin_assume_aligned(kept, 16), sizeof(g));
+  __builtin_memcpy(u, __builtin_assume_aligned(kept + z.ld_kept * ES, 16), sizeof(u));
+  const char* src = z.dy + (row * z.lddy + c) * ES;
+  if (n == 8) {
+    __builtin_memcpy(dy, src, sizeof(dy));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dy[e] = static_cast<E>(0.0f);
+      if (e < n) __builtin_memcpy(&dy[e], src + e * ES, ES);
+    }
+  }
+  dz_values(g, u, dy, dg, du, z.act);
+  char* to = z.dz + (row * z.ld_dz + c) * ES;
+  if (n == 8) {
+    __builtin_memcpy(__builtin_assume_aligned(to, 16), dg, sizeof(dg));
+    __builtin_memcpy(to + z.F * ES, du, sizeof(du));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) {
+        __builtin_memcpy(to + e * ES, &dg[e], ES);
+        __builtin_memcpy(to + (z.F + e) * ES, &du[e], ES);
+      }
+    // The row's last thread: zeros up to the next multiple of eight of 2 F.
+    const E zero = static_cast<E>(0.0f);
+    for (int e = 2 * z.F; e & 7; ++e) __builtin_memcpy(z.dz + (row * z.ld_dz + e) * ES, &zero, ES);
+  }
+}
+
+// Both gradients in one launch: the first workgroups take dx's tiles and
+// ranges, the others dw's.
+template <typename E, Epilogue EPI_DX>
+__global__ __launch_bounds__(256) void gated_gen_grads_kernel(GemmArgs dx, GemmArgs dw) {
+  __shared__ GenLds<E> lds;
+  const int ta = (dx.na + 63) / 64, tb = (dx.nb + 63) / 64, n_dx = ta * tb * dx.ranges;
+  int i = blockIdx.x;
+  if (i < n_dx) {
+    gen_tile<E, kRow, kSum, EPI_DX>(dx, lds, i % ta, i / ta % tb, i / ta / tb);
+  } else {
+    i -= n_dx;
+    gen_tile<E, kRow, kRow, kEpiStore>(dw, lds, i % ta, i / ta, 0);
+  }
+}
+
+}  // namespace
+}  // namespace fconv
+
+struct fconv_gated_plan_s {
+  fconv_gated_desc d;
+  int32_t es;
+  int64_t ld_kept;  // F in whole 16 bytes: kept is [T, 2, ld_kept]
+  size_t kept_bytes;
+  bool few;                       // at most kFewTokens, by their own kernel
+  bool pack_fwd, pack_dx;         // rows of bf16 copied to 16-byte boundaries: x and w; w
+  fconv::Split fwd, dx, dw;
+  int64_t ld_pack;
+  size_t fwd_x, fwd_w, fwd_bytes;
+  int64_t ld_dz;
+  size_t o_dz, o_x, o_w, o_dx, o_dw, bwd_bytes;
+};
+
+namespace fconv {
+namespace {
+
+constexpr int32_t kFewTokens = 64;
+
+// Time (us) of the few-token kernel: w at 4.1, 3.2 or 2.5 TB/s for 16, 32 or 64
+// tokens, or what a workgroup's steps and its launch cost.
+double few_us(int64_t T, int64_t F, int64_t D, int es) {
+  const int k = T <= 16 ? 0 : T <= 32 ? 1 : 2;
+  static const double rate[] = {4.1e6, 3.2e6, 2.5e6}, each[] = {0.8e-5, 1.0e-5, 1.85e-5};
+  const double memory = 4.0 + 2.0 * es * static_cast<double>(F) * static_cast<double>(D) / rate[k];
+  const double work = 2.6 + static_cast<double>(ceil_div(F, 16)) * (0.005 + each[k] * static_cast<double>(D));
+  return memory > work ? memory : work;
+}
+
+template <typename E, bool ODD>
+hipError_t launch_few_of(const GatedFew& f, hipStream_t s) {
+  const int64_t groups = round_up(ceil_div(f.F, 16), 8);
+  const dim3 grid(static_cast<unsigned>(ODD ? groups * ceil_div(f.T, 32) : groups));
+  if (f.T <= 16) {
+    hipLaunchKernelGGL((gated_few_kernel<E, ODD, 1, 4>), grid, dim3(256), 0, s, f);
+  } else if (ODD || f.T <= 32) {
+    hipLaunchKernelGGL((gated_few_kernel<E, ODD, 2, 4>), grid, dim3(256), 0, s, f);
+  } else {
+    if constexpr (!ODD) hipLaunchKernelGGL((gated_few_kernel<E, ODD, 4, 4>), grid, dim3(256), 0, s, f);
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t run_forward(const fconv_gated_plan_s* p, const fconv_gated_args* args, hipStream_t s) {
+  const fconv_gated_desc& d = p->d;
+  char* ws = static_cast<char*>(args->workspace);
+  Operand w = {static_cast<const char*>(args->w), args->ldw, d.F};
+  Operand x = {static_cast<const char*>(args->x), args->ldx, 0};
+  const bool fits = fits_tiles(w.p, w.ld) && fits_tiles(x.p, x.ld);
+  if (p->few || (d.T <= kFewTokens && !fits && p->fwd.edge != 64)) {
+    const GatedFew f = {w.p, w.ld, x.p, x.ld, static_cast<char*>(args->y), args->ldy, static_cast<char*>(args->kept),
+                        p->ld_kept, d.T, d.D, d.F, d.activation};
+    if constexpr (sizeof(E) == 2) {
+      if (odd_rows(w) || odd_rows(x)) return launch_few_of<E, true>(f, s);
+    }
+    return launch_few_of<E, false>(f, s);
+  }
+  int edge = p->fwd.edge;
+  hipError_t e;
+  if (p->pack_fwd) {
+    if ((e = launch_pack(x.p, x.ld, d.T, d.D, ws + p->fwd_x, p->ld_pack, s)) != hipSuccess) return e;
+    if ((e = launch_pack(w.p, w.ld, 2ll * d.F, d.D, ws + p->fwd_w, p->ld_pack, s)) != hipSuccess) return e;
+    x = {ws + p->fwd_x, p->ld_pack, 0};
+    w = {ws + p->fwd_w, p->ld_pack, d.F};
+  } else if (!fits) {
+    edge = 64;
+  }
+  GemmArgs g = {};
+  g.a = w;
+  g.b = x;
+  g.na = d.F;
+  g.nb = d.T;
+  g.nk = d.D;
+  g.ranges = 1;
+  g.out = static_cast<char*>(args->y);
+  g.ld_out = args->ldy;
+  g.act = d.activation;
+  g.kept = static_cast<char*>(args->kept);
+  g.ld_kept = p->ld_kept;
+  return launch_gemm<E, kSum, kSum, kEpiGated>(g, edge, s);
+}
+
+template <typename E>
+hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* args, hipStream_t s) {
+  const fconv_gated_desc& d = p->d;
+  char* ws = static_cast<char*>(args->workspace);
+  char* dw = static_cast<char*>(args->dw);
+  char* dx = static_cast<char*>(args->dx);
+  const int32_t F2 = 2 * d.F;
+  hipError_t e;
+  if (d.T == 0) {
+    if (!dw) return hipSuccess;
+    hipLaunchKernelGGL(gemm_zero_kernel<E>, dim3(F2 < 4096 ? F2 : 4096), dim3(256), 0, s, dw, args->lddw,
+                       static_cast<int64_t>(F2), d.D);
+    return hipGetLastError();
+  }
+  const GatedDz z = {static_cast<const char*>(args->kept), p->ld_kept, static_cast<const char*>(args->dy), args->lddy,
+                     ws + p->o_dz, p->ld_dz, d.T, d.F, d.activation};
+  hipLaunchKernelGGL(gated_dz_kernel<E>, dim3(static_cast<unsigned>(ceil_div(d.T * (p->ld_kept / 8), 256))), dim3(256), 0,
+                     s, z);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+
+  Operand w = {static_cast<const char*>(args->w), args->ldw, d.D};
+  Operand x = {static_cast<const char*>(args->x), args->ldx, d.D};
+  const int dx_edge = p->pack_dx || fits_tiles(w.p, w.ld) ? p->dx.edge : 64;
+  const bool dx_whole = p->dx.ranges == 1, dw_whole = p->dw.ranges == 1;
+  if (dx && p->pack_dx) {
+    if ((e = launch_pack(w.p, w.ld, F2, d.D, ws + p->o_w, p->ld_pack, s)) != hipSuccess) return e;
+    w = {ws + p->o_w, p->ld_pack, p->ld_pack};
+  }
+  if (dw && p->dw.edge != 64 && !fits_tiles(x.p, x.ld)) {
+    if ((e = launch_pack(x.p, x.ld, d.T, d.D, ws + p->o_x, p->ld_pack, s)) != hipSuccess) return e;
+    x = {ws + p->o_x, p->ld_pack, p->ld_pack};
+  }
+  GemmArgs gx = {};
+  gx.a = w;
+  gx.b = Operand{ws + p->o_dz, p->ld_dz, 0};
+  gx.na = d.D;
+  gx.nb = d.T;
+  gx.nk = F2;
+  gx.ranges = p->dx.ranges;
+  gx.out = dx_whole ? dx : ws + p->o_dx;
+  gx.ld_out = dx_whole ? args->lddx : round_up(d.D, 4);
+  gx.part_stride = gx.ld_out * d.T;
+  GemmArgs gw = {};
+  gw.a = x;
+  gw.b = Operand{ws + p->o_dz, p->ld_dz, round_up(F2, 8)};
+  gw.na = d.D;
+  gw.nb = F2;
+  gw.nk = d.T;
+  gw.ranges = p->dw.ranges;
+  gw.out = dw_whole ? dw : ws + p->o_dw;
+  gw.ld_out = dw_whole ? args->lddw : round_up(d.D, 4);
+  gw.part_stride = gw.ld_out * F2;
+  if (dx && dw && dx_edge == 64 && p->dw.edge == 64 && dw_whole) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(d.D, 64) * (ceil_div(d.T, 64) * gx.ranges + ceil_div(F2, 64))));
+    if (dx_whole)
+      hipLaunchKernelGGL((gated_gen_grads_kernel<E, kEpiStore>), grid, dim3(256), 0, s, gx, gw);
+    else
+      hipLaunchKernelGGL((gated_gen_grads_kernel<E, kEpiPart>), grid, dim3(256), 0, s, gx, gw);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else {
+    if (dx) {
+      e = dx_whole ? launch_gemm<E, kRow, kSum, kEpiStore>(gx, dx_edge, s)
+                   : launch_gemm<E, kRow, kSum, kEpiPart>(gx, dx_edge, s);
+      if (e != hipSuccess) return e;
+    }
+    if (dw) {
+      // Past the caches where dw is larger than the L2s together and written in whole lines.
+      const bool past = p->es == 2 && static_cast<int64_t>(F2) * d.D * 2 > (32 << 20) && d.D % 64 == 0 &&
+                        args->lddw % 64 == 0 && (reinterpret_cast<uintptr_t>(dw) & 127) == 0;
+      e = !dw_whole ? launch_gemm<E, kRow, kRow, kEpiPart>(gw, p->dw.edge, s)
+          : past    ? launch_gemm<E, kRow, kRow, kEpiStoreStream>(gw, p->dw.edge, s)
+                    : launch_gemm<E, kRow, kRow, kEpiStore>(gw, p->dw.edge, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (dx && !dx_whole) {
+    e = launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dx), gx.ranges, gx.part_stride, gx.ld_out, d.T, nullptr,
+                      nullptr, nullptr, 0, d.D, dx, args->lddx, s);
+    if (e != hipSuccess) return e;
+  }
+  if (dw && !dw_whole)
+    return launch_sum<E>(reinterpret_cast<const float*>(ws + p->o_dw), gw.ranges, gw.part_stride, gw.ld_out, F2, nullptr,
+                         nullptr, nullptr, 0, d.D, dw, args->lddw, s);
+  return hipSuccess;
+}
+
+const Split* split_of(const fconv_gated_plan_s* p, int32_t product) {
+  switch (product) {
+    case FCONV_GATED_FORWARD: return &p->fwd;
+    case FCONV_GATED_DX: return &p->dx;
+    case FCONV_GATED_DW: return &p->dw;
+    default: return nullptr;
+  }
+}
+
+}  // namespace
+}  // namespace fconv
+
+extern "C" {
+
+fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_plan* out) {
+  using namespace fconv;
+  if (!desc || !out) return FCONV_ERR_INVALID_ARG;
+  *out = nullptr;
+  const fconv_gated_desc& d = *desc;
+  if (d.dtype != FCONV_BF16 && d.dtype != FCONV_FP32) return FCONV_ERR_UNSUPPORTED;
+  if (d.activation < FCONV_ACT_SILU || d.activation > FCONV_ACT_RELU || d.flags) return FCONV_ERR_UNSUPPORTED;
+  if (d.T < 0 || d.D < 1 || d.F < 1) return FCONV_ERR_INVALID_ARG;
+  if (d.D > kMaxD || d.F > kMaxD) return FCONV_ERR_UNSUPPORTED;
+  const int64_t T = d.T, D = d.D, F2 = 2ll * d.F, tb = ceil_div(T, 64);
+  if (tb > kMaxGridY || ceil_div(F2, 64) * tb > kMaxTiles || ceil_div(D, 64) * tb > kMaxTiles || T * D > kMaxSum ||
+      T * F2 > kMaxSum || F2 * D > kMaxSum)
+    return FCONV_ERR_UNSUPPORTED;
+  fconv_gated_plan_s* p = new (std::nothrow) fconv_gated_plan_s();
+  if (!p) return FCONV_ERR_INVALID_ARG;
+  p->d = d;
+  p->es = d.dtype == FCONV_BF16 ? 2 : 4;
+  p->ld_kept = round_up(d.F, 8);
+  p->kept_bytes = static_cast<size_t>(T) * 2 * p->ld_kept * p->es;
+  const bool bf16 = d.dtype == FCONV_BF16, tiled = bf16 && D % 8 == 0;
+  p->ld_pack = round_up(D, 8);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  if (T > 0) {
+    p->fwd = choose(F2, T, D, tiled, false);
+    if (bf16 && !tiled && T > kFewTokens) {
+      const Split packed = choose(F2, T, D, true, false);
+      p->pack_fwd = packed.us + pack_us(F2, D) + pack_us(T, D) < p->fwd.us;
+      if (p->pack_fwd) p->fwd = packed;
+    }
+    p->few = T <= kFewTokens;
+    p->fwd_x = take(p->pack_fwd ? static_cast<size_t>(T) * p->ld_pack * 2 : 0);
+    p->fwd_w = take(p->pack_fwd ? static_cast<size_t>(F2) * p->ld_pack * 2 : 0);
+    p->fwd_bytes = at;
+    at = 0;
+    p->ld_dz = round_up(F2, 64);
+    p->dx = choose(D, T, F2, tiled, true);
+    if (bf16 && !tiled) {
+      const Split packed = choose(D, T, F2, true, true);
+      p->pack_dx = packed.us + pack_us(F2, D) < p->dx.us;
+      if (p->pack_dx) p->dx = packed;
+    }
+    p->dw = choose(D, F2, T, bf16, true);
+    // Both gradients in general tiles take one launch, in which they overlap.
+    const Split dx64 = choose(D, T, F2, false, true), dw64 = choose(D, F2, T, false, false);
+    const double longer = dx64.us > dw64.us ? dx64.us : dw64.us, other = dx64.us + dw64.us - longer;
+    if (!p->pack_dx && longer + 0.5 * other < p->dx.us + p->dw.us + 4.0) {
+      p->dx = dx64;
+      p->dw = dw64;
+    }
+    const size_t ld4 = static_cast<size_t>(round_up(D, 4)) * 4;
+    p->o_dz = take(static_cast<size_t>(T) * p->ld_dz * p->es);
+    p->o_x = take(bf16 && p->dw.edge != 64 ? static_cast<size_t>(T) * p->ld_pack * 2 : 0);
+    p->o_w = take(p->pack_dx ? static_cast<size_t>(F2) * p->ld_pack * 2 : 0);
+    p->o_dx = take(p->dx.ranges > 1 ? static_cast<size_t>(p->dx.ranges) * T * ld4 : 0);
+    p->o_dw = take(p->dw.ranges > 1 ? static_cast<size_t>(p->dw.ranges) * F2 * ld4 : 0);
+    p->bwd_bytes = at;
+  }
+  *out = p;
+  return FCONV_OK;
+}
+
+fconv_status fconv_gated_plan_kept_size(fconv_gated_plan p, size_t* bytes) {
+  if (!p || !bytes) return FCONV_ERR_INVALID_ARG;
+  *bytes = p->kept_bytes;
+  return FCONV_OK;
+}
+
+fconv_status fconv_gated_plan_forward_workspace_size(fconv_gated_plan p, size_t* bytes) {
+  if (!p || !bytes) return FCONV_ERR_INVALID_ARG;
+  *bytes = p->fwd_bytes;
+  return FCONV_OK;
+}
+
+fconv_status fconv_gated_plan_backward_workspace_size(fconv_gated_plan p, size_t* bytes) {
+  if (!p || !bytes) return FCONV_ERR_INVALID_ARG;
+  *bytes = p->bwd_bytes;
+  return FCONV_OK;
+}
+
+fconv_status fconv_gated_plan_forward(fconv_gated_plan p, void* stream, const fconv_gated_args* a) {
+  using namespace fconv;
+  if (!p || !a) return FCONV_ERR_INVALID_ARG;
+  const fconv_gated_desc& d = p->d;
+  if (d.T == 0) return FCONV_OK;
+  if (!a->x || !a->w || !a->y) return FCONV_ERR_INVALID_ARG;
+  if (bad_ld(a->ldx, d.D) || bad_ld(a->ldw, d.D) || bad_ld(a->ldy, d.F)) return FCONV_ERR_INVALID_ARG;
+  if (p->fwd_bytes && (!a->workspace || a->workspace_bytes < p->fwd_bytes)) return FCONV_ERR_WORKSPACE;
+  if (!aligned(a->x, p->es) || !aligned(a->w, p->es) || !aligned(a->y, p->es) || !aligned(a->kept, 16) ||
+      !aligned(a->workspace, 16))
+    return FCONV_ERR_MISALIGNED;
+  const Range in[] = {{a->x, span(d.T, d.D, a->ldx, p->es)}, {a->w, span(2ll * d.F, d.D, a->ldw, p->es)}};
+  const Range wr[] = {{a->y, span(d.T, d.F, a->ldy, p->es)}, {a->kept, p->kept_bytes}, {a->workspace, p->fwd_bytes}};
+  if (clash(wr, 3, in, 2)) return FCONV_ERR_INVALID_ARG;
+  const hipError_t e = d.dtype == FCONV_BF16 ? run_forward<__bf16>(p, a, as_stream(stream))
+                                             : run_forward<float>(p, a, as_stream(stream));
+  return e == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
+}
+
+fconv_status fconv_gated_plan_backward(fconv_gated_plan p, void* stream, const fconv_gated_args* a) {
+  using namespace fconv;
+  if (!p || !a) return FCONV_ERR_INVALID_ARG;
+  const fconv_gated_desc& d = p->d;
+  if (!a->dx && !a->dw) return FCONV_ERR_INVALID_ARG;
+  if ((a->dx && bad_ld(a->lddx, d.D)) || (a->dw && bad_ld(a->lddw, d.D))) return FCONV_ERR_INVALID_ARG;
+  if (!aligned(a->dx, p->es) || !aligned(a->dw, p->es)) return FCONV_ERR_MISALIGNED;
+  if (d.T > 0) {
+    if (!a->x || !a->w || !a->kept || !a->dy) return FCONV_ERR_INVALID_ARG;
+    if (bad_ld(a->ldx, d.D) || bad_ld(a->ldw, d.D) || bad_ld(a->lddy, d.F)) return FCONV_ERR_INVALID_ARG;
+    if (!a->workspace || a->workspace_bytes < p->bwd_bytes) return FCONV_ERR_WORKSPACE;
+    if (!aligned(a->x, p->es) || !aligned(a->w, p->es) || !aligned(a->kept, 16) || !aligned(a->dy, p->es) ||
+        !aligned(a->workspace, 16))
+      return FCONV_ERR_MISALIGNED;
+    const Range in[] = {{a->x, span(d.T, d.D, a->ldx, p->es)}, {a->w, span(2ll * d.F, d.D, a->ldw, p->es)},
+                        {a->kept, p->kept_bytes}, {a->dy, span(d.T, d.F, a->lddy, p->es)}};
+    const Range wr[] = {{a->dx, span(d.T, d.D, a->lddx, p->es)}, {a->dw, span(2ll * d.F, d.D, a->lddw, p->es)},
+                        {a->workspace, p->bwd_bytes}};
+    if (clash(wr, 3, in, 4)) return FCONV_ERR_INVALID_ARG;
+  }
+  const hipError_t e = d.dtype == FCONV_BF16 ? run_backward<__bf16>(p, a, as_stream(stream))
+                                             : run_backward<float>(p, a, as_stream(stream));
+  return e == hipSuccess ? FCONV_OK : FCONV_ERR_DEVICE;
+}
+
+const char* fconv_gated_plan_kernel_name(fconv_gated_plan p, int32_t product) {
+  using namespace fconv;
+  if (!p || p->d.T == 0) return nullptr;
+  const Split* split = split_of(p, product);
+  if (!split) return nullptr;
+  if (product == FCONV_GATED_FORWARD && p->few) return "gated_few";
+  const bool packed = product == FCONV_GATED_FORWARD ? p->pack_fwd
+                      : product == FCONV_GATED_DX    ? p->pack_dx
+                                                     : split->edge != 64 && p->d.D % 8 != 0;
+  if (split->edge == 64) return packed ? "gemm_gen_64_packed" : "gemm_gen_64";
+  if (split->edge == 128) return packed ? "gemm_tile_128_packed" : "gemm_tile_128";
+  return packed ? "gemm_tile_256_packed" : "gemm_tile_256";
+}
+
+fconv_status fconv_gated_plan_ranges(fconv_gated_plan p, int32_t product, int32_t* ranges) {
+  using namespace fconv;
+  if (!p || !ranges) return FCONV_ERR_INVALID_ARG;
+  const Split* split = split_of(p, product);
+  if (!split) return FCONV_ERR_INVALID_ARG;
+  *ranges = p->d.T == 0 ? 0 : split->ranges;
+  return FCONV_OK;
+}
+
+fconv_status fconv_gated_plan_destroy(fconv_gated_plan p) {
+  delete p;
+  return FCONV_OK;
+}
+
+}  // extern "C"

@@ -41,12 +41,17 @@ enum Order { kSum, kRow };
 struct Operand {
   const char* p;
   int64_t ld;     // elements
-  int64_t width;  // kRow: readable elements of a row
+  int64_t width;  // kRow: readable elements of a row; kEpiGated's A: rows to its second half
 };
 
 // kEpiStream: kEpiOut past the caches.  kEpiAdd: kEpiPart added to what is there.
-enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart, kEpiStream, kEpiAdd };
-constexpr bool is_out(Epilogue e) { return e == kEpiOut || e == kEpiStream; }
+// kEpiStore: C as it is, kEpiStoreStream: past the caches.  kEpiGated: A has two
+// halves of na rows; a tile holds the same rows of both, and what goes out is
+// act(C of the first) (C of the second).
+enum Epilogue { kEpiLse, kEpiGrad, kEpiOut, kEpiPart, kEpiStream, kEpiAdd, kEpiStore, kEpiStoreStream, kEpiGated };
+constexpr bool is_scaled(Epilogue e) { return e == kEpiOut || e == kEpiStream; }
+constexpr bool is_out(Epilogue e) { return is_scaled(e) || e == kEpiStore || e == kEpiStoreStream; }
+constexpr bool is_stream(Epilogue e) { return e == kEpiStream || e == kEpiStoreStream; }
 constexpr bool is_part(Epilogue e) { return e == kEpiPart || e == kEpiAdd; }
 
 struct GemmArgs {
@@ -72,6 +77,10 @@ struct GemmArgs {
   int32_t scale_step;
   int32_t v0;                 // vocabulary index of a = 0
   int32_t na_pad;             // kEpiGrad: columns of g written, zeros past na
+  // kEpiGated
+  int32_t act;
+  char* kept;                 // both halves of C: row b at b * 2 * ld_kept, the second ld_kept on; or NULL
+  int64_t ld_kept;
 };
 
 __device__ inline uint16_t f32_to_bf16(float f) {
@@ -177,6 +186,68 @@ __device__ inline void join(float& m, float& s, float m2, float s2) {
 }
 
 
+// ------------------------------------------------------- activations of a gate
+//
+// The logistic function and its complement from one exponential that cannot
+// overflow: both keep their relative accuracy in the tails.
+enum Act { kSilu, kGelu, kGeluTanh, kActRelu };
+
+struct Logistic {
+  float s, c;  // 1 / (1 + exp(-x)) and 1 - that
+};
+__device__ inline Logistic logistic(float x) {
+  const float e = exp_of(-__builtin_fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e), l = e * r;
+  return x < 0.0f ? Logistic{l, r} : Logistic{r, l};  // NaN: both are
+}
+constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi): 0.5 (1 + tanh y) is the logistic function of 2 y
+constexpr float kGeluK = 0.044715f, kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+
+template <int ACT>
+__device__ inline float act_of(float g) {
+  if constexpr (ACT == kSilu) return g * logistic(g).s;
+  if constexpr (ACT == kGelu) return g * (0.5f * erfcf(-kSqrtHalf * g));
+  if constexpr (ACT == kGeluTanh) return g * logistic(kGeluC * __builtin_fmaf(kGeluK * g * g, g, g)).s;
+  return g <= 0.0f ? 0.0f : g;  // NaN stays
+}
+// act and its derivative.
+template <int ACT>
+__device__ inline float2 act_grad(float g) {
+  if constexpr (ACT == kSilu) {
+    const Logistic p = logistic(g);
+    return make_float2(g * p.s, __builtin_fmaf(g * p.s, p.c, p.s));
+  }
+  if constexpr (ACT == kGelu) {
+    const float cdf = 0.5f * erfcf(-kSqrtHalf * g);
+    return make_float2(g * cdf, __builtin_fmaf(g * kInvSqrt2Pi, exp_of(-0.5f * g * g), cdf));
+  }
+  if constexpr (ACT == kGeluTanh) {
+    const Logistic p = logistic(kGeluC * __builtin_fmaf(kGeluK * g * g, g, g));
+    const float d = p.s * p.c;
+    // g g may be infinite where d is 0.
+    const float slope = d > 0.0f ? g * d * (kGeluC * __builtin_fmaf(3.0f * kGeluK * g, g, 1.0f)) : 0.0f;
+    return make_float2(g * p.s, p.s + slope);
+  }
+  return g <= 0.0f ? make_float2(0.0f, 0.0f) : make_float2(g, g > 0.0f ? 1.0f : g);
+}
+
+// The first half of column j's tiles through the activation.
+template <int ACT, int NI, int NJ>
+__device__ inline void activate_by(f32x4 (&acc)[NI][NJ], int j) {
+#pragma unroll
+  for (int i = 0; i < NI / 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = act_of<ACT>(acc[i][j][e]);
+}
+template <int NI, int NJ>
+__device__ inline void activate(f32x4 (&acc)[NI][NJ], int j, int act) {
+  switch (act) {
+    case kSilu: return activate_by<kSilu>(acc, j);
+    case kGelu: return activate_by<kGelu>(acc, j);
+    case kGeluTanh: return activate_by<kGeluTanh>(acc, j);
+    default: return activate_by<kActRelu>(acc, j);
+  }
+}
+
 // What a workgroup does with its tile of C: NI x NJ matrix tiles per wave, of
 // which this lane holds a = a_of(i) .. + 3 of b = b_of(j); ra x rb of the EDGE^2
 // tile exist.  Two waves (wa) share the tile's b.  Nothing is asked element by
@@ -212,7 +283,7 @@ __device__ inline PerB<EPI, NJ> load_per_b(const GemmArgs& g, int64_t a0, int64_
       p.at[j] = static_cast<int>(t[j] - g.v0 - a0);
       p.f[j] = t[j] < 0 ? __builtin_nanf("") : p.f[j];
     }
-  } else if constexpr (is_out(EPI)) {
+  } else if constexpr (is_scaled(EPI)) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       p.at[j] = static_cast<int>(b[j]);
@@ -230,8 +301,8 @@ template <Epilogue EPI, int NJ>
 __device__ inline void have_per_b(PerB<EPI, NJ>& p) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    if constexpr (!is_part(EPI)) asm volatile("" : "+v"(p.at[j]));
-    if constexpr (!is_part(EPI) && EPI != kEpiLse) asm volatile("" : "+v"(p.f[j]));
+    if constexpr (EPI == kEpiLse || EPI == kEpiGrad || is_scaled(EPI)) asm volatile("" : "+v"(p.at[j]));
+    if constexpr (EPI == kEpiGrad || is_scaled(EPI)) asm volatile("" : "+v"(p.f[j]));
   }
 }
 
@@ -324,6 +395,36 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
         }
       }
     }
+  } else if constexpr (EPI == kEpiGated) {
+    constexpr int N = NI / 2;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int b = b_of(j);
+      if (b >= rb) continue;
+      // Rows of [NI] tiles at p from `first` on.
+      auto put = [&](char* p, int first) __attribute__((always_inline)) {
+        if (whole && ES == 2 && N > 1) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2)
+            store_pair(p + (a_of(i) - 4 * q + pair_at(q)) * ES, acc[first + i][j], acc[first + (N > 1 ? i + 1 : i)][j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int n = ra - a_of(i);
+            if (n > 0) store4<E>(p + a_of(i) * ES, acc[first + i][j], n);
+          }
+        }
+      };
+      if (g.kept) {
+        char* row = g.kept + ((b0 + b) * 2 * g.ld_kept + a0) * ES;
+        put(row, 0);
+        put(row + g.ld_kept * ES, N);
+      }
+      activate(acc, j, g.act);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i][j] *= acc[N + i][j];
+      put(g.out + ((b0 + b) * g.ld_out + a0) * ES, 0);
+    }
   } else {
     using O = std::conditional_t<is_out(EPI), E, float>;
     // kEpiAdd: what is there, the next b's on its way while this one is added to
@@ -347,7 +448,7 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       if (b >= rb) continue;
       int64_t row = b0 + b;
       float scale = 1.0f;
-      if constexpr (is_out(EPI)) {
+      if constexpr (is_scaled(EPI)) {
         row = per.at[j];
         scale = per.f[j];
         if (row < 0) {
@@ -362,7 +463,7 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
         if constexpr (sizeof(O) == 2) {
 #pragma unroll
           for (int i = 0; i < NI; i += 2)
-            store_pair<EPI == kEpiStream>(out + (a_of(i) - 4 * q + pair_at(q)) * sizeof(O), acc[i][j] * scale,
+            store_pair<is_stream(EPI)>(out + (a_of(i) - 4 * q + pair_at(q)) * sizeof(O), acc[i][j] * scale,
                                           acc[i + 1][j] * scale);
         } else {
 #pragma unroll
@@ -426,14 +527,21 @@ struct Gen {
 };
 
 // 32 bytes of an operand's slab for this thread.
-template <typename E, Order O>
+// GATED: 32 rows of each half of A, 16 of the first and the same of the second in turn,
+// so that a wave's two tiles are a gate's and what it multiplies.
+template <typename E, Order O, bool GATED>
 __device__ inline void gen_load(const Operand& op, int64_t row0, int rows, int64_t k0, int64_t k1,
                                 E v[32 / sizeof(E)]) {
   constexpr int N = 32 / sizeof(E);
   const int tid = threadIdx.x;
   const char* p;
   int n;
-  if constexpr (O == kSum) {
+  if constexpr (GATED) {
+    const int r = tid >> 2, f = (r >> 5) * 16 + (r & 15);
+    const int64_t k = k0 + (tid & 3) * N;
+    n = f < rows ? static_cast<int>(min(k1 - k, static_cast<int64_t>(N))) : 0;
+    p = op.p + ((row0 + f + (r & 16 ? op.width : 0)) * op.ld + k) * static_cast<int64_t>(sizeof(E));
+  } else if constexpr (O == kSum) {
     const int r = tid >> 2;
     const int64_t k = k0 + (tid & 3) * N;
     n = r < rows ? static_cast<int>(min(k1 - k, static_cast<int64_t>(N))) : 0;
@@ -515,9 +623,11 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
   const int live = g.n_live ? *g.n_live : 0;
   const int nb = g.n_live && OB == kSum ? live : g.nb;
   const int nk = g.n_live && OB == kRow ? live : g.nk;
-  const int64_t a0 = static_cast<int64_t>(x) * 64, b0 = static_cast<int64_t>(y) * 64;
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr int EA = GATED ? 32 : 64;
+  const int64_t a0 = static_cast<int64_t>(x) * EA, b0 = static_cast<int64_t>(y) * 64;
   if (b0 >= nb) return;
-  const int ra = static_cast<int>(min<int64_t>(g.na - a0, 64)), rb = static_cast<int>(min<int64_t>(nb - b0, 64));
+  const int ra = static_cast<int>(min<int64_t>(g.na - a0, EA)), rb = static_cast<int>(min<int64_t>(nb - b0, 64));
   const int64_t per = round_up(ceil_div(nk, g.ranges), G::SLAB);
   const int64_t k0 = z * per;
   const int64_t k1 = min<int64_t>(nk, k0 + per);
@@ -531,8 +641,8 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
   E va[2][32 / G::ES], vb[2][32 / G::ES];
   auto load = [&](int s, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     if (s >= slabs) return;
-    gen_load<E, OA>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, xa);
-    gen_load<E, OB>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, xb);
+    gen_load<E, OA, GATED>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, xa);
+    gen_load<E, OB, false>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, xb);
   };
   auto step = [&](int s, char* ba, char* bb, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     gen_write<E, OA>(ba, xa);
@@ -562,8 +672,8 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
 
   auto b_of = [&](int j) { return wb * 32 + 16 * j + r; };
   const auto per_b = load_per_b<EPI, 2>(g, a0, b0, ra, rb, b_of);
-  epilogue<E, EPI, 2, 2, 64>(
-      g, acc, per_b, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return wa * 32 + 16 * i + 4 * q; }, b_of, lds.red);
+  epilogue<E, EPI, 2, 2, EA>(
+      g, acc, per_b, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return (wa * EA / 2) + 16 * i + 4 * q; }, b_of, lds.red);
 }
 
 template <typename E, Order OA, Order OB, Epilogue EPI>
@@ -609,12 +719,14 @@ __global__ __launch_bounds__(256) void gemm_gen_kernel(GemmArgs g) {
 // by swz(k) so that the rows that one read touches lie on different banks.
 // One operand of a workgroup: where its half tiles come from, and this lane's
 // places in them.
-template <Order O, int H, int NW>
+// GATED: the halves are the same H rows of A's two halves.
+template <Order O, int H, int NW, bool GATED = false>
 struct Feed {
   const char* base;  // of the tile's first element of the next slab to copy
   int64_t left;      // bytes readable from base
   int64_t step;      // bytes from slab to slab
   int krem;          // k left from base (kSum)
+  int64_t second;    // GATED: bytes to the second half
   uint32_t off[2][2];  // per half and copy of this wave
   int chunk;           // kSum: first k of this lane's piece
 
@@ -626,7 +738,8 @@ struct Feed {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          off[h][c] = static_cast<uint32_t>(((h * H + (wave * 2 + c) * 8 + (lane >> 3)) * op.ld + chunk) * 2);
+          off[h][c] = static_cast<uint32_t>((((GATED ? 0 : h * H) + (wave * 2 + c) * 8 + (lane >> 3)) * op.ld + chunk) * 2);
+      if constexpr (GATED) second = op.width * op.ld * 2;
     } else {
       step = op.ld * 128;
       krem = 0;
@@ -655,7 +768,7 @@ struct Feed {
   }
   // Copies half h of the next slab into buf (this wave's 2 KiB of it).
   __device__ void copy(int h, char* buf, int wave) const {
-    const auto rsrc = make_rsrc(base, left);
+    const auto rsrc = make_rsrc(GATED && h == 1 ? base + second : base, left);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       uint32_t o = off[h][c];
@@ -714,7 +827,9 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
   // Workgroups of one XCD (block ids go round the 8 XCDs) take neighbouring
   // tiles: eight rows of them together, so both operands stay in its L2; the
   // ranges of a sum come one after the other.
-  const int tiles_a = (g.na + 2 * H - 1) / (2 * H), tiles_b = (nb + 2 * H - 1) / (2 * H);
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr int EA = GATED ? H : 2 * H;
+  const int tiles_a = (g.na + EA - 1) / EA, tiles_b = (nb + 2 * H - 1) / (2 * H);
   const int tiles = tiles_a * tiles_b;
   const int total = tiles * g.ranges, share = (total + 7) / 8;
   const int first_id = (blockIdx.x % 8) * share, end = min(share, total - first_id);
@@ -731,9 +846,9 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
     const int first = tile / (8 * tiles_a) * 8, rows8 = min(8, tiles_b - first), in = tile % (8 * tiles_a);
     p.range = id / tiles;
     p.ta = in / rows8;
-    p.a0 = static_cast<int64_t>(p.ta) * 2 * H;
+    p.a0 = static_cast<int64_t>(p.ta) * EA;
     p.b0 = static_cast<int64_t>(first + in % rows8) * 2 * H;
-    p.ra = static_cast<int>(min<int64_t>(g.na - p.a0, 2 * H));
+    p.ra = static_cast<int>(min<int64_t>(g.na - p.a0, EA));
     p.rb = static_cast<int>(min<int64_t>(nb - p.b0, 2 * H));
     p.k0 = static_cast<int64_t>(p.range) * per * 64;
     p.slabs = max(0, min(per, all - p.range * per));
@@ -747,7 +862,7 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
   const int wa = wave / (NW / 2), wb = wave % (NW / 2);
 
   f32x4 acc[2 * MI][2 * MJ];
-  Feed<OA, H, NW> fa;
+  Feed<OA, H, NW, GATED> fa;
   Feed<OB, H, NW> fb;
   fa.init(g.a, wave, lane);
   fb.init(g.b, wave, lane);
@@ -881,7 +996,7 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
       at = locate(first_id + slot);
       if (at.slabs > 0) begin(at);
     }
-    epilogue<__bf16, EPI, 2 * MI, 2 * MJ, 2 * H>(g, acc, per_b, done.a0, done.b0, done.ra, done.rb, done.ta,
+    epilogue<__bf16, EPI, 2 * MI, 2 * MJ, EA>(g, acc, per_b, done.a0, done.b0, done.ra, done.rb, done.ta,
                                                  done.range, wa, q, a_of, b_of, red);
     if (!more) break;
   }
@@ -1047,7 +1162,7 @@ __global__ __launch_bounds__(256) void gemm_sum_kernel(const float* part, int ra
     for (int p = 1; p < PARTS; ++p) s += sums[p * QUADS + threadIdx.x];
   }
   if (!live) return;
-  s *= scale[row * scale_step];
+  if (scale) s *= scale[row * scale_step];
   int64_t to = row_map ? row_map[row] : row;
   if (to < 0) {
     to = -1 - to;
@@ -1113,7 +1228,7 @@ inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 // The kernel of a product: tiles of 64 (general), 128 or 256.
 template <typename E, Order OA, Order OB, Epilogue EPI>
 hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
-  const int64_t ta = ceil_div(g.na, edge), tb = ceil_div(g.nb, edge);
+  const int64_t ta = ceil_div((EPI == kEpiGated ? 2ll : 1ll) * g.na, edge), tb = ceil_div(g.nb, edge);
   if constexpr (sizeof(E) == 2) {
     // As many workgroups as the device holds at once (one or two a CU, by their
     // LDS), in eighths; each takes every so manieth tile of its XCD's share.
@@ -1126,7 +1241,7 @@ hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
     if (edge != 64) return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(ta), static_cast<unsigned>(tb), static_cast<unsigned>(g.ranges));
-  hipLaunchKernelGGL((gemm_gen_kernel<E, OA, OB, EPI == kEpiStream ? kEpiOut : EPI>), grid, dim3(256), 0, s, g);
+  hipLaunchKernelGGL((gemm_gen_kernel<E, OA, OB, EPI == kEpiStream ? kEpiOut : EPI == kEpiStoreStream ? kEpiStore : EPI>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
 

@@ -24,10 +24,11 @@
 // their own rounding to bf16 (perf/operators.py's cases, with q in fp32 and here).
 // r h is rounded to bf16 too, exactly where all dloss are equal.
 //
-// Every product has the form C[b, a] = sum_k A(a, k) B(b, k) with a contiguous
-// in C: the matrix core then ends with four consecutive a per lane.
+// The products as gemm.h has them, C[b, a] = sum_k A(a, k) B(b, k):
 //   logits  a = v, b = t, k = d: A = w, B = h, both with k contiguous
 //   dh      a = d, b = t, k = v: A = w with a contiguous, B = g
+//   dw      a = d, b = v, k = t: A = h, B = g, a and b contiguous
+#include <hip/hip_runtime.h>
 #include <limits.h>
 #include <stdint.h>
 #include <stdio.h>
