@@ -21,6 +21,20 @@ loss without the logits, and 4-bit weights and activations.
 
     w4 = MxQuantPlan(N, K, "bf16")(w)                       # MXFP4, laid out once
     y = MxPlan(M, N, K, "bf16", ops=("bias", "relu"))(x, w4, bias=b)
+
+What stands around the output layer in training (``include/fconv_embed.h``,
+``fconv_gated.h``, ``fconv_clip.h``): the embedding lookup, a gated feed-forward
+layer, each with its gradients, and the clipping of all gradients by their norm.
+
+    e = EmbedPlan(T, D, V, "bf16", scale=D ** 0.5)
+    x = e.forward(table, token)
+    dtable = e.backward(token, dx)                # or added to dw: dw=dw, accumulate=True
+
+    f = GatedPlan(T, D, F, "bf16", activation="silu")
+    y, kept = f.forward(x, w, keep=True)
+    dx, dw = f.backward(x, w, kept, dy)
+
+    norm = ClipPlan([(g.numel(), "bf16") for g in grads]).clip(grads, max_norm)
 """
 from __future__ import annotations
 
@@ -31,10 +45,10 @@ import operator
 
 from . import _abi
 
-# The output layer's plans take torch tensors only.  Their modules import torch and are loaded on first
+# The dense operators' plans take torch tensors only.  Their modules import torch and are loaded on first
 # use, so that the package can be imported, built and used with raw addresses where torch is not installed.
 _WITH_TORCH = {"MxTensor": ".mx", "MxQuantPlan": ".mx", "MxPlan": ".mx", "XentPlan": ".xent",
-               "GatedPlan": ".gated"}
+               "GatedPlan": ".gated", "EmbedPlan": ".embed", "ClipPlan": ".clip"}
 
 __all__ = ["Plan", "WgradPlan", "FconvError", "DTYPES", "OPS"]
 if importlib.util.find_spec("torch") is not None:

@@ -274,6 +274,86 @@ def gated_lib():
     return _gated_lib
 
 
+# --- include/fconv_embed.h (bound on first use, as above) -------------------
+
+FCONV_EMBED_ADD = 1
+
+# Every symbol include/fconv_embed.h declares.
+EMBED_EXPORTS = ("fconv_embed_plan_create", "fconv_embed_plan_workspace_size", "fconv_embed_plan_forward",
+                 "fconv_embed_plan_backward", "fconv_embed_plan_destroy")
+
+
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "V", "dtype")] + \
+               [("ignore_index", ctypes.c_int64), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class EmbedArgs(ctypes.Structure):
+    _fields_ = [("token", ctypes.c_void_p), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("dy", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("run_flags", ctypes.c_uint32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+_embed_lib = None
+
+
+def embed_lib():
+    """The loaded library with the symbols of include/fconv_embed.h declared."""
+    global _embed_lib
+    if _embed_lib is None:
+        L = lib()
+        P = ctypes.c_void_p
+        L.fconv_embed_plan_create.argtypes = [ctypes.POINTER(EmbedDesc), ctypes.POINTER(P)]
+        L.fconv_embed_plan_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        L.fconv_embed_plan_forward.argtypes = [P, P, ctypes.POINTER(EmbedArgs)]
+        L.fconv_embed_plan_backward.argtypes = [P, P, ctypes.POINTER(EmbedArgs)]
+        L.fconv_embed_plan_destroy.argtypes = [P]
+        for name in EMBED_EXPORTS:
+            getattr(L, name).restype = ctypes.c_int
+        _embed_lib = L
+    return _embed_lib
+
+
+# --- include/fconv_clip.h (bound on first use, as above) --------------------
+
+# Every symbol include/fconv_clip.h declares.
+CLIP_EXPORTS = ("fconv_clip_plan_create", "fconv_clip_plan_workspace_size", "fconv_clip_plan_tensors",
+                "fconv_clip_plan_norm", "fconv_clip_plan_clip", "fconv_clip_plan_destroy")
+
+
+class ClipTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class ClipArgs(ctypes.Structure):
+    _fields_ = [("in_", ctypes.POINTER(ctypes.c_void_p)), ("out", ctypes.POINTER(ctypes.c_void_p)),
+                ("max_norm", ctypes.c_float), ("norm", ctypes.c_void_p), ("given_norm", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_clip_lib = None
+
+
+def clip_lib():
+    """The loaded library with the symbols of include/fconv_clip.h declared."""
+    global _clip_lib
+    if _clip_lib is None:
+        L = lib()
+        P, i32 = ctypes.c_void_p, ctypes.c_int32
+        L.fconv_clip_plan_create.argtypes = [ctypes.POINTER(ClipTensor), i32, ctypes.c_float, ctypes.POINTER(P)]
+        L.fconv_clip_plan_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        L.fconv_clip_plan_tensors.argtypes = [P, ctypes.POINTER(ctypes.POINTER(ClipTensor)), ctypes.POINTER(i32)]
+        L.fconv_clip_plan_norm.argtypes = [P, P, ctypes.POINTER(ClipArgs)]
+        L.fconv_clip_plan_clip.argtypes = [P, P, ctypes.POINTER(ClipArgs)]
+        L.fconv_clip_plan_destroy.argtypes = [P]
+        for name in CLIP_EXPORTS:
+            getattr(L, name).restype = ctypes.c_int
+        _clip_lib = L
+    return _clip_lib
+
+
 # --- csrc/call.cpp: the short way through a call --------------------------
 
 _call = None

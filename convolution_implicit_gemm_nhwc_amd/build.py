@@ -28,7 +28,7 @@ CALL = os.path.join(PKG, "_call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["plan.cpp", "conv.hip", "wgrad.hip", "mx.hip", "xent.hip", "gated.hip"]
+SOURCES = ["plan.cpp", "conv.hip", "wgrad.hip", "mx.hip", "xent.hip", "gated.hip", "embed.hip", "clip.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-fast-math",
           "-Wall", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
@@ -62,7 +62,7 @@ def build(verbose: bool = False) -> str:
     else:
         if os.path.exists(CALL):  # of other sources
             os.remove(CALL)
-        print("torch is not installed: %s not built (MxPlan, MxQuantPlan, XentPlan need it)" % CALL,
+        print("torch is not installed: %s not built (the dense operators' plans need it)" % CALL,
               file=sys.stderr, flush=True)
     return LIB
 

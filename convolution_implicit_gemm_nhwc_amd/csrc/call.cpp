@@ -1,4 +1,4 @@
-// The short way through a call of the dense operators (mx.py, xent.py, gated.py).
+// The short way through a call of the dense operators (mx.py, xent.py, gated.py, embed.py, clip.py).
 //
 // Their smallest calls take 2 to 5 us on the GPU; through ctypes the host took
 // 6.5 us for a quantisation and 32 us for a loss with its gradient.  Here a call
@@ -19,6 +19,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
+#include "fconv_clip.h"
+#include "fconv_embed.h"
 #include "fconv_gated.h"
 #include "fconv_mx.h"
 #include "fconv_xent.h"
@@ -51,9 +55,10 @@ struct Call {
     return reinterpret_cast<F>(p);
   }
   // The tensor at i, if it lives on the call's device (that of the first one) and is of the type.
-  const at::Tensor* tensor(int i, ScalarType type) {
-    if (!THPVariable_Check(args[i])) return fail();
-    const at::Tensor& t = THPVariable_Unpack(args[i]);
+  const at::Tensor* tensor(int i, ScalarType type) { return tensor(args[i], type); }
+  const at::Tensor* tensor(PyObject* object, ScalarType type) {
+    if (!THPVariable_Check(object)) return fail();
+    const at::Tensor& t = THPVariable_Unpack(object);
     if (!t.defined() || !t.is_cuda() || t.scalar_type() != type || t.layout() != at::kStrided ||
         t.unsafeGetTensorImpl()->is_python_dispatch())
       return fail();
@@ -79,6 +84,13 @@ struct Call {
     const at::Tensor* t = tensor(i, type);
     if (!t) return nullptr;
     if (t->numel() != numel || !t->is_contiguous()) return fail(), nullptr;
+    return t->data_ptr();
+  }
+  // Address of a tensor whose numel elements fill their memory, in any order of its dimensions.
+  void* filled(PyObject* object, ScalarType type, int64_t numel, const at::Tensor** at) {
+    const at::Tensor* t = *at = tensor(object, type);
+    if (!t) return nullptr;
+    if (t->numel() != numel || !t->unsafeGetTensorImpl()->is_non_overlapping_and_dense()) return fail(), nullptr;
     return t->data_ptr();
   }
   // After the tensors: whether the call can go on, on the current device.
@@ -315,11 +327,99 @@ PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// embed_forward(w, token, fn, plan, T, D, V, dtype) -> y
+PyObject* embed_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count_is(n, 8)) return nullptr;
+  Call c{args};
+  const auto fn = c.function<decltype(&fconv_embed_plan_forward)>(2);
+  const auto plan = c.function<fconv_embed_plan>(3);
+  const int64_t T = c.whole(4), D = c.whole(5), V = c.whole(6), dtype = c.whole(7);
+  fconv_embed_args a = {};
+  a.w = c.matrix(0, type_of(dtype), V, D, &a.ldw);
+  a.token = static_cast<const int64_t*>(c.vector(1, at::kLong, T));
+  if (!c.ready()) Py_RETURN_NONE;
+  at::TensorBase y = make({T, D}, type_of(dtype), c.device);
+  a.y = y.data_ptr();
+  a.ldy = D;
+  return launch(
+      c, [&](void* s) { return fn(plan, s, &a); }, [&] { return THPVariable_Wrap(std::move(y)); });
+  END_HANDLE_TH_ERRORS
+}
+
+// embed_backward(token, dy, fn, plan, T, D, V, dtype, workspace bytes) -> dw
+PyObject* embed_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count_is(n, 9)) return nullptr;
+  Call c{args};
+  const auto fn = c.function<decltype(&fconv_embed_plan_backward)>(2);
+  const auto plan = c.function<fconv_embed_plan>(3);
+  const int64_t T = c.whole(4), D = c.whole(5), V = c.whole(6), dtype = c.whole(7), ws_bytes = c.whole(8);
+  fconv_embed_args a = {};
+  a.token = static_cast<const int64_t*>(c.vector(0, at::kLong, T));
+  a.dy = c.matrix(1, type_of(dtype), T, D, &a.lddy);
+  if (!c.ready()) Py_RETURN_NONE;
+  at::TensorBase dw = make({V, D}, type_of(dtype), c.device), ws;
+  a.dw = dw.data_ptr();
+  a.lddw = D;
+  if (ws_bytes) {
+    ws = make({ws_bytes}, at::kByte, c.device);
+    a.workspace = ws.data_ptr();
+    a.workspace_bytes = static_cast<size_t>(ws_bytes);
+  }
+  return launch(
+      c, [&](void* s) { return fn(plan, s, &a); }, [&] { return THPVariable_Wrap(std::move(dw)); });
+  END_HANDLE_TH_ERRORS
+}
+
+// clip(gradients, outputs or None, fn, plan, plan's tensors fn, max_norm, workspace bytes) -> norm
+// The norm alone, without outputs, where max_norm is None.
+PyObject* clip(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count_is(n, 7)) return nullptr;
+  Call c{args};
+  const auto fn = c.function<decltype(&fconv_clip_plan_clip)>(2);
+  const auto plan = c.function<fconv_clip_plan>(3);
+  const auto tensors_of = c.function<decltype(&fconv_clip_plan_tensors)>(4);
+  const int64_t ws_bytes = c.whole(6);
+  const bool out_given = args[1] != Py_None, scale = args[5] != Py_None;
+  if (!c.ok || !PyList_CheckExact(args[0]) || (out_given && !PyList_CheckExact(args[1])) ||
+      (scale && !PyFloat_CheckExact(args[5])))
+    Py_RETURN_NONE;
+  const fconv_clip_tensor* tensors = nullptr;
+  int32_t count = 0;
+  if (tensors_of(plan, &tensors, &count) != FCONV_OK || PyList_GET_SIZE(args[0]) != count ||
+      (out_given && PyList_GET_SIZE(args[1]) != count))
+    Py_RETURN_NONE;
+  std::vector<void*> in(count), out(count);
+  for (int32_t i = 0; i < count && c.ok; ++i) {
+    const at::Tensor *g, *o;
+    in[i] = out[i] = c.filled(PyList_GET_ITEM(args[0], i), type_of(tensors[i].dtype), tensors[i].numel, &g);
+    if (!out_given || !c.ok) continue;
+    out[i] = c.filled(PyList_GET_ITEM(args[1], i), type_of(tensors[i].dtype), tensors[i].numel, &o);
+    c.ok = c.ok && g->sizes() == o->sizes() && g->strides() == o->strides();
+  }
+  if (!c.ready()) Py_RETURN_NONE;
+  at::TensorBase norm = make({}, at::kFloat, c.device), ws = make({ws_bytes}, at::kByte, c.device);
+  fconv_clip_args a = {};
+  a.in = in.data();
+  a.out = scale ? out.data() : nullptr;
+  a.max_norm = scale ? static_cast<float>(PyFloat_AS_DOUBLE(args[5])) : 0.0f;
+  a.norm = static_cast<float*>(norm.data_ptr());
+  a.workspace = ws.data_ptr();
+  a.workspace_bytes = static_cast<size_t>(ws_bytes);
+  return launch(
+      c, [&](void* s) { return fn(plan, s, &a); }, [&] { return THPVariable_Wrap(std::move(norm)); });
+  END_HANDLE_TH_ERRORS
+}
+
 #define FCONV_CALL(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {FCONV_CALL(quantize),     FCONV_CALL(dequantize),    FCONV_CALL(product),
                           FCONV_CALL(xent_forward), FCONV_CALL(xent_backward),
-                          FCONV_CALL(gated_forward), FCONV_CALL(gated_backward), {nullptr, nullptr, 0, nullptr}};
+                          FCONV_CALL(gated_forward), FCONV_CALL(gated_backward),
+                          FCONV_CALL(embed_forward), FCONV_CALL(embed_backward),
+                          FCONV_CALL(clip),          {nullptr, nullptr, 0, nullptr}};
 #undef FCONV_CALL
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -15,6 +15,8 @@
 
 #include <type_traits>
 
+#include "dense.h"
+
 namespace fconv {
 namespace {
 
@@ -28,11 +30,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // of a join takes four of them, and a launch's threads stay below 2^32.  Tokens:
 // tiles of 64 in grid.y.
 constexpr int64_t kMaxTiles = 1ll << 28, kMaxSum = 1ll << 33, kMaxGridY = 65535;
-constexpr int64_t kMaxLd = 1 << 21;
 constexpr int32_t kMaxD = 1 << 20, kMaxTV = 1 << 24;
-
-__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-__host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // Which index of an operand is contiguous in memory: the sum's (element
 // (r, k) at r * ld + k) or the row's (at k * ld + r).
@@ -1223,8 +1221,6 @@ inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) 
 // Time (us) of packing a matrix: a launch, one read and one write.
 inline double pack_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 4e6; }
 
-inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
-
 // The kernel of a product: tiles of 64 (general), 128 or 256.
 template <typename E, Order OA, Order OB, Epilogue EPI>
 hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
@@ -1271,34 +1267,6 @@ hipError_t launch_sum(const float* part, int ranges, int64_t stride, int64_t ld,
                        part, ranges, stride, ld, rows, n_live, row_map, scale, scale_step, cols, out, ld_out);
   return hipGetLastError();
 }
-
-inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-inline bool aligned(const void* ptr, uintptr_t n) { return (reinterpret_cast<uintptr_t>(ptr) & (n - 1)) == 0; }
-// Bytes from the first to the last element of a strided matrix.
-inline size_t span(int64_t rows, int64_t cols, int64_t ld, int es) {
-  return rows <= 0 ? 0 : static_cast<size_t>((rows - 1) * ld + cols) * es;
-}
-
-struct Range {
-  const void* p;
-  size_t bytes;
-};
-// Whether any of the written ranges meets another range.
-inline bool clash(const Range* out, int n_out, const Range* in, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
-  }
-  return false;
-}
-
-inline bool bad_ld(int64_t ld, int32_t D) { return ld < D || ld > kMaxLd; }
 
 }  // namespace
 }  // namespace fconv
