@@ -285,7 +285,7 @@ PyObject* gated_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   a.y = y.data_ptr();
   a.ldy = F;
   if (keep) {
-    kept = make({keep}, type_of(dtype), c.device);
+    kept = make({keep}, at::kFloat, c.device);
     a.kept = kept.data_ptr();
   }
   if (ws_bytes) {
@@ -311,7 +311,7 @@ PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   fconv_gated_args a = {};
   a.x = c.matrix(0, type_of(dtype), T, D, &a.ldx);
   a.w = c.matrix(1, type_of(dtype), 2 * F, D, &a.ldw);
-  a.kept = c.vector(2, type_of(dtype), keep);
+  a.kept = c.vector(2, at::kFloat, keep);
   a.dy = c.matrix(3, type_of(dtype), T, F, &a.lddy);
   if (!c.ready()) Py_RETURN_NONE;
   at::TensorBase dx = make({T, D}, type_of(dtype), c.device), dw = make({2 * F, D}, type_of(dtype), c.device),

@@ -10,10 +10,11 @@
 //   dx       a = d, b = t, k = g's f, then u's: A = w with a contiguous, B = [dg du]
 //   dw       a = d, b = g's f, then u's, k = t: A = x, B = [dg du], a and b contiguous
 //
-// g and u are kept in the operands' type for the gradients: computing them again
-// would take half as much as the gradients' own products (4 T D F operations
-// beside 8), reading them back takes 4 T F bytes of bf16.  Their rounding is off
-// by 2^-9 of themselves on average, half of what a bf16 gradient's own rounding is.
+// g and u are kept for the gradients: computing them again would take half as
+// much as the gradients' own products (4 T D F operations beside 8), writing and
+// reading them 16 T F bytes.  They are kept in fp32: rounded to bf16, with dg and
+// du that are rounded too, bf16 gradients were off by 0.0030 of their norm instead
+// of 0.0023, of which 0.0017 is their own rounding.
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -47,7 +48,7 @@ struct GatedFew {
   int64_t ldx;
   char* y;
   int64_t ldy;
-  char* kept;
+  float* kept;
   int64_t ld_kept;
   int32_t T, D, F, act;
 };
@@ -153,9 +154,9 @@ __global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
     for (int x = 1; x < NW; ++x) z[i][0] += sums[x][wave * 2 + i][lane];
   }
   if (f.kept) {
-    char* row = f.kept + (2 * t * f.ld_kept + at) * ES;
-    store4<E>(row, z[0][0], f.F - at);
-    store4<E>(row + f.ld_kept * ES, z[1][0], f.F - at);
+    float* row = f.kept + 2 * t * f.ld_kept + at;  // rows are whole fours
+    *reinterpret_cast<f32x4*>(row) = z[0][0];
+    *reinterpret_cast<f32x4*>(row + f.ld_kept) = z[1][0];
   }
   activate(z, 0, f.act);
   store4<E>(f.y + (t * f.ldy + at) * ES, z[0][0] * z[1][0], f.F - at);
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
 // kernel multiplies whole pieces of 16 bytes of them by zeros).  A thread takes
 // eight f of a row: 3 T F elements are read and 2 T F written.
 struct GatedDz {
-  const char* kept;
+  const float* kept;
   int64_t ld_kept;
   const char* dy;
   int64_t lddy;
@@ -177,13 +178,13 @@ struct GatedDz {
 };
 
 template <typename E>
-__device__ inline void dz_values(const E* g, const E* u, const E* dy, E* dg, E* du, int act) {
+__device__ inline void dz_values(const float* g, const float* u, const E* dy, E* dg, E* du, int act) {
   auto by = [&](auto grad) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float2 a = grad(static_cast<float>(g[e]));
+      const float2 a = grad(g[e]);
       const float d = static_cast<float>(dy[e]);
-      dg[e] = static_cast<E>(d * static_cast<float>(u[e]) * a.y);
+      dg[e] = static_cast<E>(d * u[e] * a.y);
       du[e] = static_cast<E>(d * a.x);
     }
   };
@@ -204,10 +205,11 @@ __global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
   if (row >= z.T) return;
   const int c = static_cast<int>(i - static_cast<uint32_t>(row) * per_row) * 8;
   const int n = min(z.F - c, 8);
-  E g[8], u[8], dy[8], dg[8], du[8];
-  const char* kept = z.kept + (2 * row * z.ld_kept + c) * ES;
+  float g[8], u[8];
+  E dy[8], dg[8], du[8];
+  const float* kept = z.kept + 2 * row * z.ld_kept + c;
   __builtin_memcpy(g, __builtin_assume_aligned(kept, 16), sizeof(g));
-  __builtin_memcpy(u, __builtin_assume_aligned(kept + z.ld_kept * ES, 16), sizeof(u));
+  __builtin_memcpy(u, __builtin_assume_aligned(kept + z.ld_kept, 16), sizeof(u));
   const char* src = z.dy + (row * z.lddy + c) * ES;
   if (n == 8) {
     __builtin_memcpy(dy, src, sizeof(dy));
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(256) void gated_gen_grads_kernel(GemmArgs dx, GemmA
 struct fconv_gated_plan_s {
   fconv_gated_desc d;
   int32_t es;
-  int64_t ld_kept;  // F in whole 16 bytes: kept is [T, 2, ld_kept]
+  int64_t ld_kept;  // F in whole eights: kept is fp32 [T, 2, ld_kept]
   size_t kept_bytes;
   bool few;                       // at most kFewTokens, by their own kernel
   bool pack_fwd, pack_dx;         // rows of bf16 copied to 16-byte boundaries: x and w; w
@@ -305,7 +307,7 @@ hipError_t run_forward(const fconv_gated_plan_s* p, const fconv_gated_args* args
   Operand x = {static_cast<const char*>(args->x), args->ldx, 0};
   const bool fits = fits_tiles(w.p, w.ld) && fits_tiles(x.p, x.ld);
   if (p->few || (d.T <= kFewTokens && !fits && p->fwd.edge != 64)) {
-    const GatedFew f = {w.p, w.ld, x.p, x.ld, static_cast<char*>(args->y), args->ldy, static_cast<char*>(args->kept),
+    const GatedFew f = {w.p, w.ld, x.p, x.ld, static_cast<char*>(args->y), args->ldy, static_cast<float*>(args->kept),
                         p->ld_kept, d.T, d.D, d.F, d.activation};
     if constexpr (sizeof(E) == 2) {
       if (odd_rows(w) || odd_rows(x)) return launch_few_of<E, true>(f, s);
@@ -332,7 +334,7 @@ hipError_t run_forward(const fconv_gated_plan_s* p, const fconv_gated_args* args
   g.out = static_cast<char*>(args->y);
   g.ld_out = args->ldy;
   g.act = d.activation;
-  g.kept = static_cast<char*>(args->kept);
+  g.kept = static_cast<float*>(args->kept);
   g.ld_kept = p->ld_kept;
   return launch_gemm<E, kSum, kSum, kEpiGated>(g, edge, s);
 }
@@ -351,7 +353,7 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
                        static_cast<int64_t>(F2), d.D);
     return hipGetLastError();
   }
-  const GatedDz z = {static_cast<const char*>(args->kept), p->ld_kept, static_cast<const char*>(args->dy), args->lddy,
+  const GatedDz z = {static_cast<const float*>(args->kept), p->ld_kept, static_cast<const char*>(args->dy), args->lddy,
                      ws + p->o_dz, p->ld_dz, d.T, d.F, d.activation};
   hipLaunchKernelGGL(gated_dz_kernel<E>, dim3(static_cast<unsigned>(ceil_div(d.T * (p->ld_kept / 8), 256))), dim3(256), 0,
                      s, z);
@@ -455,7 +457,7 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
   p->d = d;
   p->es = d.dtype == FCONV_BF16 ? 2 : 4;
   p->ld_kept = round_up(d.F, 8);
-  p->kept_bytes = static_cast<size_t>(T) * 2 * p->ld_kept * p->es;
+  p->kept_bytes = static_cast<size_t>(T) * 2 * p->ld_kept * 4;
   const bool bf16 = d.dtype == FCONV_BF16, tiled = bf16 && D % 8 == 0;
   p->ld_pack = round_up(D, 8);
   size_t at = 0;

@@ -77,7 +77,7 @@ struct GemmArgs {
   int32_t na_pad;             // kEpiGrad: columns of g written, zeros past na
   // kEpiGated
   int32_t act;
-  char* kept;                 // both halves of C: row b at b * 2 * ld_kept, the second ld_kept on; or NULL
+  float* kept;                // both halves of C: row b at b * 2 * ld_kept, the second ld_kept on (16-byte rows); or NULL
   int64_t ld_kept;
 };
 
@@ -399,29 +399,28 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
     for (int j = 0; j < NJ; ++j) {
       const int b = b_of(j);
       if (b >= rb) continue;
-      // Rows of [NI] tiles at p from `first` on.
-      auto put = [&](char* p, int first) __attribute__((always_inline)) {
-        if (whole && ES == 2 && N > 1) {
-#pragma unroll
-          for (int i = 0; i < N; i += 2)
-            store_pair(p + (a_of(i) - 4 * q + pair_at(q)) * ES, acc[first + i][j], acc[first + (N > 1 ? i + 1 : i)][j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int n = ra - a_of(i);
-            if (n > 0) store4<E>(p + a_of(i) * ES, acc[first + i][j], n);
-          }
-        }
-      };
       if (g.kept) {
-        char* row = g.kept + ((b0 + b) * 2 * g.ld_kept + a0) * ES;
-        put(row, 0);
-        put(row + g.ld_kept * ES, N);
+        float* row = g.kept + (b0 + b) * 2 * g.ld_kept + a0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (whole || a_of(i % N) < ra)  // rows are whole fours
+            *reinterpret_cast<f32x4*>(row + (i / N) * g.ld_kept + a_of(i % N)) = acc[i][j];
       }
       activate(acc, j, g.act);
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i][j] *= acc[N + i][j];
-      put(g.out + ((b0 + b) * g.ld_out + a0) * ES, 0);
+      char* row = g.out + ((b0 + b) * g.ld_out + a0) * ES;
+      if (whole && ES == 2 && N > 1) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+          store_pair(row + (a_of(i) - 4 * q + pair_at(q)) * ES, acc[i][j], acc[N > 1 ? i + 1 : i][j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int n = ra - a_of(i);
+          if (n > 0) store4<E>(row + a_of(i) * ES, acc[i][j], n);
+        }
+      }
     }
   } else {
     using O = std::conditional_t<is_out(EPI), E, float>;

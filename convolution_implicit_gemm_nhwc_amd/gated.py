@@ -39,7 +39,7 @@ class GatedPlan:
         self.kept_bytes = self._size("kept")
         self.forward_workspace_bytes = self._size("forward_workspace")
         self.backward_workspace_bytes = self._size("backward_workspace")
-        self._kept = self.kept_bytes // self._torch.itemsize
+        self._kept = self.kept_bytes // 4  # fp32
         self._call = _abi.native()
         sizes = (self._h.value, T, D, F, d.dtype)
         self._forward = (_abi.address(L.fconv_gated_plan_forward),) + sizes + (self.forward_workspace_bytes,)
@@ -91,7 +91,7 @@ class GatedPlan:
             else:
                 out = torch.empty(self.T, self.F, dtype=self._torch, device=device)
                 a.y, a.ldy = out.data_ptr(), self.F
-            kept = torch.empty(self._kept, dtype=self._torch, device=device) if keep else None
+            kept = torch.empty(self._kept, dtype=torch.float32, device=device) if keep else None
             ws = torch.empty(self.forward_workspace_bytes, dtype=torch.uint8, device=device)
             a.kept = kept.data_ptr() if keep else None
             a.workspace, a.workspace_bytes = ws.data_ptr(), self.forward_workspace_bytes
@@ -113,7 +113,7 @@ class GatedPlan:
             if r is not None:
                 return done(r, "fconv_gated_plan_backward")
         a = self._inputs(x, w)
-        a.kept = vector(kept, "kept", self._kept, self._torch)
+        a.kept = vector(kept, "kept", self._kept, torch.float32)
         a.dy, a.lddy = matrix(dy, "dy", self.T, self.F, self._torch)
 
         def run(s, device):

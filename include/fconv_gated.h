@@ -17,9 +17,9 @@
  * Both projections, the activation and the product are one kernel.  dtype is
  * the type of x, w, y, dy, dx and dw (FCONV_BF16 or FCONV_FP32); products are
  * summed in fp32 by the matrix cores, activations are fp32.  For the gradients
- * the forward pass can keep g and u, rounded to dtype; with FCONV_BF16, dg and
- * du are rounded to bf16 before they are multiplied.  All roundings are to
- * nearest even.  Results do not depend on the order in which workgroups run.
+ * the forward pass can keep g and u, in fp32; with FCONV_BF16, dg and du are
+ * rounded to bf16 before they are multiplied.  All roundings are to nearest
+ * even.  Results do not depend on the order in which workgroups run.
  *
  * Conventions as in fconv.h: status codes only; every check happens before
  * anything is enqueued; the caller owns every buffer; plans are host objects
