@@ -14,10 +14,13 @@
 //           smaller ones of its chunk: n^2 / 2 operations a token and no passes
 //   merge   sixteen sorted runs at a time: a key's place is the sum of its ranks
 //           in them, found by binary searches
-//   reduce  pieces of `piece` sorted keys: their rows of dy are summed; a token
+//   sums    pieces of `piece` sorted keys: their rows of dy are summed; a token
 //           whose keys all lie in the piece is done, the others' sums of the piece
-//           go out.  Other workgroups of the launch write the rows of zeros.
+//           go out
 //   join    adds the pieces' sums of a token, in order
+// Rows without a token are written by other workgroups: beside the ranking, whose
+// time that hides, as long as each of them can look at all tokens (kScan), and of
+// longer batches beside the sums, by searching the sorted keys.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -33,9 +36,10 @@ namespace fconv {
 namespace {
 
 constexpr int kSmall = 256;   // tokens that a workgroup sorts by itself
+constexpr int kScan = 32768;  // tokens that a workgroup looks through for its rows
 constexpr int kChunk = 4096;  // tokens of a chunk that is ranked, at most
 constexpr int kWays = 16;     // runs merged at a time
-constexpr uint32_t kNoToken = 0xffffffffu;  // sorts behind every token
+constexpr uint32_t kNoToken = 0x7fffffffu;  // sorts behind every token
 
 __device__ inline uint64_t key_of(uint32_t token, uint32_t place) { return static_cast<uint64_t>(token) << 32 | place; }
 __device__ inline uint32_t token_of(uint64_t key) { return static_cast<uint32_t>(key >> 32); }
@@ -48,9 +52,12 @@ template <typename E>
 struct Vec {
   static constexpr int N = 16 / sizeof(E);
   E v[N];
-  // n of them at p, zeros past those.
+  // n of them at p, zeros past those.  WHOLE: all exist.  Where that is not known
+  // beforehand a load waits for the one before it, since either may be the one that
+  // fills a register.
+  template <bool WHOLE = false>
   __device__ void load(const char* p, int n) {
-    if (n >= N) {
+    if (WHOLE || n >= N) {
       __builtin_memcpy(v, p, 16);
     } else {
 #pragma unroll
@@ -60,9 +67,18 @@ struct Vec {
       }
     }
   }
+  // PAST: past the caches.
+  template <bool PAST = false>
   __device__ void store(char* p, int n) const {
     if (n >= N) {
-      __builtin_memcpy(p, v, 16);
+      if constexpr (PAST) {
+        typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+        Words w;
+        __builtin_memcpy(&w, v, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<Words*>(p));
+      } else {
+        __builtin_memcpy(p, v, 16);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e)
@@ -86,8 +102,8 @@ struct LookupArgs {
 
 // Four pieces of 16 bytes of a thread in flight.  Pieces are counted in 32 bits:
 // T D is at most 2^33 elements.
-template <typename E>
-__global__ __launch_bounds__(256) void embed_lookup_kernel(LookupArgs a) {
+template <typename E, bool WHOLE>
+__device__ inline void lookup(const LookupArgs& a) {
   constexpr int N = Vec<E>::N, U = 4;
   constexpr int64_t ES = sizeof(E);
   const uint32_t per_row = static_cast<uint32_t>((a.D + N - 1) / N), total = per_row * static_cast<uint32_t>(a.T);
@@ -104,7 +120,7 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(LookupArgs a) {
     const uint32_t i = first + 256u * u;
     if (i >= total) break;
     const int c = static_cast<int>(i % per_row) * N;
-    if (usable(tok[u], a.ignore, a.V) != kNoToken) v[u].load(a.w + (tok[u] * a.ldw + c) * ES, a.D - c);
+    if (usable(tok[u], a.ignore, a.V) != kNoToken) v[u].template load<WHOLE>(a.w + (tok[u] * a.ldw + c) * ES, a.D - c);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -120,87 +136,16 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(LookupArgs a) {
 #pragma unroll
       for (int e = 0; e < N; ++e) v[u].v[e] = static_cast<E>(a.scale * static_cast<float>(v[u].v[e]));
     }
-    v[u].store(a.y + (row * a.ldy + c) * ES, a.D - c);
+    v[u].store(a.y + (row * a.ldy + c) * ES, WHOLE ? N : a.D - c);
   }
 }
 
-// -------------------------------------------------------------------- sorting
-
-// Keys of chunk blockIdx.y, sorted: a workgroup ranks 64 of them, each wave
-// against every fourth block of 64.  Of equal tokens the earlier one is smaller:
-// in a block before the own one "not larger" counts, in one behind it "smaller".
-__global__ __launch_bounds__(256) void embed_rank_kernel(const int64_t* token, int64_t ignore, int32_t T, int32_t V,
-                                                         int chunk, uint64_t* keys) {
-  __shared__ __attribute__((aligned(16))) uint32_t all[kChunk];
-  __shared__ int ranks[4][64];
-  const int base = blockIdx.y * chunk, n = min(chunk, T - base), n64 = (n + 63) / 64 * 64;
-  const int own = blockIdx.x * 64;
-  if (own >= n) return;
-  for (int i = threadIdx.x; i < n64; i += 256) all[i] = i < n ? usable(token[base + i], ignore, V) : kNoToken;
-  __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t mine = all[own + lane];
-  int rank = 0;
-  for (int b = wave * 64; b < n64; b += 256) {
-    const uint4* p = reinterpret_cast<const uint4*>(all + b);
-    if (b < own) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint4 k = p[i];
-        rank += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
-      }
-    } else if (b > own) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint4 k = p[i];
-        rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
-      }
-    } else {
-      for (int i = 0; i < 64; ++i) rank += all[b + i] < mine || (all[b + i] == mine && i < lane);
-    }
-  }
-  ranks[wave][lane] = rank;
-  __syncthreads();
-  // What fills the last block up ranks behind the chunk's own keys.
-  if (wave == 0 && own + lane < n)
-    keys[base + ranks[0][lane] + ranks[1][lane] + ranks[2][lane] + ranks[3][lane]] =
-        key_of(mine, static_cast<uint32_t>(base + own + lane));
-}
-
-// Groups of kWays sorted runs of `run` keys become one each.  Four lanes share a
-// key, each with four of the runs, whose searches go on side by side.
-__global__ __launch_bounds__(256) void embed_merge_kernel(const uint64_t* in, uint64_t* out, int32_t T, int32_t run) {
-  constexpr int M = kWays / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x / 4;
-  const int part = threadIdx.x & 3;
-  const bool live = i < T;
-  const int64_t at = live ? i : T - 1;
-  const uint64_t key = in[at];
-  const int64_t own = at / run, group = own / kWays * kWays;
-  int len[M], lo[M];
-  int64_t base[M];
-#pragma unroll
-  for (int k = 0; k < M; ++k) {
-    const int64_t r = group + part * M + k;
-    base[k] = r * run;
-    const int64_t left = T - base[k];
-    len[k] = left <= 0 ? 0 : left < run ? static_cast<int>(left) : run;
-    lo[k] = 0;
-  }
-  // The number of keys of each run that are below this one.
-  for (int step = 1 << (31 - __builtin_clz(run)); step > 0; step >>= 1) {
-    uint64_t x[M];
-#pragma unroll
-    for (int k = 0; k < M; ++k) x[k] = lo[k] + step <= len[k] ? in[base[k] + lo[k] + step - 1] : ~0ull;
-#pragma unroll
-    for (int k = 0; k < M; ++k) lo[k] += x[k] < key ? step : 0;
-  }
-  int rank = 0;
-#pragma unroll
-  for (int k = 0; k < M; ++k) rank += lo[k];
-  rank += __shfl_xor(rank, 1);
-  rank += __shfl_xor(rank, 2);
-  if (live && part == 0) out[group * run + rank] = key;
+template <typename E>
+__global__ __launch_bounds__(256) void embed_lookup_kernel(LookupArgs a) {
+  if (a.D % Vec<E>::N == 0)
+    lookup<E, true>(a);
+  else
+    lookup<E, false>(a);
 }
 
 // ------------------------------------------------------------------- gradient
@@ -223,6 +168,7 @@ struct GradArgs {
   int32_t zero_rows;      // rows of dw of a workgroup of the zeros
   float scale;
   bool add;
+  bool past;              // zeros go past the caches
 };
 
 // First index of the sorted keys at or above `key`: 64 probes of a wave at a time.
@@ -269,18 +215,14 @@ __device__ inline void sort_small(const GradArgs& g, uint64_t* sorted) {
   __syncthreads();
 }
 
-// Sums of dy's rows.  A team's threads each hold 16 bytes of columns; eight rows
-// are in flight.  Without SMALL, a piece's first token may have begun before it and
-// its last one may go on behind it: their sums go to `part`.  With SMALL a token
-// belongs to the piece in which it begins, which then reads on.
-template <typename E, bool SMALL>
-__device__ inline void sum_rows(const GradArgs& g, const uint64_t* keys) {
+// Sums of dy's rows: those of sorted keys [at, end), columns from c on.  Eight rows are in flight.  Without
+// SMALL, a piece's first token may have begun before it and its last one may go on
+// behind it: their sums go to `part`.  With SMALL a token belongs to the piece in
+// which it begins, which then reads on.
+template <typename E, bool SMALL, bool WHOLE>
+__device__ inline void sum_piece(const GradArgs& g, const uint64_t* keys, int piece, int c) {
   constexpr int N = Vec<E>::N, U = 8;
   constexpr int64_t ES = sizeof(E);
-  const int teams = 256 / g.team, block = blockIdx.x % g.col_blocks;
-  const int piece = blockIdx.x / g.col_blocks * teams + threadIdx.x / g.team;
-  const int c = (block * g.team + threadIdx.x % g.team) * N;
-  if (piece >= g.pieces || c >= g.D) return;
   int at = piece * g.piece;
   const int end = min(at + g.piece, g.T);
   // Whether the token at `at` began before this piece; with SMALL it is another piece's.
@@ -313,7 +255,7 @@ __device__ inline void sum_rows(const GradArgs& g, const uint64_t* keys) {
       const uint64_t key = keys[min(at + u, last - 1)];
       tok[u] = at + u < last ? token_of(key) : kNoToken;
       // Rows past the end, and of tokens without a gradient, are read for nothing.
-      x[u].load(g.dy + (static_cast<int64_t>(static_cast<uint32_t>(key)) * g.lddy + c) * ES, g.D - c);
+      x[u].template load<WHOLE>(g.dy + (static_cast<int64_t>(static_cast<uint32_t>(key)) * g.lddy + c) * ES, g.D - c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -336,32 +278,56 @@ __device__ inline void sum_rows(const GradArgs& g, const uint64_t* keys) {
   if (!done) flush(!SMALL && end < g.T && token_of(keys[end]) == now);
 }
 
-// Zeros in the rows without a token, of zero_rows rows.
+// A team's threads each hold 16 bytes of a piece's columns.
 template <typename E, bool SMALL>
-__device__ inline void zero_rows(const GradArgs& g, const uint64_t* keys, uint32_t* used) {
+__device__ inline void sum_rows(const GradArgs& g, const uint64_t* keys) {
   constexpr int N = Vec<E>::N;
+  const int teams = 256 / g.team, block = blockIdx.x % g.col_blocks;
+  const int piece = blockIdx.x / g.col_blocks * teams + threadIdx.x / g.team;
+  const int c = (block * g.team + threadIdx.x % g.team) * N;
+  if (piece >= g.pieces || c >= g.D) return;
+  if (c + N <= g.D)
+    sum_piece<E, SMALL, true>(g, keys, piece, c);
+  else
+    sum_piece<E, SMALL, false>(g, keys, piece, c);
+}
+
+constexpr int kZeroRows = 1024;  // of a workgroup, at most
+
+// Zeros in the rows without a token, of the `group`th zero_rows rows; THREADS
+// threads.  SCAN: which rows have one is seen by looking through all tokens,
+// eight of a thread in flight, else by the sorted keys.
+template <typename E, bool SCAN, int THREADS>
+__device__ inline void zero_rows(const GradArgs& g, int group) {
+  __shared__ uint32_t used[kZeroRows / 32];
+  constexpr int N = Vec<E>::N, U = 8;
   constexpr int64_t ES = sizeof(E);
-  const int v0 = (static_cast<int>(blockIdx.x) - g.sum_groups) * g.zero_rows, rows = min(g.zero_rows, g.V - v0);
-  for (int i = threadIdx.x; i < (rows + 31) / 32; i += 256) used[i] = 0;
+  const int v0 = group * g.zero_rows, rows = min(g.zero_rows, g.V - v0), tid = threadIdx.x;
+  for (int i = tid; i < (rows + 31) / 32; i += THREADS) used[i] = 0;
   __syncthreads();
-  if (SMALL) {
-    if (threadIdx.x < static_cast<unsigned>(g.T)) {
-      const uint32_t v = usable(g.token[threadIdx.x], g.ignore, g.V) - static_cast<uint32_t>(v0);
-      if (v < static_cast<uint32_t>(rows)) atomicOr(&used[v / 32], 1u << (v % 32));
+  auto mark = [&](uint32_t token) __attribute__((always_inline)) {
+    const uint32_t v = token - static_cast<uint32_t>(v0);
+    if (v < static_cast<uint32_t>(rows)) atomicOr(&used[v / 32], 1u << (v % 32));
+  };
+  if (SCAN) {
+    for (int i = tid; i < g.T; i += THREADS * U) {
+      int64_t tok[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) tok[u] = g.token[min(i + u * THREADS, g.T - 1)];
+#pragma unroll
+      for (int u = 0; u < U; ++u) mark(usable(tok[u], g.ignore, g.V));
     }
   } else {
-    // 256 keys at a time from the first of these rows on.  Where the next token is
-    // the last one again, its end is searched for: a batch may be one token.
-    int at = lower_bound(keys, g.T, key_of(v0, 0));
+    // From the first of these rows on.  Where the next token is the last one again,
+    // its end is searched for: a batch may be one token.
+    int at = lower_bound(g.keys, g.T, key_of(v0, 0));
     while (at < g.T) {
-      const int i = at + static_cast<int>(threadIdx.x);
-      const uint32_t v = i < g.T ? token_of(keys[i]) - static_cast<uint32_t>(v0) : kNoToken;
-      if (v < static_cast<uint32_t>(rows)) atomicOr(&used[v / 32], 1u << (v % 32));
-      at += 256;
+      mark(at + tid < g.T ? token_of(g.keys[at + tid]) : kNoToken);
+      at += THREADS;
       if (at >= g.T) break;
-      const uint32_t before = token_of(keys[at - 1]), next = token_of(keys[at]);
+      const uint32_t before = token_of(g.keys[at - 1]), next = token_of(g.keys[at]);
       if (next >= static_cast<uint32_t>(v0 + rows)) break;
-      if (next == before) at = lower_bound(keys, g.T, key_of(next + 1, 0));
+      if (next == before) at = lower_bound(g.keys, g.T, key_of(next + 1, 0));
     }
   }
   __syncthreads();
@@ -369,79 +335,230 @@ __device__ inline void zero_rows(const GradArgs& g, const uint64_t* keys, uint32
   Vec<E> z;
 #pragma unroll
   for (int e = 0; e < N; ++e) z.v[e] = static_cast<E>(0.0f);
-  for (uint32_t i = threadIdx.x; i < total; i += 256) {
+  for (uint32_t i = tid; i < total; i += THREADS) {
     const uint32_t row = i / per_row;
     const int c = static_cast<int>(i - row * per_row) * N;
-    if (!(used[row / 32] >> (row % 32) & 1)) z.store(g.dw + ((v0 + static_cast<int64_t>(row)) * g.lddw + c) * ES, g.D - c);
+    if (used[row / 32] >> (row % 32) & 1) continue;
+    char* p = g.dw + ((v0 + static_cast<int64_t>(row)) * g.lddw + c) * ES;
+    if (g.past)
+      z.template store<true>(p, g.D - c);
+    else
+      z.store(p, g.D - c);
   }
 }
 
-constexpr int kZeroRows = 1024;  // of a workgroup, at most
-
 template <typename E, bool SMALL>
 __global__ __launch_bounds__(256) void embed_grad_kernel(GradArgs g) {
-  __shared__ uint64_t sorted[SMALL ? kSmall : 1];
-  __shared__ uint32_t used[kZeroRows / 32];
-  if (static_cast<int>(blockIdx.x) >= g.sum_groups) return zero_rows<E, SMALL>(g, g.keys, used);
-  if constexpr (SMALL) sort_small(g, sorted);
-  sum_rows<E, SMALL>(g, SMALL ? sorted : g.keys);
+  if (static_cast<int>(blockIdx.x) >= g.sum_groups)
+    return zero_rows<E, SMALL, 256>(g, static_cast<int>(blockIdx.x) - g.sum_groups);
+  if constexpr (SMALL) {
+    __shared__ uint64_t sorted[kSmall];
+    sort_small(g, sorted);
+    sum_rows<E, SMALL>(g, sorted);
+  } else {
+    sum_rows<E, SMALL>(g, g.keys);
+  }
+}
+
+// -------------------------------------------------------------------- sorting
+
+// Keys of each chunk, sorted: a workgroup ranks 64 of them, each of its sixteen
+// waves against every sixteenth block of 64.  Of equal tokens the earlier
+// one is smaller: in a block before the own one "not larger" counts, in one behind
+// it "smaller".  Workgroups behind those that rank write the rows of zeros.
+template <typename E>
+__global__ __launch_bounds__(1024) void embed_rank_kernel(GradArgs g, int chunk, int rank_groups, uint64_t* keys) {
+  if (static_cast<int>(blockIdx.x) >= rank_groups)
+    return zero_rows<E, true, 1024>(g, static_cast<int>(blockIdx.x) - rank_groups);
+  __shared__ __attribute__((aligned(16))) uint32_t all[kChunk];
+  __shared__ int ranks[16][64];
+  const int blocks = chunk / 64, base = blockIdx.x / blocks * chunk, n = min(chunk, g.T - base), n64 = (n + 63) / 64 * 64;
+  const int own = blockIdx.x % blocks * 64;
+  if (own >= n) return;
+  int64_t tok[kChunk / 1024];
+#pragma unroll
+  for (int u = 0; u < kChunk / 1024; ++u) {
+    const int i = u * 1024 + static_cast<int>(threadIdx.x);
+    tok[u] = i < n ? g.token[base + i] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kChunk / 1024; ++u) {
+    const int i = u * 1024 + static_cast<int>(threadIdx.x);
+    if (i < n64) all[i] = i < n ? usable(tok[u], g.ignore, g.V) : kNoToken;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t mine = all[own + lane];
+  int rank = 0;
+  for (int b = wave * 64; b < n64; b += 1024) {
+    const uint4* p = reinterpret_cast<const uint4*>(all + b);
+    // Smaller than mine, or than the next one where equal ones count too (no overflow: kNoToken is not the largest).
+    const uint32_t below = b < own ? mine + 1 : mine;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 k = p[i];
+      rank += (k.x < below) + (k.y < below) + (k.z < below) + (k.w < below);
+      if (b == own) {
+        rank += (k.x == mine && 4 * i < lane) + (k.y == mine && 4 * i + 1 < lane) + (k.z == mine && 4 * i + 2 < lane) +
+                (k.w == mine && 4 * i + 3 < lane);
+      }
+    }
+  }
+  ranks[wave][lane] = rank;
+  __syncthreads();
+  // What fills the last block up ranks behind the chunk's own keys.
+  if (wave != 0 || own + lane >= n) return;
+  rank = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) rank += ranks[w][lane];
+  keys[base + rank] = key_of(mine, static_cast<uint32_t>(base + own + lane));
+}
+
+// Groups of kWays sorted runs of `run` keys become one each.  Four lanes share a
+// key, each with four of the runs, whose searches go on side by side.  The last
+// keys of 64 parts of each run are brought to LDS first: a step of a search that
+// goes to memory takes most of a microsecond (16384 tokens, sixteen runs: 11.7 us
+// with all eleven steps there).
+__global__ __launch_bounds__(512) void embed_merge_kernel(const uint64_t* in, uint64_t* out, int32_t T, int32_t run) {
+  constexpr int M = kWays / 4;
+  __shared__ uint64_t samples[kWays][64];
+  const int per_group = run * kWays, blocks = (per_group + 127) / 128;  // of 128 keys
+  const int64_t first = static_cast<int64_t>(blockIdx.x / blocks) * per_group;  // of the group
+  const int step = (run + 63) / 64;  // of a part
+  const int64_t block = first + static_cast<int64_t>(blockIdx.x % blocks) * 128, at = block + threadIdx.x / 4;
+  if (block >= T) return;
+#pragma unroll
+  for (int i = threadIdx.x; i < kWays * 64; i += 512) {
+    const int k = i / 64, p = i % 64;
+    const int in_run = (p + 1) * step - 1;
+    const int64_t x = first + static_cast<int64_t>(k) * run + in_run;
+    samples[k][p] = in_run < run && x < T ? in[x] : ~0ull;
+  }
+  const bool live = at < T && at < first + per_group;
+  const uint64_t key = in[live ? at : first];
+  const int part = threadIdx.x & 3;
+  __syncthreads();
+  int lo[M], hi[M];  // keys below this one: of lo .. hi of the run
+  int64_t base[M];
+#pragma unroll
+  for (int k = 0; k < M; ++k) {
+    const int r = part * M + k;
+    base[k] = first + static_cast<int64_t>(r) * run;
+    const int64_t left = T - base[k];
+    const int len = left <= 0 ? 0 : left < run ? static_cast<int>(left) : run;
+    int p = 0;  // parts whose last key is below
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) p += samples[r][p + s - 1] < key ? s : 0;
+    p += samples[r][p] < key;  // p is at most 63 here
+    lo[k] = min(p * step, len);
+    hi[k] = min(lo[k] + step - 1, len);
+  }
+  for (int s = step; s > 1; s = (s + 1) / 2) {  // hi - lo is below s
+    uint64_t x[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) x[k] = lo[k] < hi[k] ? in[base[k] + (lo[k] + hi[k]) / 2] : 0;
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      const int mid = (lo[k] + hi[k]) / 2;
+      if (lo[k] < hi[k]) {
+        if (x[k] < key)
+          lo[k] = mid + 1;
+        else
+          hi[k] = mid;
+      }
+    }
+  }
+  int rank = 0;
+#pragma unroll
+  for (int k = 0; k < M; ++k) rank += lo[k];
+  rank += __shfl_xor(rank, 1);
+  rank += __shfl_xor(rank, 2);
+  if (live && part == 0) out[first + rank] = key;
 }
 
 // The sums of a token that goes on from piece to piece: the piece in which it
-// begins adds up its own part and the others', in order.  Four waves share the
-// pieces; a lane has four columns, eight loads in flight.
+// begins adds up its own part and the others', in order.  A workgroup has 1024
+// columns: each wave 256 of them, four of a lane, or of a long token (kShared pieces)
+// all waves the same 256 at a time, each with a quarter of the pieces.  Eight
+// loads of a lane are in flight.
+constexpr int kShared = 32;
+
 template <typename E>
 __global__ __launch_bounds__(256) void embed_join_kernel(GradArgs g) {
   constexpr int64_t ES = sizeof(E);
   __shared__ float4 sums[4][64];
   const int piece = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int first = piece * g.piece, end = first + g.piece;  // not the last piece
-  const uint32_t v = token_of(g.keys[end]);
-  if (v == kNoToken || token_of(g.keys[end - 1]) != v) return;  // nothing goes on
-  if (first > 0 && token_of(g.keys[first - 1]) == v) return;    // it began before
-  const int stop = lower_bound(g.keys, g.T, key_of(v + 1, 0));
-  const int n = (stop - 1) / g.piece - piece;  // pieces behind this one, one at least
-  const int per = (n + 3) / 4, from = wave * per, to = min(from + per, n);
-  for (int c = (blockIdx.y * 64 + lane) * 4; c - 4 * lane < g.D; c += gridDim.y * 256) {
-    const bool live = c < g.D;
+  // All at once: the keys about this piece's ends, and those that the next 64 begin with.
+  auto begins = [&](int n) __attribute__((always_inline)) {
+    return g.keys[min(end + (static_cast<int64_t>(n) + lane) * g.piece, static_cast<int64_t>(g.T) - 1)];
+  };
+  uint64_t key = begins(0);
+  const uint32_t last = token_of(g.keys[end - 1]), before = token_of(g.keys[first > 0 ? first - 1 : 0]);
+  const uint32_t v = token_of(__shfl(key, 0));
+  if (v == kNoToken || last != v || (first > 0 && before == v)) return;  // nothing goes on, or it began before
+  // Pieces behind this one that begin with the token, one at least.
+  int n = 0;
+  for (;;) {
+    const bool there = end + (static_cast<int64_t>(n) + lane) * g.piece < g.T && token_of(key) == v;
+    const int more = __popcll(__ballot(there));
+    n += more;
+    if (more < 64) break;
+    key = begins(n);
+  }
+  auto add = [&](float4& s, const float4& x) __attribute__((always_inline)) {
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  };
+  // Parts [from, to) behind this piece's own, which comes first if `own`.
+  auto sum = [&](int c, int from, int to, bool own) __attribute__((always_inline)) {
     float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto add = [&](const float4& x) __attribute__((always_inline)) {
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
-    };
-    if (live) {
-      const float* p = g.part + 2ll * (piece + 1) * g.ld_part + c;
-      if (wave == 0) add(*reinterpret_cast<const float4*>(p - g.ld_part));
-      for (int k = from; k < to; k += 8) {
-        float4 x[8];
+    const float* p = g.part + 2ll * (piece + 1) * g.ld_part + c;
+    if (own) s = *reinterpret_cast<const float4*>(p - g.ld_part);
+    for (int k = from; k < to; k += 8) {
+      float4 x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const float4*>(p + 2ll * min(k + u, to - 1) * g.ld_part);
+      for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const float4*>(p + 2ll * min(k + u, to - 1) * g.ld_part);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (k + u < to) add(x[u]);
-      }
+      for (int u = 0; u < 8; ++u)
+        if (k + u < to) add(s, x[u]);
     }
-    sums[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && live) {
+    return s;
+  };
+  auto put = [&](int c, const float4& s) __attribute__((always_inline)) {
+    const float f[4] = {s.x, s.y, s.z, s.w};
+    char* p = g.dw + (static_cast<int64_t>(v) * g.lddw + c) * ES;
 #pragma unroll
-      for (int x = 1; x < 4; ++x) add(sums[x][lane]);
-      const float v4[4] = {s.x, s.y, s.z, s.w};
-      char* to_row = g.dw + (static_cast<int64_t>(v) * g.lddw + c) * ES;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (c + e >= g.D) continue;
-        E x;
-        if (g.add) {
-          __builtin_memcpy(&x, to_row + e * ES, ES);
-          x = static_cast<E>(__builtin_fmaf(g.scale, v4[e], static_cast<float>(x)));
-        } else {
-          x = static_cast<E>(g.scale * v4[e]);
-        }
-        __builtin_memcpy(to_row + e * ES, &x, ES);
+    for (int e = 0; e < 4; ++e) {
+      if (c + e >= g.D) continue;
+      E x;
+      if (g.add) {
+        __builtin_memcpy(&x, p + e * ES, ES);
+        x = static_cast<E>(__builtin_fmaf(g.scale, f[e], static_cast<float>(x)));
+      } else {
+        x = static_cast<E>(g.scale * f[e]);
       }
+      __builtin_memcpy(p + e * ES, &x, ES);
+    }
+  };
+  const int c0 = blockIdx.y * 1024 + lane * 4;
+  if (n < kShared) {
+    const int c = c0 + wave * 256;
+    if (c < g.D) put(c, sum(c, 0, n, true));
+    return;
+  }
+  const int per = (n + 3) / 4, from = wave * per, to = min(from + per, n);
+  for (int b = 0; b < 4; ++b) {
+    const int c = c0 + b * 256;
+    if (c < g.D) sums[wave][lane] = sum(c, from, to, wave == 0);
+    __syncthreads();
+    if (wave == b && c < g.D) {
+      float4 s = sums[0][lane];
+#pragma unroll
+      for (int x = 1; x < 4; ++x) add(s, sums[x][lane]);
+      put(c, s);
     }
     __syncthreads();
   }
@@ -483,23 +600,7 @@ hipError_t run_backward(const fconv_embed_plan_s* p, const fconv_embed_args* a, 
   char* ws = static_cast<char*>(a->workspace);
   hipError_t e;
   uint64_t *keys = reinterpret_cast<uint64_t*>(ws), *other = reinterpret_cast<uint64_t*>(ws + p->o_other);
-  if (!p->small) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(d.T < p->chunk ? d.T : p->chunk, 64)),
-                    static_cast<unsigned>(ceil_div(d.T, p->chunk)));
-    hipLaunchKernelGGL(embed_rank_kernel, grid, dim3(256), 0, s, a->token, d.ignore_index, d.T, d.V, p->chunk, keys);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    int64_t run = p->chunk;
-    for (int i = 0; i < p->merges; ++i, run *= kWays) {
-      hipLaunchKernelGGL(embed_merge_kernel, dim3(static_cast<unsigned>(ceil_div(d.T, 64))), dim3(256), 0, s, keys,
-                         other, d.T, static_cast<int32_t>(run));
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      uint64_t* t = keys;
-      keys = other;
-      other = t;
-    }
-  }
   GradArgs g = {};
-  g.keys = keys;
   g.token = a->token;
   g.ignore = d.ignore_index;
   g.dy = static_cast<const char*>(a->dy);
@@ -519,7 +620,31 @@ hipError_t run_backward(const fconv_embed_plan_s* p, const fconv_embed_args* a, 
   g.zero_rows = p->zero_rows;
   g.scale = d.scale;
   g.add = add;
-  const int64_t groups = g.sum_groups + (add ? 0 : ceil_div(d.V, p->zero_rows));
+  // Where dy and dw are more than the last-level cache holds, zeros past it leave dy there (16384 tokens, 65536 x
+  // 4096 bf16: 135 us instead of 160; 65536 tokens, 65536 x 1024: 100 and 110); where dw stays in it, or dy is
+  // small, they cost (1999 tokens, 32001 x 1000: 29 and 27; 300 tokens, 65536 x 4096: 105 and 103).
+  const int64_t dy_bytes = static_cast<int64_t>(d.T) * d.D * p->es, dw_bytes = static_cast<int64_t>(d.V) * d.D * p->es;
+  g.past = dy_bytes + dw_bytes >= 256ll << 20 && dy_bytes >= 32ll << 20;
+  int64_t zero_groups = add ? 0 : ceil_div(d.V, p->zero_rows);
+  if (!p->small) {
+    const int64_t rank_groups = ceil_div(d.T, p->chunk) * (p->chunk / 64), beside = d.T <= kScan ? zero_groups : 0;
+    hipLaunchKernelGGL(embed_rank_kernel<E>, dim3(static_cast<unsigned>(rank_groups + beside)), dim3(1024), 0, s, g,
+                       p->chunk, static_cast<int>(rank_groups), keys);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    zero_groups -= beside;
+    int64_t run = p->chunk;
+    for (int i = 0; i < p->merges; ++i, run *= kWays) {
+      const int64_t group = run * kWays, blocks = ceil_div(d.T, group) * ceil_div(group, 128);
+      hipLaunchKernelGGL(embed_merge_kernel, dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s, keys, other, d.T,
+                         static_cast<int32_t>(run));
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      uint64_t* t = keys;
+      keys = other;
+      other = t;
+    }
+    g.keys = keys;
+  }
+  const int64_t groups = g.sum_groups + zero_groups;
   if (groups == 0) return hipSuccess;
   if (p->small)
     hipLaunchKernelGGL((embed_grad_kernel<E, true>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, s, g);
@@ -527,8 +652,7 @@ hipError_t run_backward(const fconv_embed_plan_s* p, const fconv_embed_args* a, 
     hipLaunchKernelGGL((embed_grad_kernel<E, false>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, s, g);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (p->small || p->pieces < 2) return hipSuccess;
-  const int64_t cols = ceil_div(d.D, 256);
-  hipLaunchKernelGGL(embed_join_kernel<E>, dim3(static_cast<unsigned>(p->pieces - 1), static_cast<unsigned>(cols < 64 ? cols : 64)),
+  hipLaunchKernelGGL(embed_join_kernel<E>, dim3(static_cast<unsigned>(p->pieces - 1), static_cast<unsigned>(ceil_div(d.D, 1024))),
                      dim3(256), 0, s, g);
   return hipGetLastError();
 }
