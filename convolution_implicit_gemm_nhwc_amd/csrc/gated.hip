@@ -177,24 +177,21 @@ struct GatedDz {
   int32_t T, F, act;
 };
 
-template <typename E>
-__device__ inline void dz_values(const float* g, const float* u, const E* dy, E* dg, E* du, int act) {
-  auto by = [&](auto grad) __attribute__((always_inline)) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 a = grad(g[e]);
-      const float d = static_cast<float>(dy[e]);
-      dg[e] = static_cast<E>(d * u[e] * a.y);
-      du[e] = static_cast<E>(d * a.x);
-    }
-  };
+// f(act and act' of a gate) of the activation.
+template <typename F>
+__device__ inline void with_act(int act, F f) {
   switch (act) {
-    case kSilu: return by(act_grad<kSilu>);
-    case kGelu: return by(act_grad<kGelu>);
-    case kGeluTanh: return by(act_grad<kGeluTanh>);
-    default: return by(act_grad<kActRelu>);
+    case kSilu: return f(act_grad<kSilu>);
+    case kGelu: return f(act_grad<kGelu>);
+    case kGeluTanh: return f(act_grad<kGeluTanh>);
+    default: return f(act_grad<kActRelu>);
   }
 }
+// The two gradients of one f, rounded as they are multiplied.
+template <typename E>
+__device__ inline E dg_of(float dy, float u, float2 a) { return static_cast<E>(dy * u * a.y); }
+template <typename E>
+__device__ inline E du_of(float dy, float2 a) { return static_cast<E>(dy * a.x); }
 
 template <typename E>
 __global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
@@ -220,7 +217,14 @@ __global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
       if (e < n) __builtin_memcpy(&dy[e], src + e * ES, ES);
     }
   }
-  dz_values(g, u, dy, dg, du, z.act);
+  with_act(z.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 a = act(g[e]);
+      dg[e] = dg_of<E>(static_cast<float>(dy[e]), u[e], a);
+      du[e] = du_of<E>(static_cast<float>(dy[e]), a);
+    }
+  });
   char* to = z.dz + (row * z.ld_dz + c) * ES;
   if (n == 8) {
     __builtin_memcpy(__builtin_assume_aligned(to, 16), dg, sizeof(dg));
@@ -275,21 +279,39 @@ namespace {
 
 constexpr int32_t kFewTokens = 64;
 
-// Time (us) of the few-token kernel: w at 4.1, 3.2 or 2.5 TB/s for 16, 32 or 64
-// tokens, or what a workgroup's steps and its launch cost.
+// Time (us) of the few-token kernel: w out of memory, at a rate that falls with the
+// tokens (16, 32, 64), or the steps of a wave one after another (fitted to D 64 ..
+// 8192, F 64 .. 16384).
 double few_us(int64_t T, int64_t F, int64_t D, int es) {
   const int k = T <= 16 ? 0 : T <= 32 ? 1 : 2;
-  static const double rate[] = {4.1e6, 3.2e6, 2.5e6}, each[] = {0.8e-5, 1.0e-5, 1.85e-5};
-  const double memory = 4.0 + 2.0 * es * static_cast<double>(F) * static_cast<double>(D) / rate[k];
-  const double work = 2.6 + static_cast<double>(ceil_div(F, 16)) * (0.005 + each[k] * static_cast<double>(D));
-  return memory > work ? memory : work;
+  static const double rates[][3] = {{5.5e6, 4.6e6, 3.2e6}, {5.0e6, 3.8e6, 2.3e6}}, each[] = {0.0025, 0.0033, 0.005};
+  const double memory = 2.0 * es * static_cast<double>(F) * static_cast<double>(D) / rates[es == 4][k];
+  const double steps = each[k] * static_cast<double>(D);
+  return 3.0 + (memory > steps ? memory : steps);
+}
+// The tiles' time for few tokens: choose() leaves w's way out of memory out (64 x 8192
+// x 16384: 132 us).
+double few_tiles_us(const Split& s, int64_t F, int64_t D, int es) {
+  const double memory = 4.0 + 2.0 * es * static_cast<double>(F) * static_cast<double>(D) / 4.4e6;
+  return memory > s.us ? memory : s.us;
+}
+
+// choose() with this layer's times of 64 k in the general kernel (fp32 takes them in
+// two slabs: 4.6 us busy, 2048 x 1024 x 2816) and of a range (dx of 32 x 1024 x 2816 in
+// 15 ranges 15.2 us with dw, in 44 17.0).
+Split divide(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, int es) {
+  return es == 2 ? choose(na, nb, nk, tiled, split, 1.15, 0.85, 0.06) : choose(na, nb, nk, tiled, split, 4.6, 1.4, 0.06);
 }
 
 template <typename E, bool ODD>
 hipError_t launch_few_of(const GatedFew& f, hipStream_t s) {
   const int64_t groups = round_up(ceil_div(f.F, 16), 8);
   const dim3 grid(static_cast<unsigned>(ODD ? groups * ceil_div(f.T, 32) : groups));
-  if (f.T <= 16) {
+  // Of a few tokens the waves' loads are nearly all of w, and more of them read a large one quicker
+  // (one token, 4096 x 12288: eight 37.2 us, four 38.8; 8192 x 16384: 107 and 124; 16 tokens: 43.4 and 41.9).
+  if (f.T <= 8 && static_cast<int64_t>(f.F) * f.D * 2 * static_cast<int64_t>(sizeof(E)) >= 128 << 20) {
+    hipLaunchKernelGGL((gated_few_kernel<E, ODD, 1, 8>), grid, dim3(512), 0, s, f);
+  } else if (f.T <= 16) {
     hipLaunchKernelGGL((gated_few_kernel<E, ODD, 1, 4>), grid, dim3(256), 0, s, f);
   } else if (ODD || f.T <= 32) {
     hipLaunchKernelGGL((gated_few_kernel<E, ODD, 2, 4>), grid, dim3(256), 0, s, f);
@@ -467,27 +489,27 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
     return o;
   };
   if (T > 0) {
-    p->fwd = choose(F2, T, D, tiled, false);
+    p->fwd = divide(F2, T, D, tiled, false, p->es);
     if (bf16 && !tiled && T > kFewTokens) {
-      const Split packed = choose(F2, T, D, true, false);
+      const Split packed = divide(F2, T, D, true, false, p->es);
       p->pack_fwd = packed.us + pack_us(F2, D) + pack_us(T, D) < p->fwd.us;
       if (p->pack_fwd) p->fwd = packed;
     }
-    p->few = T <= kFewTokens;
+    p->few = T <= kFewTokens && few_us(T, d.F, D, p->es) < few_tiles_us(p->fwd, d.F, D, p->es);
     p->fwd_x = take(p->pack_fwd ? static_cast<size_t>(T) * p->ld_pack * 2 : 0);
     p->fwd_w = take(p->pack_fwd ? static_cast<size_t>(F2) * p->ld_pack * 2 : 0);
     p->fwd_bytes = at;
     at = 0;
     p->ld_dz = round_up(F2, 64);
-    p->dx = choose(D, T, F2, tiled, true);
+    p->dx = divide(D, T, F2, tiled, true, p->es);
     if (bf16 && !tiled) {
-      const Split packed = choose(D, T, F2, true, true);
+      const Split packed = divide(D, T, F2, true, true, p->es);
       p->pack_dx = packed.us + pack_us(F2, D) < p->dx.us;
       if (p->pack_dx) p->dx = packed;
     }
-    p->dw = choose(D, F2, T, bf16, true);
+    p->dw = divide(D, F2, T, bf16, true, p->es);
     // Both gradients in general tiles take one launch, in which they overlap.
-    const Split dx64 = choose(D, T, F2, false, true), dw64 = choose(D, F2, T, false, false);
+    const Split dx64 = divide(D, T, F2, false, true, p->es), dw64 = divide(D, F2, T, false, false, p->es);
     const double longer = dx64.us > dw64.us ? dx64.us : dw64.us, other = dx64.us + dw64.us - longer;
     if (!p->pack_dx && longer + 0.5 * other < p->dx.us + p->dw.us + 4.0) {
       p->dx = dx64;

@@ -523,7 +523,9 @@ struct Gen {
   static constexpr int BUF = 64 * PITCH;
 };
 
-// 32 bytes of an operand's slab for this thread.
+// 32 bytes of an operand's slab for this thread.  In place of rows past the last one
+// others are read again, and what comes of them is not stored: with zeros there
+// every load waited for the slab before it, since either may be what fills a register.
 // GATED: 32 rows of each half of A, 16 of the first and the same of the second in turn,
 // so that a wave's two tiles are a gate's and what it multiplies.
 template <typename E, Order O, bool GATED>
@@ -534,19 +536,19 @@ __device__ inline void gen_load(const Operand& op, int64_t row0, int rows, int64
   const char* p;
   int n;
   if constexpr (GATED) {
-    const int r = tid >> 2, f = (r >> 5) * 16 + (r & 15);
+    const int r = tid >> 2, f = min((r >> 5) * 16 + (r & 15), rows - 1);
     const int64_t k = k0 + (tid & 3) * N;
-    n = f < rows ? static_cast<int>(min(k1 - k, static_cast<int64_t>(N))) : 0;
+    n = static_cast<int>(min(k1 - k, static_cast<int64_t>(N)));
     p = op.p + ((row0 + f + (r & 16 ? op.width : 0)) * op.ld + k) * static_cast<int64_t>(sizeof(E));
   } else if constexpr (O == kSum) {
-    const int r = tid >> 2;
+    const int r = min(tid >> 2, rows - 1);
     const int64_t k = k0 + (tid & 3) * N;
-    n = r < rows ? static_cast<int>(min(k1 - k, static_cast<int64_t>(N))) : 0;
+    n = static_cast<int>(min(k1 - k, static_cast<int64_t>(N)));
     p = op.p + ((row0 + r) * op.ld + k) * static_cast<int64_t>(sizeof(E));
   } else {
     constexpr int TPK = 64 / N;  // threads per k
     const int64_t k = k0 + tid / TPK;
-    const int c = (tid % TPK) * N;
+    const int c = (tid % TPK) * N < rows ? (tid % TPK) * N : 0;
     n = k < k1 ? min(rows - c, N) : 0;
     p = op.p + (k * op.ld + row0 + c) * static_cast<int64_t>(sizeof(E));
   }
@@ -1195,13 +1197,16 @@ constexpr int64_t kGBytes = 512ll << 20;
 // read once more.
 // Those fill at most kGBytes, as a piece of q does: what a call needs beside its
 // inputs and outputs stays linear in the tokens and in the vocabulary.
-inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) {
+// slab64, alone64: what a slab takes in the general kernel, busy and alone;
+// per_range: what each range costs the join beside its bytes.
+inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, double slab64 = 1.15,
+                    double alone64 = 0.7, double per_range = 0.0) {
   struct Kind {
     int32_t edge;
     int64_t at_once;  // workgroups on the device
     double slab, slab_alone, tile;
   };
-  static const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, 1.15, 0.7, 2.5}};
+  const Kind kinds[] = {{256, 256, 1.0, 1.0, 5.0}, {128, 512, 0.7, 0.55, 5.0}, {64, 1024, slab64, alone64, 2.5}};
   Split best = {64, 1, 1e300};
   for (const Kind& k : kinds) {
     if (k.edge != 64 && !tiled) continue;
@@ -1210,7 +1215,7 @@ inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split) 
       const int64_t n = tiles * r;
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
-      if (r > 1) us += 6.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
+      if (r > 1) us += 6.0 + per_range * r + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
       if (us < best.us) best = Split{k.edge, r, us};
     }
   }
