@@ -164,9 +164,9 @@ __global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
 
 // ----------------------------------------------------------------- dg and du
 //
-// [dg du] in rows of ld_dz, zeros past 2 F up to a multiple of eight (the tiled
-// kernel multiplies whole pieces of 16 bytes of them by zeros).  A thread takes
-// eight f of a row: 3 T F elements are read and 2 T F written.
+// [dg du] in rows of ld_dz, zeros past 2 F (what reads them takes whole pieces, and
+// multiplies the rest by zeros).  A thread takes eight f of a row: 3 T F elements are
+// read and 2 T F written.
 struct GatedDz {
   const float* kept;
   int64_t ld_kept;
@@ -236,10 +236,10 @@ __global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
         __builtin_memcpy(to + e * ES, &dg[e], ES);
         __builtin_memcpy(to + (z.F + e) * ES, &du[e], ES);
       }
-    // The row's last thread: zeros up to the next multiple of eight of 2 F.
-    const E zero = static_cast<E>(0.0f);
-    for (int e = 2 * z.F; e & 7; ++e) __builtin_memcpy(z.dz + (row * z.ld_dz + e) * ES, &zero, ES);
   }
+  if (c + 8 < z.F) return;
+  const E zero = static_cast<E>(0.0f);
+  for (int64_t e = 2 * z.F; e < z.ld_dz; ++e) __builtin_memcpy(z.dz + (row * z.ld_dz + e) * ES, &zero, ES);
 }
 
 // Both gradients in one launch: the first workgroups take dx's tiles and
@@ -257,6 +257,20 @@ __global__ __launch_bounds__(256) void gated_gen_grads_kernel(GemmArgs dx, GemmA
   }
 }
 
+// The same with dx by few_rows, at most 16 MT tokens.
+template <typename E, int MT>
+__global__ __launch_bounds__(256) void gated_few_grads_kernel(GemmArgs dx, GemmArgs dw) {
+  __shared__ GenLds<E> lds;
+  static_assert(sizeof(lds.buf) >= 4 * MT * 64 * sizeof(f32x4), "the sums fit");
+  const int n_dx = (dx.na + 15) / 16, i = static_cast<int>(blockIdx.x) - n_dx;
+  if (i < 0) {
+    few_rows<E, MT, kEpiStore>(dx, reinterpret_cast<f32x4*>(&lds.buf[0][0][0]), static_cast<int>(blockIdx.x) * 16);
+  } else {
+    const int ta = (dw.na + 63) / 64;
+    gen_tile<E, kRow, kRow, kEpiStore>(dw, lds, i % ta, i / ta, 0);
+  }
+}
+
 }  // namespace
 }  // namespace fconv
 
@@ -266,6 +280,7 @@ struct fconv_gated_plan_s {
   int64_t ld_kept;  // F in whole eights: kept is fp32 [T, 2, ld_kept]
   size_t kept_bytes;
   bool few;                       // at most kFewTokens, by their own kernel
+  bool few_dx;                    // dx by few_rows, in one launch with dw
   bool pack_fwd, pack_dx;         // rows of bf16 copied to 16-byte boundaries: x and w; w
   fconv::Split fwd, dx, dw;
   int64_t ld_pack;
@@ -278,6 +293,13 @@ namespace fconv {
 namespace {
 
 constexpr int32_t kFewTokens = 64;
+// 2 F up to which few_rows takes dx: its time grows with the sum, partial sums cost a launch more (both gradients
+// of 32 x 512 x 500 bf16 8.2 instead of 10.9 us, x 1000 10.0 and 10.7, of 64 x 512 x 1000 13.4 and 11.1; fp32, whose
+// fragments are twice as large, 11.1 and 13.2, 16.4 and 14.3, 24.6 and 16.1).
+int32_t few_dx_sum(int32_t T, int es) {
+  static const int32_t most[][3] = {{2048, 2048, 1024}, {2048, 1024, 704}};
+  return most[es == 4][T <= 16 ? 0 : T <= 32 ? 1 : 2];
+}
 
 // Time (us) of the few-token kernel: w out of memory, at a rate that falls with the
 // tokens (16, 32, 64), or the steps of a wave one after another (fitted to D 64 ..
@@ -413,6 +435,16 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
   gw.out = dw_whole ? dw : ws + p->o_dw;
   gw.ld_out = dw_whole ? args->lddw : round_up(d.D, 4);
   gw.part_stride = gw.ld_out * F2;
+  if (dx && p->few_dx) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(d.D, 16) + (dw ? ceil_div(d.D, 64) * ceil_div(F2, 64) : 0)));
+    if (d.T <= 16)
+      hipLaunchKernelGGL((gated_few_grads_kernel<E, 1>), grid, dim3(256), 0, s, gx, gw);
+    else if (d.T <= 32)
+      hipLaunchKernelGGL((gated_few_grads_kernel<E, 2>), grid, dim3(256), 0, s, gx, gw);
+    else
+      hipLaunchKernelGGL((gated_few_grads_kernel<E, 4>), grid, dim3(256), 0, s, gx, gw);
+    return hipGetLastError();
+  }
   if (dx && dw && dx_edge == 64 && p->dw.edge == 64 && dw_whole) {
     const dim3 grid(static_cast<unsigned>(ceil_div(d.D, 64) * (ceil_div(d.T, 64) * gx.ranges + ceil_div(F2, 64))));
     if (dx_whole)
@@ -515,6 +547,11 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
       p->dx = dx64;
       p->dw = dw64;
     }
+    p->few_dx = T <= kFewTokens && F2 <= few_dx_sum(d.T, p->es) && p->dw.edge == 64 && p->dw.ranges == 1;
+    if (p->few_dx) {
+      p->pack_dx = false;
+      p->dx.ranges = 1;
+    }
     const size_t ld4 = static_cast<size_t>(round_up(D, 4)) * 4;
     p->o_dz = take(static_cast<size_t>(T) * p->ld_dz * p->es);
     p->o_x = take(bf16 && p->dw.edge != 64 ? static_cast<size_t>(T) * p->ld_pack * 2 : 0);
@@ -595,6 +632,7 @@ const char* fconv_gated_plan_kernel_name(fconv_gated_plan p, int32_t product) {
   const Split* split = split_of(p, product);
   if (!split) return nullptr;
   if (product == FCONV_GATED_FORWARD && p->few) return "gated_few";
+  if (product == FCONV_GATED_DX && p->few_dx) return "gated_few_grads";
   const bool packed = product == FCONV_GATED_FORWARD ? p->pack_fwd
                       : product == FCONV_GATED_DX    ? p->pack_dx
                                                      : split->edge != 64 && p->d.D % 8 != 0;

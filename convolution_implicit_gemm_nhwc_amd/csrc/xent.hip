@@ -59,82 +59,6 @@ __global__ __launch_bounds__(256) void xent_gen_grads_kernel(GemmArgs dh, GemmAr
   }
 }
 
-// dh of at most 16 MT tokens over a short vocabulary, sixteen d of all tokens for
-// a workgroup, so that no partial sums go out and no launch joins them: its four
-// waves take turns at steps of 32 v and add their sums in LDS, in order.  A lane
-// picks its eight v of a column out of memory one by one, from any row distance
-// and alignment; rows of g are whole 64s, zeros past the vocabulary.
-template <typename E, int MT>
-__device__ inline void few_dh(const GemmArgs& g, f32x4* sums, int d0) {
-  using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
-  constexpr int ES = sizeof(E), STEPS = 2;  // of a turn, whose loads are in flight together
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  const int steps = (g.nk + 31) / 32;
-  const int64_t row = g.a.ld * ES;
-  // Columns past the last one read it again; they are not stored.
-  const char* wp = g.a.p + static_cast<int64_t>(min(d0 + r, g.na - 1)) * ES;
-  const char* gp[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j)
-    gp[j] = g.b.p + (static_cast<int64_t>(min(16 * j + r, g.nb - 1)) * g.b.ld + 8 * q) * ES;
-  struct Turn {
-    E a[STEPS][8];
-    Frag b[STEPS][MT];
-  };
-  auto load = [&](Turn& x, int first) __attribute__((always_inline)) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int step = first + 4 * s;
-      if (step >= steps) break;  // uniform
-      const int v = 32 * step + 8 * q;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        __builtin_memcpy(&x.a[s][e], wp + static_cast<int64_t>(min(v + e, g.nk - 1)) * row, ES);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) __builtin_memcpy(&x.b[s][j], gp[j] + static_cast<int64_t>(step) * 32 * ES, 8 * ES);
-    }
-  };
-  f32x4 acc[MT] = {};
-  auto multiply = [&](const Turn& x, int first) __attribute__((always_inline)) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int step = first + 4 * s;
-      if (step >= steps) break;
-      E v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 32 * step + 8 * q + e < g.nk ? x.a[s][e] : static_cast<E>(0.0f);
-      Frag a;
-      __builtin_memcpy(&a, v, sizeof(a));
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[j] = mma8(a, x.b[s][j], acc[j]);
-    }
-  };
-  Turn now, next;
-  constexpr int NEXT = 4 * STEPS;
-  int first = wave;
-  if (first < steps) load(now, first);
-  for (; first < steps; first += 2 * NEXT) {
-    if (first + NEXT < steps) load(next, first + NEXT);
-    multiply(now, first);
-    if (first + NEXT >= steps) break;
-    if (first + 2 * NEXT < steps) load(now, first + 2 * NEXT);
-    multiply(next, first + NEXT);
-  }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) sums[(wave * MT + j) * 64 + lane] = acc[j];
-  __syncthreads();
-  const int t = 16 * wave + r, d = d0 + 4 * q;
-  if (wave >= MT || t >= g.nb || d >= g.na) return;
-  f32x4 sum = sums[wave * 64 + lane];
-#pragma unroll
-  for (int x = 1; x < 4; ++x) sum += sums[(x * MT + wave) * 64 + lane];
-  sum *= g.scale[t];
-  if (g.row_map[t] < 0) sum = f32x4{0.f, 0.f, 0.f, 0.f};
-  store4<E>(g.out + (t * g.ld_out + d) * static_cast<int64_t>(ES), sum, g.na - d);
-}
-
 // The first workgroups take dh, the others (if dw is wanted) dw's tiles.
 template <typename E, int MT>
 __global__ __launch_bounds__(256) void xent_few_grads_kernel(GemmArgs dh, GemmArgs dw) {
@@ -142,7 +66,7 @@ __global__ __launch_bounds__(256) void xent_few_grads_kernel(GemmArgs dh, GemmAr
   static_assert(sizeof(lds.buf) >= 4 * MT * 64 * sizeof(f32x4), "the sums fit");
   const int n_dh = (dh.na + 15) / 16, i = static_cast<int>(blockIdx.x) - n_dh;
   if (i < 0) {
-    few_dh<E, MT>(dh, reinterpret_cast<f32x4*>(&lds.buf[0][0][0]), static_cast<int>(blockIdx.x) * 16);
+    few_rows<E, MT, kEpiOut>(dh, reinterpret_cast<f32x4*>(&lds.buf[0][0][0]), static_cast<int>(blockIdx.x) * 16);
   } else {
     const int ta = (dw.na + 63) / 64;
     gen_tile<E, kRow, kRow, kEpiOut>(dw, lds, i % ta, i / ta, 0);
