@@ -47,15 +47,18 @@ __device__ inline uint32_t usable(int64_t token, int64_t ignore, int32_t V) {
   return token != ignore && token >= 0 && token < V ? static_cast<uint32_t>(token) : kNoToken;
 }
 
-// 16 bytes of elements of type E.
+// 16 bytes of elements of type E.  A row's last piece, if it is not whole, is moved
+// back to end with the row (piece_at), so that every piece of a row of at least N
+// elements is whole: a load that may not happen waits for the one before it, since
+// either may be what fills a register (sums of 448 tokens of 667 columns: 18 us with
+// the last piece's elements one by one).  What two threads then both have is the
+// same in both.
 template <typename E>
 struct Vec {
   static constexpr int N = 16 / sizeof(E);
   E v[N];
-  // n of them at p, zeros past those.  WHOLE: all exist.  Where that is not known
-  // beforehand a load waits for the one before it, since either may be the one that
-  // fills a register.
-  template <bool WHOLE = false>
+  // WHOLE: rows of at least N elements; else n of them at p, zeros past those.
+  template <bool WHOLE>
   __device__ void load(const char* p, int n) {
     if (WHOLE || n >= N) {
       __builtin_memcpy(v, p, 16);
@@ -68,9 +71,9 @@ struct Vec {
     }
   }
   // PAST: past the caches.
-  template <bool PAST = false>
+  template <bool WHOLE, bool PAST = false>
   __device__ void store(char* p, int n) const {
-    if (n >= N) {
+    if (WHOLE || n >= N) {
       if constexpr (PAST) {
         typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
         Words w;
@@ -86,6 +89,11 @@ struct Vec {
     }
   }
 };
+// First column of a row's piece that begins with c.
+template <typename E, bool WHOLE>
+__device__ inline int piece_at(int c, int D) {
+  return WHOLE ? min(c, D - Vec<E>::N) : c;
+}
 
 // --------------------------------------------------------------------- lookup
 
@@ -119,7 +127,7 @@ __device__ inline void lookup(const LookupArgs& a) {
   for (int u = 0; u < U; ++u) {
     const uint32_t i = first + 256u * u;
     if (i >= total) break;
-    const int c = static_cast<int>(i % per_row) * N;
+    const int c = piece_at<E, WHOLE>(static_cast<int>(i % per_row) * N, a.D);
     if (usable(tok[u], a.ignore, a.V) != kNoToken) v[u].template load<WHOLE>(a.w + (tok[u] * a.ldw + c) * ES, a.D - c);
   }
 #pragma unroll
@@ -127,7 +135,7 @@ __device__ inline void lookup(const LookupArgs& a) {
     const uint32_t i = first + 256u * u;
     if (i >= total) break;
     const int64_t row = i / per_row;
-    const int c = static_cast<int>(i - static_cast<uint32_t>(row) * per_row) * N;
+    const int c = piece_at<E, WHOLE>(static_cast<int>(i - static_cast<uint32_t>(row) * per_row) * N, a.D);
     if (usable(tok[u], a.ignore, a.V) == kNoToken) {
       const float f = tok[u] == a.ignore ? 0.0f : __builtin_nanf("");
 #pragma unroll
@@ -136,13 +144,13 @@ __device__ inline void lookup(const LookupArgs& a) {
 #pragma unroll
       for (int e = 0; e < N; ++e) v[u].v[e] = static_cast<E>(a.scale * static_cast<float>(v[u].v[e]));
     }
-    v[u].store(a.y + (row * a.ldy + c) * ES, WHOLE ? N : a.D - c);
+    v[u].template store<WHOLE>(a.y + (row * a.ldy + c) * ES, a.D - c);
   }
 }
 
 template <typename E>
 __global__ __launch_bounds__(256) void embed_lookup_kernel(LookupArgs a) {
-  if (a.D % Vec<E>::N == 0)
+  if (a.D >= Vec<E>::N)
     lookup<E, true>(a);
   else
     lookup<E, false>(a);
@@ -184,22 +192,36 @@ __device__ inline int lower_bound(const uint64_t* keys, int n, uint64_t key) {
   return lo;
 }
 
-// scale sum, or that added to what is there.
+// scale sum, or that added to what is there, from column c on; the first `own` of
+// the columns are another thread's.
 template <typename E>
-__device__ inline void put_row(const GradArgs& g, uint32_t v, int c, const float (&sum)[Vec<E>::N]) {
+__device__ inline void put_row(const GradArgs& g, uint32_t v, int c, int own, const float (&sum)[Vec<E>::N]) {
   constexpr int N = Vec<E>::N;
-  const int n = g.D - c;
-  char* p = g.dw + (static_cast<int64_t>(v) * g.lddw + c) * static_cast<int64_t>(sizeof(E));
-  Vec<E> x;
-  if (g.add) {
-    x.load(p, n);
+  constexpr int64_t ES = sizeof(E);
+  char* p = g.dw + (static_cast<int64_t>(v) * g.lddw + c) * ES;
+  if (own == 0 && g.D - c >= N) {
+    Vec<E> x;
+    if (g.add) {
+      x.template load<true>(p, N);
 #pragma unroll
-    for (int e = 0; e < N; ++e) x.v[e] = static_cast<E>(__builtin_fmaf(g.scale, sum[e], static_cast<float>(x.v[e])));
-  } else {
+      for (int e = 0; e < N; ++e) x.v[e] = static_cast<E>(__builtin_fmaf(g.scale, sum[e], static_cast<float>(x.v[e])));
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) x.v[e] = static_cast<E>(g.scale * sum[e]);
+      for (int e = 0; e < N; ++e) x.v[e] = static_cast<E>(g.scale * sum[e]);
+    }
+    x.template store<true>(p, N);
+    return;
   }
-  x.store(p, n);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (e < own || c + e >= g.D) continue;
+    E x = static_cast<E>(g.scale * sum[e]);
+    if (g.add) {
+      __builtin_memcpy(&x, p + e * ES, ES);
+      x = static_cast<E>(__builtin_fmaf(g.scale, sum[e], static_cast<float>(x)));
+    }
+    __builtin_memcpy(p + e * ES, &x, ES);
+  }
 }
 
 // The keys of all (at most kSmall) tokens, sorted, in LDS.
@@ -215,12 +237,13 @@ __device__ inline void sort_small(const GradArgs& g, uint64_t* sorted) {
   __syncthreads();
 }
 
-// Sums of dy's rows: those of sorted keys [at, end), columns from c on.  Eight rows are in flight.  Without
+// Sums of dy's rows of a piece of the sorted keys, 16 bytes of columns from c on, of
+// which the first `own` are another thread's.  Eight rows are in flight.  Without
 // SMALL, a piece's first token may have begun before it and its last one may go on
 // behind it: their sums go to `part`.  With SMALL a token belongs to the piece in
 // which it begins, which then reads on.
 template <typename E, bool SMALL, bool WHOLE>
-__device__ inline void sum_piece(const GradArgs& g, const uint64_t* keys, int piece, int c) {
+__device__ inline void sum_piece(const GradArgs& g, const uint64_t* keys, int piece, int c, int own) {
   constexpr int N = Vec<E>::N, U = 8;
   constexpr int64_t ES = sizeof(E);
   int at = piece * g.piece;
@@ -243,7 +266,7 @@ __device__ inline void sum_piece(const GradArgs& g, const uint64_t* keys, int pi
         __builtin_memcpy(p + e, &x, 16);
       }
     } else {
-      put_row<E>(g, now, c, sum);
+      put_row<E>(g, now, c, own, sum);
     }
   };
   bool done = now == kNoToken;  // tokens without a gradient come last
@@ -286,10 +309,12 @@ __device__ inline void sum_rows(const GradArgs& g, const uint64_t* keys) {
   const int piece = blockIdx.x / g.col_blocks * teams + threadIdx.x / g.team;
   const int c = (block * g.team + threadIdx.x % g.team) * N;
   if (piece >= g.pieces || c >= g.D) return;
-  if (c + N <= g.D)
-    sum_piece<E, SMALL, true>(g, keys, piece, c);
-  else
-    sum_piece<E, SMALL, false>(g, keys, piece, c);
+  if (g.D >= N) {
+    const int at = piece_at<E, true>(c, g.D);
+    sum_piece<E, SMALL, true>(g, keys, piece, at, c - at);
+  } else {
+    sum_piece<E, SMALL, false>(g, keys, piece, c, 0);
+  }
 }
 
 constexpr int kZeroRows = 1024;  // of a workgroup, at most
@@ -337,13 +362,13 @@ __device__ inline void zero_rows(const GradArgs& g, int group) {
   for (int e = 0; e < N; ++e) z.v[e] = static_cast<E>(0.0f);
   for (uint32_t i = tid; i < total; i += THREADS) {
     const uint32_t row = i / per_row;
-    const int c = static_cast<int>(i - row * per_row) * N;
+    const int c0 = static_cast<int>(i - row * per_row) * N, c = g.D >= N ? piece_at<E, true>(c0, g.D) : c0;
     if (used[row / 32] >> (row % 32) & 1) continue;
     char* p = g.dw + ((v0 + static_cast<int64_t>(row)) * g.lddw + c) * ES;
     if (g.past)
-      z.template store<true>(p, g.D - c);
+      z.template store<false, true>(p, g.D - c);
     else
-      z.store(p, g.D - c);
+      z.template store<false>(p, g.D - c);
   }
 }
 
@@ -683,12 +708,18 @@ fconv_status fconv_embed_plan_create(const fconv_embed_desc* desc, fconv_embed_p
   p->chunk = static_cast<int32_t>(T <= kChunk ? round_up(T < 64 ? 64 : T, 64) : round_up(ceil_div(T, kWays), 64));
   if (p->chunk > kChunk) p->chunk = kChunk;
   for (int64_t run = p->chunk; run < T; run *= kWays) ++p->merges;
-  p->piece = T <= 4096 ? 16 : T <= 32768 ? 32 : 64;
-  p->pieces = static_cast<int32_t>(ceil_div(T, p->piece));
   p->team = 8;
   while (p->team < 256 && p->team < vecs) p->team *= 2;
   p->col_blocks = static_cast<int32_t>(ceil_div(vecs, p->team));
-  int64_t rows = (256 << 10) / (static_cast<int64_t>(d.D) * p->es);
+  // Long pieces leave fewer sums to join; four workgroups a CU hide the reads' latency.
+  p->piece = 64;
+  while (p->piece > 16 && ceil_div(ceil_div(T, p->piece), 256 / p->team) * p->col_blocks < 1024) p->piece /= 2;
+  p->pieces = static_cast<int32_t>(ceil_div(T, p->piece));
+  // Up to 256 KB of zeros for a workgroup; less of a small table, for more workgroups, as long as these do not look
+  // through more than 32 MB of tokens.
+  int64_t rows = (256 << 10) / (static_cast<int64_t>(d.D) * p->es), most = (4ll << 20) / (T > 0 ? T : 1);
+  most = most > 1024 ? 1024 : most < 1 ? 1 : most;
+  if (rows > ceil_div(d.V, most)) rows = ceil_div(d.V, most);
   p->zero_rows = static_cast<int32_t>(rows < 4 ? 4 : rows > kZeroRows ? kZeroRows : rows);
   p->ld_part = round_up(d.D, 8);
   if (!p->small) {

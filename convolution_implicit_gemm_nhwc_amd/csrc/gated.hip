@@ -318,12 +318,50 @@ double few_tiles_us(const Split& s, int64_t F, int64_t D, int es) {
   return memory > s.us ? memory : s.us;
 }
 
-// choose() with this layer's times of 64 k in the general kernel (fp32 takes them in
-// two slabs: 4.6 us busy, 2048 x 1024 x 2816) and of a range (dx of 32 x 1024 x 2816 in
-// 15 ranges 15.2 us with dw, in 44 17.0).
-Split divide(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, int es) {
-  return es == 2 ? choose(na, nb, nk, tiled, split, 1.15, 0.85, 0.06) : choose(na, nb, nk, tiled, split, 4.6, 1.4, 0.06);
+// What 64 k take in the general kernel (us) of a workgroup alone on its CU and of one
+// among four.  Forward both operands' k are contiguous (69 x 2590 x 704: 0.55 alone),
+// backward a fragment is transposed.  Rows of bf16 that are not aligned take longer
+// where the CU is busy (384 x 3754 x 5440: 1.75); fp32 takes 64 k in two slabs (2048 x
+// 1024 x 2816: 4.6).
+struct Slab {
+  double alone, busy;
+  double us(int64_t n) const {  // of n workgroups
+    return n <= 256 ? alone : n >= 1024 ? busy : alone + (busy - alone) * static_cast<double>(n - 256) / 768.0;
+  }
+};
+Slab slab_us(int64_t D, int es, bool forward) {
+  return es == 4 ? Slab{2.3, 4.6} : Slab{forward ? 0.6 : 0.85, D % 8 ? 1.9 : 1.15};
 }
+// What r ranges of na x nb values cost beside their slabs: a launch that joins them, and their bytes (dx of 32 x
+// 1024 x 2816 in 15 ranges 15.2 us with dw, in 44 17.0).
+double ranges_us(int32_t r, int64_t na, int64_t nb) {
+  return r == 1 ? 0.0 : 6.0 + 0.06 * r + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
+}
+// The division of a product in general tiles, `beside` other workgroups of
+// `beside_slabs` in the same launch.
+Split general(int64_t na, int64_t nb, int64_t nk, bool split, const Slab& slab, int64_t beside = 0,
+              int64_t beside_slabs = 0) {
+  const int64_t tiles = ceil_div(na, 64) * ceil_div(nb, 64), slabs = ceil_div(nk, 64);
+  Split best = {64, 1, 1e300};
+  for (int32_t r = 1; r <= (split ? 128 : 1) && (r == 1 || (slabs / r >= 2 && r * na * nb * 4 <= kGBytes)); ++r) {
+    const int64_t n = tiles * r + beside, own = ceil_div(slabs, r), most = own > beside_slabs ? own : beside_slabs;
+    double us = static_cast<double>(most) * slab.us(n) + 2.5;
+    // More of them than the device holds: their work.
+    const double work = (static_cast<double>(tiles * slabs + beside * beside_slabs) * slab.busy + 2.5 * static_cast<double>(n)) / 1024.0;
+    us = (work > us ? work : us) + ranges_us(r, na, nb);
+    if (us < best.us) best = Split{64, r, us};
+  }
+  return best;
+}
+// In general tiles or, where they can be, in those of 128 or 256.
+Split divide(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, const Slab& slab) {
+  const Split g = general(na, nb, nk, split, slab);
+  if (!tiled) return g;
+  const Split t = choose(na, nb, nk, true, split, 1e9, 1e9);
+  return t.edge != 64 && t.us < g.us ? t : g;
+}
+// Time (us) of copying a matrix to 16-byte boundaries (10880 x 3754: 26).
+double copy_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 6e6; }
 
 template <typename E, bool ODD>
 hipError_t launch_few_of(const GatedFew& f, hipStream_t s) {
@@ -521,10 +559,11 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
     return o;
   };
   if (T > 0) {
-    p->fwd = divide(F2, T, D, tiled, false, p->es);
+    const Slab fwd = slab_us(D, p->es, true), bwd = slab_us(D, p->es, false);
+    p->fwd = divide(F2, T, D, tiled, false, fwd);
     if (bf16 && !tiled && T > kFewTokens) {
-      const Split packed = divide(F2, T, D, true, false, p->es);
-      p->pack_fwd = packed.us + pack_us(F2, D) + pack_us(T, D) < p->fwd.us;
+      const Split packed = divide(F2, T, D, true, false, fwd);
+      p->pack_fwd = packed.edge != 64 && packed.us + copy_us(F2, D) + copy_us(T, D) < p->fwd.us;
       if (p->pack_fwd) p->fwd = packed;
     }
     p->few = T <= kFewTokens && few_us(T, d.F, D, p->es) < few_tiles_us(p->fwd, d.F, D, p->es);
@@ -533,19 +572,24 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
     p->fwd_bytes = at;
     at = 0;
     p->ld_dz = round_up(F2, 64);
-    p->dx = divide(D, T, F2, tiled, true, p->es);
+    p->dx = divide(D, T, F2, tiled, true, bwd);
+    double dx_us = p->dx.us;
     if (bf16 && !tiled) {
-      const Split packed = divide(D, T, F2, true, true, p->es);
-      p->pack_dx = packed.us + pack_us(F2, D) < p->dx.us;
-      if (p->pack_dx) p->dx = packed;
+      const Split packed = divide(D, T, F2, true, true, bwd);
+      p->pack_dx = packed.edge != 64 && packed.us + copy_us(F2, D) < p->dx.us;
+      if (p->pack_dx) {
+        p->dx = packed;
+        dx_us = packed.us + copy_us(F2, D);
+      }
     }
-    p->dw = divide(D, F2, T, bf16, true, p->es);
+    p->dw = divide(D, F2, T, bf16, true, bwd);
+    const double dw_us = p->dw.us + (bf16 && !tiled && p->dw.edge != 64 ? copy_us(T, D) : 0.0);
     // Both gradients in general tiles take one launch, in which they overlap.
-    const Split dx64 = divide(D, T, F2, false, true, p->es), dw64 = divide(D, F2, T, false, false, p->es);
-    const double longer = dx64.us > dw64.us ? dx64.us : dw64.us, other = dx64.us + dw64.us - longer;
-    if (!p->pack_dx && longer + 0.5 * other < p->dx.us + p->dw.us + 4.0) {
-      p->dx = dx64;
-      p->dw = dw64;
+    const Split both = general(D, T, F2, true, bwd, ceil_div(D, 64) * ceil_div(F2, 64), ceil_div(T, 64));
+    if (both.us < dx_us + dw_us + 4.0) {
+      p->pack_dx = false;
+      p->dx = both;
+      p->dw = Split{64, 1, both.us};
     }
     p->few_dx = T <= kFewTokens && F2 <= few_dx_sum(d.T, p->es) && p->dw.edge == 64 && p->dw.ranges == 1;
     if (p->few_dx) {

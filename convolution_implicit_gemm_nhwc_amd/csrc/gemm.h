@@ -1277,10 +1277,9 @@ constexpr int64_t kGBytes = 512ll << 20;
 // read once more.
 // Those fill at most kGBytes, as a piece of q does: what a call needs beside its
 // inputs and outputs stays linear in the tokens and in the vocabulary.
-// slab64, alone64: what a slab takes in the general kernel, busy and alone;
-// per_range: what each range costs the join beside its bytes.
+// slab64, alone64: what a slab takes in the general kernel, busy and alone.
 inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, double slab64 = 1.15,
-                    double alone64 = 0.7, double per_range = 0.0) {
+                    double alone64 = 0.7) {
   struct Kind {
     int32_t edge;
     int64_t at_once;  // workgroups on the device
@@ -1295,7 +1294,7 @@ inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, 
       const int64_t n = tiles * r;
       double us = static_cast<double>(ceil_div(n, k.at_once)) *
                   (static_cast<double>(ceil_div(slabs, r)) * (n > 256 ? k.slab : k.slab_alone) + k.tile);
-      if (r > 1) us += 6.0 + per_range * r + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
+      if (r > 1) us += 6.0 + 8.0 * r * static_cast<double>(na) * static_cast<double>(nb) / 4e6;
       if (us < best.us) best = Split{k.edge, r, us};
     }
   }
