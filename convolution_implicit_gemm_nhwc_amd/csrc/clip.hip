@@ -12,8 +12,8 @@
 //   scale    every workgroup adds up to kOwnParts sums itself, in the same order,
 //            which is quicker than a launch, then scales its chunks, the last one
 //            first: the last-level cache still holds what `squares` read last, and
-//            its own results go past it (505 million bf16 gradients: 537 us instead
-//            of 600)
+//            results that it could not hold go past it (505 million bf16 gradients:
+//            537 us instead of 600)
 // Squares and sums are in 64 bits: in 32 those of gradients above 2^64 are infinite
 // and those below 2^-75 vanish.
 #include <hip/hip_runtime.h>
@@ -53,6 +53,7 @@ struct ScaleArgs {
   int32_t n_parts;
   float* write_norm;    // the norm is written there by the first workgroup, or NULL
   float max_norm, eps;
+  bool past;            // results go past the caches
 };
 
 struct Chunk {
@@ -132,13 +133,15 @@ struct Pieces {
       }
     }
   }
-  // Past the caches.
-  __device__ void store(char* p, int left) const {
+  __device__ void store(char* p, int left, bool past) const {
     typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (at(u) + 16 <= left) {
-        __builtin_nontemporal_store(Words{d[u][0], d[u][1], d[u][2], d[u][3]}, reinterpret_cast<Words*>(p + at(u)));
+      const Words w = {d[u][0], d[u][1], d[u][2], d[u][3]};
+      if (at(u) + 16 <= left && past) {
+        __builtin_nontemporal_store(w, reinterpret_cast<Words*>(p + at(u)));
+      } else if (at(u) + 16 <= left) {
+        *reinterpret_cast<Words*>(p + at(u)) = w;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -242,7 +245,7 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(Batch b, ScaleArgs a) {
             }
           }
       }
-      x.store(c.out, c.left);
+      x.store(c.out, c.left, a.past);
     }
     if (!w.more()) break;
   }
@@ -257,6 +260,7 @@ struct fconv_clip_plan_s {
   float eps = 0.0f;
   int32_t parts = 0;  // sums of all launches
   size_t bytes = 0;   // of the sums, and the norm behind them
+  int64_t total = 0;  // bytes of all tensors
   ~fconv_clip_plan_s() { delete[] tensors; }
 };
 
@@ -265,6 +269,7 @@ namespace {
 
 constexpr int64_t kMaxNumel = 1ll << 40, kMaxTotal = 1ll << 43;
 constexpr int32_t kMaxTensors = 1 << 20;
+constexpr int64_t kCacheBytes = 256ll << 20;  // the last-level cache
 
 int elem_size(const fconv_clip_tensor& t) { return t.dtype == FCONV_BF16 ? 2 : 4; }
 int64_t chunks_of(const fconv_clip_tensor& t) { return ceil_div(t.numel * elem_size(t), kChunkBytes); }
@@ -321,6 +326,7 @@ hipError_t run(const fconv_clip_plan_s* p, const fconv_clip_args* a, bool clip, 
   ScaleArgs c = {};
   c.max_norm = a->max_norm;
   c.eps = p->eps;
+  c.past = p->total > kCacheBytes;
   if (given) {
     c.norm = a->given_norm;
   } else if (!clip || n == 0 || n > kOwnParts) {
@@ -429,6 +435,7 @@ fconv_status fconv_clip_plan_create(const fconv_clip_tensor* tensors, int32_t n,
   p->eps = eps;
   each_batch(p, [&](int32_t, int32_t, int64_t chunks) {
     p->parts += groups_of(chunks);
+    p->total += chunks * kChunkBytes;
     return true;
   });
   p->bytes = static_cast<size_t>(p->parts) * 8 + 16;
