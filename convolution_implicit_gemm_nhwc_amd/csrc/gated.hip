@@ -281,6 +281,7 @@ struct fconv_gated_plan_s {
   size_t kept_bytes;
   bool few;                       // at most kFewTokens, by their own kernel
   bool few_dx;                    // dx by few_rows, in one launch with dw
+  bool pair;                      // both gradients in one launch of tiles
   bool pack_fwd, pack_dx;         // rows of bf16 copied to 16-byte boundaries: x and w; w
   fconv::Split fwd, dx, dw;
   int64_t ld_pack;
@@ -360,6 +361,41 @@ Split divide(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, const S
   const Split t = choose(na, nb, nk, true, split, 1e9, 1e9);
   return t.edge != 64 && t.us < g.us ? t : g;
 }
+// dx's ranges where it shares a launch of tiles of one edge with dw (of one range),
+// and the time of both: dx's tiles first, dw's as places become free.
+Split pair(int64_t T, int64_t D, int64_t F2) {
+  struct Kind {
+    int32_t edge;
+    int64_t at_once;
+    double slab;
+  };
+  Split best = {64, 1, 1e300};
+  for (const Kind& k : {Kind{256, 256, 1.0}, Kind{128, 512, 0.7}}) {
+    const int64_t tx = ceil_div(D, k.edge) * ceil_div(T, k.edge), tw = ceil_div(D, k.edge) * ceil_div(F2, k.edge);
+    const int64_t sx = ceil_div(F2, 64);
+    const double each_w = static_cast<double>(ceil_div(T, 64)) * k.slab + 5.0;
+    for (int32_t r = 1; r <= 128 && (r == 1 || (sx / r >= 2 && r * D * T * 4 <= kGBytes)); ++r) {
+      const int64_t n = tx * r, late = n % k.at_once;  // places that dx leaves a turn later than the others
+      const double each_x = static_cast<double>(ceil_div(sx, r)) * k.slab + 5.0;
+      const double first = static_cast<double>(n / k.at_once) * each_x, second = first + each_x;
+      // The first time by which all of dw's tiles fit, in turns after either.
+      double us = 1e300;
+      for (int i = 0; i < 2; ++i) {
+        const double from = i ? second : first;
+        for (int64_t turns = 0; turns <= ceil_div(tw, k.at_once) + 1; ++turns) {
+          const double end = from + static_cast<double>(turns) * each_w;
+          if (end < (late ? second : first) || end >= us) continue;
+          const int64_t a = static_cast<int64_t>((end - first) / each_w + 1e-6), b = static_cast<int64_t>((end - second) / each_w + 1e-6);
+          if ((k.at_once - late) * a + late * (b > 0 ? b : 0) >= tw) us = end;
+        }
+      }
+      // A range's sums go out and come back (4 TB/s), and a launch joins them.
+      if (r > 1) us += 6.0 + 8.0 * r * static_cast<double>(D) * static_cast<double>(T) / 4e6;
+      if (us < best.us) best = Split{k.edge, r, us};
+    }
+  }
+  return best;
+}
 // Time (us) of copying a matrix to 16-byte boundaries (10880 x 3754: 26).
 double copy_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 6e6; }
 
@@ -419,6 +455,19 @@ hipError_t run_forward(const fconv_gated_plan_s* p, const fconv_gated_args* args
   g.kept = static_cast<float*>(args->kept);
   g.ld_kept = p->ld_kept;
   return launch_gemm<E, kSum, kSum, kEpiGated>(g, edge, s);
+}
+
+// Both gradients in one launch of tiles of an edge.
+template <Epilogue EPI_X, Epilogue EPI_Y>
+hipError_t launch_pair(const GemmArgs& x, const GemmArgs& y, int edge, hipStream_t s) {
+  auto blocks = [&](const GemmArgs& g) { return tile_blocks(ceil_div(g.na, edge) * ceil_div(g.nb, edge) * g.ranges, edge); };
+  const unsigned bx = blocks(x);
+  const dim3 grid(bx + blocks(y));
+  if (edge == 256)
+    hipLaunchKernelGGL((gemm_tile_pair_kernel<EPI_X, EPI_Y, 128, 8>), grid, dim3(512), 0, s, x, y, bx);
+  else
+    hipLaunchKernelGGL((gemm_tile_pair_kernel<EPI_X, EPI_Y, 64, 4>), grid, dim3(256), 0, s, x, y, bx);
+  return hipGetLastError();
 }
 
 template <typename E>
@@ -483,6 +532,9 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
       hipLaunchKernelGGL((gated_few_grads_kernel<E, 4>), grid, dim3(256), 0, s, gx, gw);
     return hipGetLastError();
   }
+  // Past the caches where dw is larger than the L2s together and written in whole lines.
+  const bool past = p->es == 2 && static_cast<int64_t>(F2) * d.D * 2 > (32 << 20) && d.D % 64 == 0 &&
+                    args->lddw % 64 == 0 && (reinterpret_cast<uintptr_t>(dw) & 127) == 0;
   if (dx && dw && dx_edge == 64 && p->dw.edge == 64 && dw_whole) {
     const dim3 grid(static_cast<unsigned>(ceil_div(d.D, 64) * (ceil_div(d.T, 64) * gx.ranges + ceil_div(F2, 64))));
     if (dx_whole)
@@ -490,6 +542,13 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
     else
       hipLaunchKernelGGL((gated_gen_grads_kernel<E, kEpiPart>), grid, dim3(256), 0, s, gx, gw);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else if (dx && dw && p->pair && dx_edge == p->dw.edge) {
+    if constexpr (sizeof(E) == 2)
+      e = dx_whole ? past ? launch_pair<kEpiStore, kEpiStoreStream>(gx, gw, dx_edge, s)
+                          : launch_pair<kEpiStore, kEpiStore>(gx, gw, dx_edge, s)
+          : past ? launch_pair<kEpiPart, kEpiStoreStream>(gx, gw, dx_edge, s)
+                 : launch_pair<kEpiPart, kEpiStore>(gx, gw, dx_edge, s);
+    if (e != hipSuccess) return e;
   } else {
     if (dx) {
       e = dx_whole ? launch_gemm<E, kRow, kSum, kEpiStore>(gx, dx_edge, s)
@@ -497,9 +556,6 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
       if (e != hipSuccess) return e;
     }
     if (dw) {
-      // Past the caches where dw is larger than the L2s together and written in whole lines.
-      const bool past = p->es == 2 && static_cast<int64_t>(F2) * d.D * 2 > (32 << 20) && d.D % 64 == 0 &&
-                        args->lddw % 64 == 0 && (reinterpret_cast<uintptr_t>(dw) & 127) == 0;
       e = !dw_whole ? launch_gemm<E, kRow, kRow, kEpiPart>(gw, p->dw.edge, s)
           : past    ? launch_gemm<E, kRow, kRow, kEpiStoreStream>(gw, p->dw.edge, s)
                     : launch_gemm<E, kRow, kRow, kEpiStore>(gw, p->dw.edge, s);
@@ -586,12 +642,23 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
     const double dw_us = p->dw.us + (bf16 && !tiled && p->dw.edge != 64 ? copy_us(T, D) : 0.0);
     // Both gradients in general tiles take one launch, in which they overlap.
     const Split both = general(D, T, F2, true, bwd, ceil_div(D, 64) * ceil_div(F2, 64), ceil_div(T, 64));
-    if (both.us < dx_us + dw_us + 4.0) {
+    double us = dx_us + dw_us + 4.0;
+    if (both.us < us) {
+      us = both.us;
       p->pack_dx = false;
       p->dx = both;
       p->dw = Split{64, 1, both.us};
     }
-    p->few_dx = T <= kFewTokens && F2 <= few_dx_sum(d.T, p->es) && p->dw.edge == 64 && p->dw.ranges == 1;
+    if (bf16) {
+      const Split tiles = pair(T, D, F2);
+      if (tiles.us + (tiled ? 0.0 : copy_us(F2, D) + copy_us(T, D)) < us) {
+        p->pair = true;
+        p->pack_dx = !tiled;
+        p->dx = tiles;
+        p->dw = Split{tiles.edge, 1, tiles.us};
+      }
+    }
+    p->few_dx = T <= kFewTokens && F2 <= few_dx_sum(d.T, p->es) && !p->pair && p->dw.edge == 64 && p->dw.ranges == 1;
     if (p->few_dx) {
       p->pack_dx = false;
       p->dx.ranges = 1;

@@ -889,17 +889,13 @@ struct Frags {
   }
 };
 
+// Workgroup `block` of `blocks`.
 template <Order OA, Order OB, Epilogue EPI, int H, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
+__device__ __forceinline__ void tile_work(const GemmArgs& g, char* ab0, char* b01, char* a01, char* ab1, char* b11, char* a11,
+                                          float2* red, unsigned block, unsigned blocks) {
   constexpr int MI = H / 32, MJ = 2 * H / (16 * NW);  // matrix tiles of a wave in a quadrant
   constexpr int HB = H * 128;                         // bytes of a half tile
   static_assert(HB == NW * 2048, "two copies per wave and half tile");
-  // Arrays of their own, so that the compiler sees which copies a read does not
-  // meet; few enough for it to follow them all (A0 and B0 go together).
-  __shared__ __attribute__((aligned(1024))) char ab0[2 * HB], b01[HB], a01[HB];
-  __shared__ __attribute__((aligned(1024))) char ab1[2 * HB], b11[HB], a11[HB];
-  __shared__ float2 red[EPI == kEpiLse ? 4 * H : 1];
-
   const int live = g.n_live ? *g.n_live : 0;
   const int nb = g.n_live && OB == kSum ? live : g.nb;
   const int nk = g.n_live && OB == kRow ? live : g.nk;
@@ -911,8 +907,8 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
   const int tiles_a = (g.na + EA - 1) / EA, tiles_b = (nb + 2 * H - 1) / (2 * H);
   const int tiles = tiles_a * tiles_b;
   const int total = tiles * g.ranges, share = (total + 7) / 8;
-  const int first_id = (blockIdx.x % 8) * share, end = min(share, total - first_id);
-  int slot = blockIdx.x / 8;
+  const int first_id = (block % 8) * share, end = min(share, total - first_id);
+  int slot = block / 8;
   if (slot >= end) return;
   const int all = (nk + 63) / 64, per = (all + g.ranges - 1) / g.ranges;  // slabs: of all ranges, of one
   struct Place {
@@ -1069,7 +1065,7 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
     auto per_b = load_per_b<EPI, 2 * MJ>(g, at.a0, at.b0, at.ra, at.rb, b_of);
     have_per_b<EPI, 2 * MJ>(per_b);
     const Place done = at;
-    slot += gridDim.x / 8;
+    slot += blocks / 8;
     const bool more = slot < end;
     if (more) {
       at = locate(first_id + slot);
@@ -1079,6 +1075,34 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
                                                  done.range, wa, q, a_of, b_of, red);
     if (!more) break;
   }
+}
+
+// Arrays of their own, so that the compiler sees which copies a read does not
+// meet; few enough for it to follow them all (A0 and B0 go together).
+#define FCONV_TILE_LDS(H)                                                                      \
+  __shared__ __attribute__((aligned(1024))) char ab0[2 * H * 128], b01[H * 128], a01[H * 128]; \
+  __shared__ __attribute__((aligned(1024))) char ab1[2 * H * 128], b11[H * 128], a11[H * 128]
+
+template <Order OA, Order OB, Epilogue EPI, int H, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
+  FCONV_TILE_LDS(H);
+  __shared__ float2 red[EPI == kEpiLse ? 4 * H : 1];
+  tile_work<OA, OB, EPI, H, NW>(g, ab0, b01, a01, ab1, b11, a11, red, blockIdx.x, gridDim.x);
+}
+
+// Two products in one launch, C[b, a] of x with B's k contiguous, of y with its rows:
+// workgroups of y start as those of x end, so that neither leaves CUs idle at its end.
+// The first blocks_x (a multiple of eight) are x's.
+template <Epilogue EPI_X, Epilogue EPI_Y, int H, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void gemm_tile_pair_kernel(GemmArgs x, GemmArgs y, unsigned blocks_x) {
+  FCONV_TILE_LDS(H);
+  __shared__ float2 red[1];
+  const unsigned block = blockIdx.x;
+  if (block < blocks_x)
+    tile_work<kRow, kSum, EPI_X, H, NW>(x, ab0, b01, a01, ab1, b11, a11, red, block, blocks_x);
+  else
+    tile_work<kRow, kRow, EPI_Y, H, NW>(y, ab0, b01, a01, ab1, b11, a11, red, block - blocks_x,
+                                        gridDim.x - blocks_x);
 }
 
 // BYTES of elements from p on, in registers.  Loads of 16 bytes whose address is
@@ -1304,15 +1328,19 @@ inline Split choose(int64_t na, int64_t nb, int64_t nk, bool tiled, bool split, 
 // Time (us) of packing a matrix: a launch, one read and one write.
 inline double pack_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 4e6; }
 
+// Workgroups of the tiled kernel for n tiles: as many as the device holds at once (one
+// or two a CU, by their LDS), in eighths; each takes every so manieth tile of its XCD's share.
+inline unsigned tile_blocks(int64_t n, int edge) {
+  const int64_t most = edge == 256 ? 256 : 512, blocks = round_up(n, 8);
+  return static_cast<unsigned>(blocks < most ? blocks : most);
+}
+
 // The kernel of a product: tiles of 64 (general), 128 or 256.
 template <typename E, Order OA, Order OB, Epilogue EPI>
 hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
   const int64_t ta = ceil_div((EPI == kEpiGated ? 2ll : 1ll) * g.na, edge), tb = ceil_div(g.nb, edge);
   if constexpr (sizeof(E) == 2) {
-    // As many workgroups as the device holds at once (one or two a CU, by their
-    // LDS), in eighths; each takes every so manieth tile of its XCD's share.
-    const int64_t most = edge == 256 ? 256 : 512, n = round_up(ta * tb * g.ranges, 8);
-    const dim3 grid(static_cast<unsigned>(n < most ? n : most));
+    const dim3 grid(tile_blocks(ta * tb * g.ranges, edge));
     if (edge == 256)
       hipLaunchKernelGGL((gemm_tile_kernel<OA, OB, EPI, 128, 8>), grid, dim3(512), 0, s, g);
     else if (edge == 128)
