@@ -718,7 +718,7 @@ fconv_status fconv_embed_plan_create(const fconv_embed_desc* desc, fconv_embed_p
   // Up to 256 KB of zeros for a workgroup; less of a small table, for more workgroups, as long as these do not look
   // through more than 32 MB of tokens.
   int64_t rows = (256 << 10) / (static_cast<int64_t>(d.D) * p->es), most = (4ll << 20) / (T > 0 ? T : 1);
-  most = most > 1024 ? 1024 : most < 1 ? 1 : most;
+  most = most > 512 ? 512 : most < 1 ? 1 : most;
   if (rows > ceil_div(d.V, most)) rows = ceil_div(d.V, most);
   p->zero_rows = static_cast<int32_t>(rows < 4 ? 4 : rows > kZeroRows ? kZeroRows : rows);
   p->ld_part = round_up(d.D, 8);
