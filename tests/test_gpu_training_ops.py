@@ -33,6 +33,8 @@ def _embed(T, D, V, dtype, dev):
 
     def run(stream=None):
         added = base.clone()
+        if stream is not None:        # the clone is work of the current stream
+            torch.cuda.current_stream().synchronize()
         y, dw = p.forward(w, token, stream=stream), p.backward(token, dy, stream=stream)
         return y, dw, p.backward(token, dy, dw=added, accumulate=True, stream=stream)
     return run, (w, dy, base)
