@@ -108,3 +108,33 @@ def test_every_activation(T, D, F, dtype, name):
     dev = device()
     say("gated", name, T, D, F, dtype)
     check(*case(T, D, F, dtype, dev, seed=1, spread=6.0), dtype, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,D,F", [(70, 33, 21), (200, 101, 333), (960, 72, 119), (500, 5, 7), (130, 250, 43)])
+@pytest.mark.parametrize("gap", [1, 7, 40])
+def test_what_lies_between_rows_reaches_nothing(T, D, F, gap, dtype):
+    # Loads of a row's last elements may read what follows them.
+    dev = device()
+    say("between rows:", T, D, F, gap, dtype)
+    x, w, dy = case(T, D, F, dtype, dev)
+    p = fc.GatedPlan(T, D, F, dtype, "silu")
+    y, kept = p.forward(x, w, keep=True)
+    dx, dw = p.backward(x, w, kept, dy)
+
+    def apart(t):
+        whole = torch.full((t.shape[0], t.shape[1] + gap), float("nan"), dtype=t.dtype, device=dev)
+        whole[:, :t.shape[1]] = t
+        return whole[:, :t.shape[1]]
+    x2, w2, dy2 = apart(x), apart(w), apart(dy)
+    y2, kept2 = p.forward(x2, w2, keep=True)
+    out = [torch.full((r, D + gap), 5.0, dtype=x.dtype, device=dev) for r in (T, 2 * F)]
+    dx2, dw2 = p.backward(x2, w2, kept2, dy2, dx=out[0][:, :D], dw=out[1][:, :D])
+    # Rows elsewhere in memory may be multiplied by another kernel: off by its order of
+    # the sum, then one rounding more.
+    for a, b, n in ((y, y2, D), (dx, dx2, 2 * F), (dw, dw2, T)):
+        eps = torch.finfo(x.dtype).eps + 4 * n * torch.finfo(torch.float32).eps
+        assert not torch.isnan(b).any()
+        assert (a.double() - b.double()).norm() <= eps * a.double().norm()
+    for o in out:
+        assert (o[:, D:] == 5.0).all()
