@@ -40,13 +40,18 @@ static_assert(kSilu == FCONV_ACT_SILU && kGelu == FCONV_ACT_GELU && kGeluTanh ==
 
 // ------------------------------------------------------------- few tokens
 //
-// At most 64 tokens: the time is w's way out of memory, so fragments of both
+// Few tokens: the time is w's way out of memory, so fragments of both
 // operands go straight into registers, from any address, without LDS or
-// barriers.  A workgroup owns 16 f of both projections and up to 64 tokens (32
+// barriers.  A workgroup owns 16 f of both projections and 16 MT tokens (at most 32
 // with ODD, whose fragments take more registers); its NW waves take turns at
 // steps of 128 bytes of k, the next turn's loads in flight, and add their sums
 // in LDS, in order; wave j then finishes tokens 16 j .. + 15.  One token of 4096 x
 // 12288 bf16: 33 us, w at 6.1 TB/s.
+//
+// More tokens of a layer with few f and a long k have so few tiles that one's slabs,
+// one after another, are the time.  Here the waves share k, and tokens are spread
+// over workgroups until the device is full: 128 x 8192 x 512 bf16 24 us instead of
+// 80, fp32 47 instead of 197; 200 x 4000 x 300 13 and 43, 32 and 98.
 struct GatedFew {
   const char* w;
   int64_t ldw;
@@ -287,7 +292,8 @@ struct fconv_gated_plan_s {
   int32_t es;
   int64_t ld_kept;  // F in whole eights: kept is fp32 [T, 2, ld_kept]
   size_t kept_bytes;
-  bool few;                       // at most kFewTokens, by their own kernel
+  bool few;                       // few tokens, by their own kernel
+  int32_t few_mt;                 // sixteens of them in a workgroup
   bool few_dx;                    // dx by few_rows, in one launch with dw
   bool pair;                      // both gradients in one launch of tiles
   bool pack_fwd, pack_dx;         // rows of bf16 copied to 16-byte boundaries: x and w; w
@@ -301,7 +307,7 @@ struct fconv_gated_plan_s {
 namespace fconv {
 namespace {
 
-constexpr int32_t kFewTokens = 64;
+constexpr int32_t kFewTokens = 64;  // that one workgroup can take
 // 2 F up to which few_rows takes dx: its time grows with the sum, partial sums cost a launch more (both gradients
 // of 32 x 512 x 500 bf16 8.2 instead of 10.9 us, x 1000 10.0 and 10.7, of 64 x 512 x 1000 13.4 and 11.1; fp32, whose
 // fragments are twice as large, 11.1 and 13.2, 16.4 and 14.3, 24.6 and 16.1).
@@ -320,6 +326,26 @@ double few_us(int64_t T, int64_t F, int64_t D, int es) {
   const double steps = each[k] * static_cast<double>(D);
   return 3.0 + (memory > steps ? memory : steps);
 }
+// Tokens of a workgroup of the few-token kernel, in sixteens, and its time.
+struct Few {
+  int32_t mt;
+  double us;
+};
+// All of them where that is at most 64, or fewer in several workgroups: those take as
+// long as a wave's steps for each 256 of them, and past 1024 tiles do better (fitted to T 65 .. 2000, D 200 .. 8192, F
+// 64 .. 12288; bf16 rows at odd places take half as long again).
+Few few_shape(int64_t T, int64_t F, int64_t D, int es) {
+  static const double each[][4] = {{0.0026, 0.0034, 0.0, 0.0051}, {0.0052, 0.0068, 0.0, 0.0143}};
+  const bool odd = es == 2 && D % 2;
+  Few best = {T <= 16 ? 1 : T <= 32 || odd ? 2 : 4, T <= kFewTokens ? few_us(T, F, D, es) : 1e300};
+  for (int32_t mt = 1; mt <= (odd ? 2 : 4); mt *= 2) {
+    const int64_t n = round_up(ceil_div(F, 16), 8) * ceil_div(T, 16 * mt);
+    const double steps = each[es == 4][mt - 1] * static_cast<double>(D) * (odd ? 1.5 : 1.0);
+    const double us = 2.0 + (1.0 + steps) * static_cast<double>(ceil_div(n, 256));
+    if (T > 16 * mt && n <= 1024 && us < best.us) best = Few{mt, us};
+  }
+  return best;
+}
 // The tiles' time for few tokens: choose() leaves w's way out of memory out (64 x 8192
 // x 16384: 132 us).
 double few_tiles_us(const Split& s, int64_t F, int64_t D, int es) {
@@ -328,8 +354,8 @@ double few_tiles_us(const Split& s, int64_t F, int64_t D, int es) {
 }
 
 // What 64 k take in the general kernel (us) of a workgroup alone on its CU and of one
-// among four.  Forward both operands' k are contiguous (69 x 2590 x 704: 0.55 alone),
-// backward a fragment is transposed.  Rows of bf16 that are not aligned take longer
+// among four.  Forward both operands' k are contiguous (69 x 2590 x 704: 0.55 alone, 65 x
+// 4096 x 4096: 0.45, fp32 1.5), backward a fragment is transposed.  Rows of bf16 that are not aligned take longer
 // where the CU is busy (384 x 3754 x 5440: 1.75); fp32 takes 64 k in two slabs (2048 x
 // 1024 x 2816: 4.6).
 struct Slab {
@@ -339,7 +365,7 @@ struct Slab {
   }
 };
 Slab slab_us(int64_t D, int es, bool forward) {
-  return es == 4 ? Slab{2.3, 4.6} : Slab{forward ? 0.6 : 0.85, D % 8 ? 1.9 : 1.15};
+  return es == 4 ? Slab{forward ? 1.55 : 2.3, 4.6} : Slab{!forward ? 0.85 : D % 8 ? 0.6 : 0.45, D % 8 ? 1.9 : 1.15};
 }
 // What r ranges of na x nb values cost beside their slabs: a launch that joins them, and their bytes (dx of 32 x
 // 1024 x 2816 in 15 ranges 15.2 us with dw, in 44 17.0).
@@ -408,16 +434,16 @@ Split pair(int64_t T, int64_t D, int64_t F2) {
 double copy_us(int64_t rows, int64_t cols) { return 4.0 + 4.0 * static_cast<double>(rows) * static_cast<double>(cols) / 6e6; }
 
 template <typename E, bool ODD>
-hipError_t launch_few_of(const GatedFew& f, hipStream_t s) {
-  const int64_t groups = round_up(ceil_div(f.F, 16), 8);
-  const dim3 grid(static_cast<unsigned>(ODD ? groups * ceil_div(f.T, 32) : groups));
+hipError_t launch_few_of(const GatedFew& f, int mt, hipStream_t s) {
+  if (ODD && mt > 2) mt = 2;
+  const dim3 grid(static_cast<unsigned>(round_up(ceil_div(f.F, 16), 8) * ceil_div(f.T, 16 * mt)));
   // Of a few tokens the waves' loads are nearly all of w, and more of them read a large one quicker
   // (one token, 4096 x 12288: eight 37.2 us, four 38.8; 8192 x 16384: 107 and 124; 16 tokens: 43.4 and 41.9).
   if (f.T <= 8 && static_cast<int64_t>(f.F) * f.D * 2 * static_cast<int64_t>(sizeof(E)) >= 128 << 20) {
     hipLaunchKernelGGL((gated_few_kernel<E, ODD, 1, 8>), grid, dim3(512), 0, s, f);
-  } else if (f.T <= 16) {
+  } else if (mt == 1) {
     hipLaunchKernelGGL((gated_few_kernel<E, ODD, 1, 4>), grid, dim3(256), 0, s, f);
-  } else if (ODD || f.T <= 32) {
+  } else if (mt == 2) {
     hipLaunchKernelGGL((gated_few_kernel<E, ODD, 2, 4>), grid, dim3(256), 0, s, f);
   } else {
     if constexpr (!ODD) hipLaunchKernelGGL((gated_few_kernel<E, ODD, 4, 4>), grid, dim3(256), 0, s, f);
@@ -436,9 +462,9 @@ hipError_t run_forward(const fconv_gated_plan_s* p, const fconv_gated_args* args
     const GatedFew f = {w.p, w.ld, x.p, x.ld, static_cast<char*>(args->y), args->ldy, static_cast<float*>(args->kept),
                         p->ld_kept, d.T, d.D, d.F, d.activation};
     if constexpr (sizeof(E) == 2) {
-      if (odd_rows(w) || odd_rows(x)) return launch_few_of<E, true>(f, s);
+      if (odd_rows(w) || odd_rows(x)) return launch_few_of<E, true>(f, p->few_mt, s);
     }
-    return launch_few_of<E, false>(f, s);
+    return launch_few_of<E, false>(f, p->few_mt, s);
   }
   int edge = p->fwd.edge;
   hipError_t e;
@@ -630,7 +656,10 @@ fconv_status fconv_gated_plan_create(const fconv_gated_desc* desc, fconv_gated_p
       p->pack_fwd = packed.edge != 64 && packed.us + copy_us(F2, D) + copy_us(T, D) < p->fwd.us;
       if (p->pack_fwd) p->fwd = packed;
     }
-    p->few = T <= kFewTokens && few_us(T, d.F, D, p->es) < few_tiles_us(p->fwd, d.F, D, p->es);
+    const Few few = few_shape(T, d.F, D, p->es);
+    p->few = few.us < (T <= kFewTokens ? few_tiles_us(p->fwd, d.F, D, p->es) : p->fwd.us);
+    p->few_mt = few.mt;
+    if (p->few) p->pack_fwd = false;
     p->fwd_x = take(p->pack_fwd ? static_cast<size_t>(T) * p->ld_pack * 2 : 0);
     p->fwd_w = take(p->pack_fwd ? static_cast<size_t>(F2) * p->ld_pack * 2 : 0);
     p->fwd_bytes = at;

@@ -133,3 +133,14 @@ def test_a_million_tokens():
     _within("dw", dw, want, steps * U * size)
     y = p.forward(dw, torch.where(live, token, 0))
     assert torch.equal(y, dw[torch.where(live, token, 0)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,D,F", [(65, 4096, 20), (128, 8192, 33), (300, 1024, 300), (271, 3689, 88), (1000, 515, 50),
+                                   (513, 1001, 16), (64, 2048, 17), (40, 3001, 100), (1999, 260, 40)])
+def test_long_rows_of_few_outputs(T, D, F, dtype):
+    # Workgroups share the tokens, by 16, 32 or 64 of them, past those that one can take.
+    dev = device()
+    say("gated, few outputs", T, D, F, dtype)
+    assert check(T, D, F, dev, dtype).kernel_name("forward") == "gated_few"
+    check(T, D, F, dev, dtype, x_off=1, w_off=3)  # rows between dwords: fewer tokens in a workgroup
