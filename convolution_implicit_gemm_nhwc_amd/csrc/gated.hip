@@ -74,9 +74,9 @@ __global__ __launch_bounds__(NW * 64, 2) void gated_few_kernel(GatedFew f) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   // Tokens from t0 on; workgroups of the same f and other tokens follow on the same XCD (every eighth).
-  const int halves = (f.T + 16 * MT - 1) / (16 * MT);
-  const int t0 = static_cast<int>(blockIdx.x / 8 % halves) * 16 * MT;
-  const int f0 = static_cast<int>(blockIdx.x / (8 * halves) * 8 + blockIdx.x % 8) * 16;
+  const int blocks = (f.T + 16 * MT - 1) / (16 * MT);
+  const int t0 = static_cast<int>(blockIdx.x / 8 % blocks) * 16 * MT;
+  const int f0 = static_cast<int>(blockIdx.x / (8 * blocks) * 8 + blockIdx.x % 8) * 16;
   if (f0 >= f.F) return;
   const int full = f.D / STEP;  // whole steps
 
