@@ -325,11 +325,21 @@ __device__ inline void epilogue(const GemmArgs& g, f32x4 (&acc)[NI][NJ], const P
       const int b = b_of(j);
       const int at = b < rb ? per.at[j] : -1;
       if (at >= 0) {
+        // One comparison after another: with the masks of all of them at once, what
+        // every tile runs through lacked scalar registers (1728 x 72 x 51605 59.6 us,
+        // 55.2 so; 4096 x 2048 x 50021 648 and 640).
+        float x = 0.0f;
+        int here = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (a_of(i) + e == at) g.target_logit[b0 + b] = acc[i][j][e];
+          for (int e = 0; e < 4; ++e) {
+            const bool is = a_of(i) + e == at;
+            x = is ? acc[i][j][e] : x;
+            here = is ? 1 : here;
+            asm volatile("" : "+v"(x), "+v"(here));
+          }
+        if (here) g.target_logit[b0 + b] = x;
       }
       float m = acc[0][j][0], s = 0.0f;
 #pragma unroll
