@@ -532,7 +532,8 @@ hipError_t run_backward(const fconv_gated_plan_s* p, const fconv_gated_args* arg
     if ((e = launch_pack(w.p, w.ld, F2, d.D, ws + p->o_w, p->ld_pack, s)) != hipSuccess) return e;
     w = {ws + p->o_w, p->ld_pack, p->ld_pack};
   }
-  if (dw && p->dw.edge != 64 && !fits_tiles(x.p, x.ld)) {
+  // A last row that is no whole pieces of 16 bytes would be read past its end.
+  if (dw && p->dw.edge != 64 && (d.D % 8 != 0 || !fits_tiles(x.p, x.ld))) {
     if ((e = launch_pack(x.p, x.ld, d.T, d.D, ws + p->o_x, p->ld_pack, s)) != hipSuccess) return e;
     x = {ws + p->o_x, p->ld_pack, p->ld_pack};
   }
