@@ -38,8 +38,8 @@ def _filled(t, what, numel, dtype):
 
 
 class ClipPlan:
-    """tensors: (numel, dtype) of each gradient, dtype "bf16" or "fp32"; eps is
-    added to the norm that max_norm is divided by."""
+    """tensors: (numel, dtype) of each gradient (one at least), dtype "bf16" or
+    "fp32"; eps is added to the norm that max_norm is divided by."""
 
     def __init__(self, tensors, eps=1e-6):
         sizes = [(_whole("numel", n, bits=64)[0], type_name(t)) for n, t in tensors]

@@ -11,7 +11,8 @@
 // order is unique).  Up to kSmall tokens every workgroup sorts them all itself,
 // in LDS, and the gradient is one launch.  Above:
 //   rank    chunks of up to kChunk tokens, sorted by counting for each key the
-//           smaller ones of its chunk: n^2 / 2 operations a token and no passes
+//           smaller ones of its chunk: as many comparisons a token as the chunk
+//           has tokens, and no passes
 //   merge   sixteen sorted runs at a time: a key's place is the sum of its ranks
 //           in them, found by binary searches
 //   sums    pieces of `piece` sorted keys: their rows of dy are summed; a token
@@ -719,8 +720,9 @@ fconv_status fconv_embed_plan_create(const fconv_embed_desc* desc, fconv_embed_p
   p->piece = 64;
   while (p->piece > 16 && ceil_div(ceil_div(T, p->piece), 256 / p->team) * p->col_blocks < 1024) p->piece /= 2;
   p->pieces = static_cast<int32_t>(ceil_div(T, p->piece));
-  // Up to 256 KB of zeros for a workgroup; less of a small table, for more workgroups, as long as these do not look
-  // through more than 32 MB of tokens.
+  // 256 KB of zeros for a workgroup, in four rows at least; less of a small table, for more workgroups, up to 512 and
+  // as long as those do not look through more than 32 MB of tokens for it.  What 256 KB each make of a large table has no
+  // such bound: the 2048 workgroups of 65536 x 4096 bf16 look through 268 MB for 16384 tokens, out of the caches.
   int64_t rows = (256 << 10) / (static_cast<int64_t>(d.D) * p->es), most = (4ll << 20) / (T > 0 ? T : 1);
   most = most > 512 ? 512 : most < 1 ? 1 : most;
   if (rows > ceil_div(d.V, most)) rows = ceil_div(d.V, most);

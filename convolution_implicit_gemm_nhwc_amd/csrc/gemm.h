@@ -798,8 +798,8 @@ __device__ inline void few_rows(const GemmArgs& g, f32x4* sums, int d0) {
 // reads, in phase 2 for A0 and B0 of the next slab and in phase 0 for this
 // one's others.
 //
-// Measured: 8192 x 4096 x 32768 logits 1.60 to 1.68 ms from box to box, 1.31 to
-// 1.38 PFLOP/s; the matrix cores are busy 71% of the cycles, at 1.8 GHz: power
+// Measured: 8192 x 4096 x 32768 logits 1.54 to 1.68 ms from box to box, 1.31 to
+// 1.43 PFLOP/s; the matrix cores are busy 71% of the cycles, at 1.8 GHz: power
 // bounds the clock.  Of its gradient's products the logits 66% (q is written), dh
 // 66%, dw 71%.
 //

@@ -21,6 +21,13 @@
  * rounded to bf16 before they are multiplied.  All roundings are to nearest
  * even.  Results do not depend on the order in which workgroups run.
  *
+ * With FCONV_BF16 and D a multiple of 8, tiles copy rows of x and w that lie on 16
+ * bytes (address and row stride).  With others forward, and with such a w dx, takes
+ * the general kernel, which takes two to six times as long where there are many
+ * tokens; dw copies x to such rows first.  Rows of bf16 that begin or end inside a
+ * dword may be read with the rest of it, also before the first element and behind the
+ * last one; nothing depends on that.
+ *
  * Conventions as in fconv.h: status codes only; every check happens before
  * anything is enqueued; the caller owns every buffer; plans are host objects
  * that runs never modify.

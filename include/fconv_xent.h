@@ -17,7 +17,9 @@
  * dtype is the type of h, w, dh and dw (FCONV_BF16 or FCONV_FP32); products
  * are summed in fp32 by the matrix cores, loss, lse and dloss are fp32.  With
  * FCONV_BF16, softmax - onehot and h scaled by dloss / max |dloss| are rounded
- * to bf16 (to nearest even) before they are multiplied.
+ * to bf16 (to nearest even) before they are multiplied.  Rows of bf16 that begin or
+ * end inside a dword may be read with the rest of it, also before the first element
+ * and behind the last one; nothing depends on that.
  * Results do not depend on the order in which workgroups run.
  *
  * Conventions as in fconv.h: status codes only; every check happens before
