@@ -540,7 +540,8 @@ struct Gen {
 // the matrix's last row (gradients of 960 x 256 x 119 18 us with zeros, 10 so).
 // GATED: 32 rows of each half of A, 16 of the first and the same of the second in turn,
 // so that a wave's two tiles are a gate's and what it multiplies.
-template <typename E, Order O, bool GATED>
+// FEW (kSum): a wave all of whose sixteen rows are past the last one leaves `v` as it is.
+template <typename E, Order O, bool GATED, bool FEW>
 __device__ inline void gen_load(const Operand& op, int64_t row0, int rows, int64_t k0, int64_t k1,
                                 E v[32 / sizeof(E)]) {
   constexpr int N = 32 / sizeof(E);
@@ -553,6 +554,7 @@ __device__ inline void gen_load(const Operand& op, int64_t row0, int rows, int64
     n = static_cast<int>(min(k1 - k, static_cast<int64_t>(N)));
     p = op.p + ((row0 + f + (r & 16 ? op.width : 0)) * op.ld + k) * static_cast<int64_t>(sizeof(E));
   } else if constexpr (O == kSum) {
+    if (FEW && __builtin_amdgcn_readfirstlane(tid >> 6) * 16 >= rows) return;
     const int r = min(tid >> 2, rows - 1);
     const int64_t k = k0 + (tid & 3) * N;
     n = static_cast<int>(min(k1 - k, static_cast<int64_t>(N)));
@@ -626,8 +628,8 @@ struct GenLds {
   float2 red[2 * 64];
 };
 
-// Tile (x, y) of range z.
-template <typename E, Order OA, Order OB, Epilogue EPI>
+// Tile (x, y) of range z.  FEW: waves load no b where there is none.
+template <typename E, Order OA, Order OB, Epilogue EPI, bool FEW = false>
 __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y, int z) {
   using G = Gen<E>;
   using Frag = std::conditional_t<sizeof(E) == 2, bf16x8, f32x8>;
@@ -651,10 +653,14 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
   // Two slabs are on their way in registers while one is multiplied: with one,
   // a workgroup alone on its CU waited for most of a slab's time.
   E va[2][32 / G::ES], vb[2][32 / G::ES];
+  if constexpr (FEW) {
+#pragma unroll
+    for (int i = 0; i < 32 / G::ES; ++i) vb[0][i] = vb[1][i] = static_cast<E>(0.0f);
+  }
   auto load = [&](int s, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     if (s >= slabs) return;
-    gen_load<E, OA, GATED>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, xa);
-    gen_load<E, OB, false>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, xb);
+    gen_load<E, OA, GATED, false>(g.a, a0, ra, k0 + s * static_cast<int64_t>(G::SLAB), k1, xa);
+    gen_load<E, OB, false, FEW>(g.b, b0, rb, k0 + s * static_cast<int64_t>(G::SLAB), k1, xb);
   };
   auto step = [&](int s, char* ba, char* bb, E(&xa)[32 / G::ES], E(&xb)[32 / G::ES]) __attribute__((always_inline)) {
     gen_write<E, OA>(ba, xa);
@@ -688,10 +694,10 @@ __device__ inline void gen_tile(const GemmArgs& g, GenLds<E>& lds, int x, int y,
       g, acc, per_b, a0, b0, ra, rb, x, z, wa, q, [&](int i) { return (wa * EA / 2) + 16 * i + 4 * q; }, b_of, lds.red);
 }
 
-template <typename E, Order OA, Order OB, Epilogue EPI>
+template <typename E, Order OA, Order OB, Epilogue EPI, bool FEW = false>
 __global__ __launch_bounds__(256) void gemm_gen_kernel(GemmArgs g) {
   __shared__ GenLds<E> lds;
-  gen_tile<E, OA, OB, EPI>(g, lds, blockIdx.x, blockIdx.y, blockIdx.z);
+  gen_tile<E, OA, OB, EPI, FEW>(g, lds, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // ------------------------------------------------- few rows, a short sum (kEpiOut, kEpiStore)
@@ -1362,6 +1368,15 @@ hipError_t launch_gemm(const GemmArgs& g, int edge, hipStream_t s) {
     if (edge != 64) return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(ta), static_cast<unsigned>(tb), static_cast<unsigned>(g.ranges));
+  if constexpr (OB == kSum && (EPI == kEpiLse || EPI == kEpiGrad)) {
+    // Some of the last tile's waves have no b: their loads of the last one again took as long as others (loss of 10 x
+    // 343 x 41728 16.1 us, 13.3 without them; 130 29.4 and 27.7, 1030 x 343 x 9000 31.0 and 31.1).  Where every wave
+    // has some, asking is for nothing (4096 x 1024 x 8192 fp32 557 us, 565 with it).
+    if ((g.nb - 1) % 64 < 48) {
+      hipLaunchKernelGGL((gemm_gen_kernel<E, OA, OB, EPI, true>), grid, dim3(256), 0, s, g);
+      return hipGetLastError();
+    }
+  }
   hipLaunchKernelGGL((gemm_gen_kernel<E, OA, OB, EPI == kEpiStream ? kEpiOut : EPI == kEpiStoreStream ? kEpiStore : EPI>), grid, dim3(256), 0, s, g);
   return hipGetLastError();
 }
